@@ -474,6 +474,102 @@ int dash_sched_check(int n_heads, int N, int causal, int num_ctas, const int* ro
 int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* dst,
                           const double* w, double* depth, double* height, double* cp);
 
+/* ---------------------------------------------------------------------------
+ * Block selection, block-sparse attention and 8-bit checkpoints.
+ *
+ * The pages have no counterpart to these calls; they serve the long sequences the
+ * backward is made for.  Conventions that differ from the calls above:
+ *   - q, o, dout, dq: [B, H, Sq, D]; k, v, dk, dv: [B, Hkv, Sk, D], bf16, D in {64, 128},
+ *     H any multiple of Hkv up to 128 query heads per K/V head.  Sq >= 0 and Sk >= 1 are
+ *     free (no multiple of 128).  Query head h reads K/V head h / (H / Hkv).
+ *   - Inputs may be strided: `strides` holds (batch, head, row) strides in elements for
+ *     each strided input in the order of the arguments, positive multiples of 8 (the last
+ *     dimension is contiguous; the stride of an extent of 1 is not looked at); NULL means
+ *     contiguous.  Outputs are contiguous.
+ *   - kv_len: device int [B], keys of batch entry b that exist (0 to Sk; NULL: Sk).  Keys and
+ *     means past it are never used, whatever they hold; keys before it must be finite.
+ *     q_start: device int [B], the position of query 0 (NULL: Sk - Sq, the queries are the
+ *     last Sq positions of Sk).  Query i sees keys j < limit_i = min(kv_len, q_start + i + 1)
+ *     with causal = 1, j < kv_len with causal = 0.
+ *   - block: keys per block, a positive multiple of 64.  Block numbers run from 0 to
+ *     ceil(Sk / block) - 1.
+ *   - Nothing is allocated and no answer is kept: plans and workspaces are the caller's,
+ *     16-byte aligned, of the sizes the *_bytes calls give (a negative value is a negated
+ *     status), and a workspace is free again when the call's work on `stream` is done.  All
+ *     calls may be captured into a graph.  Results are bitwise reproducible.
+ *   - A timeout found on the device is reported by dash_attn_sync_status(stream); calls on
+ *     the stream between the timeout and that report may be invalid too.
+ */
+
+/*
+ * Means of key blocks: means fp32 [B, Hkv, nb, D], nb = ceil(Sk / block); a block without keys
+ * below kv_len gets zeros.  Each sum is taken in fp64 and rounded once.
+ * start (device int [B] or NULL): only the blocks from start[b] / block to the last that has
+ * keys are written, the others stay as they are: the update after positions start[b] to
+ * kv_len[b] - 1 were appended to a cache.
+ */
+int dash_block_means(const void* k, const long long* strides, float* means, const int* kv_len,
+                     const int* start, int B, int Hkv, int Sk, int D, int block, void* stream);
+
+/*
+ * The blocks that each query attends to: idx int [B, Hkv, Sq, topk], ascending, filled up with
+ * -1.  The score of block j for query i is the sum over the K/V head's query heads of
+ * q[b,h,i] . means[b,hk,j].  Of the visible blocks (first key below limit_i) the first `sink`
+ * and the last `local` are always picked (sink + local <= topk), then the highest scores;
+ * equal scores go to the lowest block, a NaN score ranks last.  Scores are compared as the
+ * fp64 sums of the exact products.  At most 4096 blocks.
+ */
+int dash_block_select(const void* q, const long long* strides, const float* means, int* idx,
+                      const int* kv_len, const int* q_start, int B, int H, int Hkv, int Sq, int Sk,
+                      int D, int block, int topk, int causal, int sink, int local, void* stream);
+
+/*
+ * The plan of a selection, which the forward and the backward read: for each tile of queries
+ * the 64-key units that any of them picked and sees.  idx: int [B, Hkv, Sq, topk] block
+ * numbers in any order; numbers outside 0 .. nb - 1 are unused places, a block named twice
+ * counts once.  kv_len and q_start are taken into the plan.
+ */
+long long dash_sparse_plan_bytes(int B, int H, int Hkv, int Sq, int Sk, int block, int topk);
+int dash_sparse_plan(const int* idx, const int* kv_len, const int* q_start, void* plan, int B,
+                     int H, int Hkv, int Sq, int Sk, int block, int topk, int causal, void* stream);
+
+/*
+ * Block-sparse forward: o and lse (fp32 [B, H, Sq], natural log) of softmax attention over the
+ * picked blocks' visible keys.  A query without any gets o = 0 and lse = -inf.  strides: q, k, v.
+ * scale: 0 for 1 / sqrt(D).  The shape arguments are those the plan was made with.
+ * work: dash_attn_sparse_work_bytes(..., backward = 0) bytes (may be 0).
+ */
+long long dash_attn_sparse_work_bytes(int B, int H, int Hkv, int Sq, int Sk, int D, int block,
+                                      int topk, int backward);
+int dash_attn_sparse_fwd(const void* q, const void* k, const void* v, const long long* strides,
+                         const void* plan, void* o, float* lse, void* work, int B, int H, int Hkv,
+                         int Sq, int Sk, int D, int block, int topk, int causal, float scale,
+                         void* stream);
+
+/*
+ * Block-sparse backward: dq, dk, dv (fully overwritten; zeros where nothing was attended to)
+ * from the forward's o (contiguous) and lse.  strides: q, k, v, dout.
+ * work: dash_attn_sparse_work_bytes(..., backward = 1) bytes.
+ */
+int dash_attn_sparse_bwd(const void* q, const void* k, const void* v, const void* dout,
+                         const long long* strides, const void* plan, const void* o,
+                         const float* lse, void* dq, void* dk, void* dv, void* work, int B, int H,
+                         int Hkv, int Sq, int Sk, int D, int block, int topk, int causal,
+                         float scale, void* stream);
+
+/*
+ * 8-bit checkpoints of up to four bf16 tensors in one launch (host arrays of n device
+ * pointers and element counts, multiples of 32).  Groups of 32 consecutive elements share an
+ * exponent: e = max(floor(log2 max|x|) - 6, -126) and m = x / 2^e rounded half to even and
+ * clamped to +-127, each in a signed byte (m: one an element, e: one a group).  The value
+ * m 2^e is exact in bf16.  A group that holds an infinity or a NaN has e = -128 and reads back
+ * as NaN.  x and m are 16-byte aligned.
+ */
+int dash_ckpt8_pack(const void* const* x, void* const* m, signed char* const* e,
+                    const long long* elems, int n, void* stream);
+int dash_ckpt8_unpack(const void* const* m, signed char* const* e, void* const* x,
+                      const long long* elems, int n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,7 +30,10 @@ EXPORTS = ("dash_attn_fwd", "dash_attn_bwd", "dash_attn_sync_status", "dash_stat
            "dash_attn_bwd_gqa_split", "dash_bwd_gqa_split_for", "dash_set_dq_chain_mode",
            "dash_dq_chain_uses_red", "dash_set_head_interleave",
            "dash_bwd_head_interleave", "dash_set_slot_placement",
-           "dash_slot_placement_by_smid", "dash_sched_table_pairs")
+           "dash_slot_placement_by_smid", "dash_sched_table_pairs",
+           "dash_block_means", "dash_block_select", "dash_sparse_plan_bytes",
+           "dash_sparse_plan", "dash_attn_sparse_work_bytes", "dash_attn_sparse_fwd",
+           "dash_attn_sparse_bwd", "dash_ckpt8_pack", "dash_ckpt8_unpack")
 
 
 class DashError(RuntimeError):
@@ -94,12 +97,25 @@ def load(path: str | None = None):
     lib.dash_sched_check.argtypes = [i, i, i, i, vp, ll]
     lib.dash_dag_longest_path.argtypes = [i, i, vp, vp, vp, vp, vp, P(d)]
     lib.dash_trace_bwd.argtypes = [vp] * 9 + [i, i, i, i, i, i, vp, vp, ll, P(i), P(i)]
+    f = ctypes.c_float
+    lib.dash_block_means.argtypes = [vp] * 5 + [i] * 5 + [vp]
+    lib.dash_block_select.argtypes = [vp] * 6 + [i] * 11 + [vp]
+    lib.dash_sparse_plan_bytes.argtypes = [i] * 7
+    lib.dash_sparse_plan.argtypes = [vp] * 4 + [i] * 8 + [vp]
+    lib.dash_attn_sparse_work_bytes.argtypes = [i] * 9
+    lib.dash_attn_sparse_fwd.argtypes = [vp] * 8 + [i] * 9 + [f, vp]
+    lib.dash_attn_sparse_bwd.argtypes = [vp] * 12 + [i] * 9 + [f, vp]
+    lib.dash_ckpt8_pack.argtypes = [vp, vp, vp, vp, i, vp]
+    lib.dash_ckpt8_unpack.argtypes = [vp, vp, vp, vp, i, vp]
+    for name in ("dash_sparse_plan_bytes", "dash_attn_sparse_work_bytes"):
+        getattr(lib, name).restype = ll
     lib.dash_profile_begin.argtypes = []
     lib.dash_profile_end.argtypes = [P(d), P(d), P(ll)]
     for name in EXPORTS:
         if name not in ("dash_status_string", "dash_sched_table", "dash_sched_table_part",
                         "dash_sched_table_gqa", "dash_attn_noalloc_sync_status",
-                        "dash_sched_table_pairs"):
+                        "dash_sched_table_pairs", "dash_sparse_plan_bytes",
+                        "dash_attn_sparse_work_bytes"):
             getattr(lib, name).restype = ctypes.c_int
     if path == LIB_PATH:
         _lib = lib
@@ -504,3 +520,313 @@ def dash_trace_bwd(q, k, v, o, do, lse, causal: bool, schedule="shift", stream=N
     if n > cap:
         raise RuntimeError("trace buffer too small")
     return dq, dk, dv, buf[:n].reshape(nc.value, rows.value, EV)
+
+
+# ---------------------------------------------------------------- block-sparse attention
+# These calls run on the tensors' device, on `stream` or that device's current stream, and
+# allocate what they return (and their scratch) on that stream.
+
+class _Launch:
+    """The device and stream of one call: tensors made inside belong to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._ctx = None
+        if stream is not None:
+            self._ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self._ctx = torch.cuda.device(device)
+        self._given, self._device = stream, device
+
+    def __enter__(self):
+        import torch
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        st = self._given if self._given is not None else torch.cuda.current_stream(self._device)
+        return st.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _expect(name, t, shape, dtype, device=None, contiguous=True):
+    """Reject what the C entry point would misread: shape, dtype, device, layout."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device else ""))
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return
+    shape, strides = t.shape, t.stride()
+    if t.numel() and strides[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.numel() and any(n > 1 and (st < 8 or st % 8) for n, st in zip(shape[:-1], strides[:-1])):
+        raise ValueError(f"{name} has strides {tuple(strides)}: positive multiples of 8 are "
+                         "needed (no broadcast dimensions)")
+    if t.numel() and t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _expect_rows(name, t, B, device):
+    """An optional int32 [B] tensor of the batch (kv_len, q_start, start)."""
+    import torch
+    if t is not None:
+        _expect(name, t, (B,), torch.int32, device)
+    return None if t is None else t.data_ptr()
+
+
+def _strides(*tensors):
+    flat = [st for t in tensors for st in t.stride()[:3]]
+    return (ctypes.c_longlong * len(flat))(*flat)
+
+
+def _block_count(Sk, block):
+    if block < 64 or block % 64:
+        raise ValueError(f"block must be a positive multiple of 64, not {block}")
+    return -(-Sk // block)
+
+
+def dash_block_means(k, block, kv_len=None, start=None, out=None, stream=None):
+    """fp32 means [B,Hkv,nb,D] of the key blocks of k [B,Hkv,Sk,D] (zeros for a block that
+    has no keys below kv_len).  With `start` (int32 [B]) only the blocks from start[b] //
+    block to the last one with keys are written into `out`, the others stay as they are."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("k must be [B,Hkv,Sk,D]")
+    B, Hkv, Sk, D = k.shape
+    _expect("k", k, k.shape, torch.bfloat16, contiguous=False)
+    nb = _block_count(Sk, block)
+    if start is not None and out is None:
+        raise ValueError("start updates means in place: give them as out")
+    n, s = _expect_rows("kv_len", kv_len, B, k.device), _expect_rows("start", start, B, k.device)
+    if out is not None:
+        _expect("out", out, (B, Hkv, nb, D), torch.float32, k.device)
+    with _Launch(k.device, stream) as st:
+        if out is None:
+            out = torch.empty((B, Hkv, nb, D), dtype=torch.float32, device=k.device)
+        _check(load().dash_block_means(k.data_ptr(), _strides(k), out.data_ptr(), n, s, B, Hkv, Sk,
+                                       D, block, st), "dash_block_means")
+    return out
+
+
+def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1, kv_len=None,
+                      q_start=None, out=None, stream=None):
+    """The blocks each query attends to, int32 [B,Hkv,Sq,topk], ascending, then -1.  q
+    [B,H,Sq,D]; means [B,Hkv,nb,D] of seq_k keys in blocks of `block`.  The first `sink` and
+    the last `local` visible blocks are always among them."""
+    import torch
+    if q.dim() != 4 or means.dim() != 4:
+        raise ValueError("q must be [B,H,Sq,D] and means [B,Hkv,nb,D]")
+    B, H, Sq, D = q.shape
+    Hkv = means.shape[1]
+    _expect("q", q, q.shape, torch.bfloat16, contiguous=False)
+    _expect("means", means, (B, Hkv, _block_count(seq_k, block), D), torch.float32, q.device)
+    n, s = _expect_rows("kv_len", kv_len, B, q.device), _expect_rows("q_start", q_start, B, q.device)
+    if out is not None:
+        _expect("out", out, (B, Hkv, Sq, topk), torch.int32, q.device)
+    with _Launch(q.device, stream) as st:
+        if out is None:
+            out = torch.empty((B, Hkv, Sq, max(int(topk), 0)), dtype=torch.int32, device=q.device)
+        _check(load().dash_block_select(q.data_ptr(), _strides(q), means.data_ptr(), out.data_ptr(),
+                                        n, s, B, H, Hkv, Sq, seq_k, D, block, topk,
+                                        int(bool(causal)), sink, local, st), "dash_block_select")
+    return out
+
+
+class SparsePlan:
+    """A selection prepared by dash_sparse_plan for the forward and the backward."""
+    __slots__ = ("buf", "shape", "causal")
+
+    def __init__(self, buf, shape, causal):
+        self.buf, self.shape, self.causal = buf, shape, causal  # shape: B,H,Hkv,Sq,Sk,block,topk
+
+
+def _bytes(n, what):
+    if n < 0:
+        raise DashError(int(-n), what)
+    return int(n)
+
+
+def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start=None, stream=None):
+    """The plan of a selection idx (int32 [B,Hkv,Sq,topk]) for `heads` query heads and seq_k
+    keys.  idx, kv_len and q_start are read by the call, not kept."""
+    import torch
+    if idx.dim() != 4:
+        raise ValueError("idx must be [B,Hkv,Sq,topk]")
+    B, Hkv, Sq, topk = idx.shape
+    _expect("idx", idx, idx.shape, torch.int32)
+    n = _expect_rows("kv_len", kv_len, B, idx.device)
+    s = _expect_rows("q_start", q_start, B, idx.device)
+    shape = (B, int(heads), Hkv, Sq, int(seq_k), int(block), topk)
+    lib = load()
+    size = _bytes(lib.dash_sparse_plan_bytes(*shape), "dash_sparse_plan")
+    with _Launch(idx.device, stream) as st:
+        buf = torch.empty(max(size, 16), dtype=torch.uint8, device=idx.device)
+        _check(lib.dash_sparse_plan(idx.data_ptr(), n, s, buf.data_ptr(), *shape, int(bool(causal)),
+                                    st), "dash_sparse_plan")
+    return SparsePlan(buf, shape, bool(causal))
+
+
+def _expect_qkv(q, k, v):
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,H,Sq,D] and k [B,Hkv,Sk,D]")
+    B, H, Sq, D = q.shape
+    _expect("q", q, q.shape, torch.bfloat16, contiguous=False)
+    _expect("k", k, (B, k.shape[1], k.shape[2], D), torch.bfloat16, q.device, contiguous=False)
+    _expect("v", v, k.shape, torch.bfloat16, q.device, contiguous=False)
+    return B, H, k.shape[1], Sq, k.shape[2], D
+
+
+def _expect_plan(plan, shape, device):
+    if plan.shape[:5] != shape:
+        raise ValueError(f"the plan is for B, H, Hkv, Sq, Sk = {plan.shape[:5]}, not {shape}")
+    if plan.buf.device != device:
+        raise ValueError(f"the plan must be on {device}")
+
+
+def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=None, scale=None,
+                         plan=None, out=None, lse=None, stream=None):
+    """O, LSE of attention over the selected blocks: q [B,H,Sq,D], k and v [B,Hkv,Sk,D] (any
+    strides with a contiguous last dimension), idx int32 [B,Hkv,Sq,topk].  A query that sees
+    nothing gets O = 0 and LSE = -inf.  Give the `plan` of idx where the backward follows;
+    idx, block, causal, kv_len and q_start are then those it was made with."""
+    import torch
+    B, H, Hkv, Sq, Sk, D = _expect_qkv(q, k, v)
+    if out is not None:
+        _expect("out", out, (B, H, Sq, D), torch.bfloat16, q.device)
+    if lse is not None:
+        _expect("lse", lse, (B, H, Sq), torch.float32, q.device)
+    if plan is None:
+        _expect("idx", idx, (B, Hkv, Sq, idx.shape[-1]), torch.int32, q.device)
+        plan = dash_sparse_plan(idx, H, Sk, block, causal, kv_len, q_start, stream)
+    _expect_plan(plan, (B, H, Hkv, Sq, Sk), q.device)
+    lib = load()
+    size = _bytes(lib.dash_attn_sparse_work_bytes(*plan.shape[:5], D, *plan.shape[5:], 0),
+                  "dash_attn_sparse_fwd")
+    with _Launch(q.device, stream) as st:
+        if out is None:
+            out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        _check(lib.dash_attn_sparse_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                        _strides(q, k, v), plan.buf.data_ptr(), out.data_ptr(),
+                                        lse.data_ptr(), work.data_ptr() if size else None,
+                                        *plan.shape[:5], D, *plan.shape[5:], int(plan.causal),
+                                        float(scale or 0.0), st), "dash_attn_sparse_fwd")
+    return out, lse
+
+
+def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None, dv=None,
+                         stream=None):
+    """dQ [B,H,Sq,D], dK and dV [B,Hkv,Sk,D] of dash_attn_sparse_fwd with the same plan, from
+    its O and LSE; bitwise reproducible."""
+    import torch
+    B, H, Hkv, Sq, Sk, D = _expect_qkv(q, k, v)
+    _expect("o", o, q.shape, torch.bfloat16, q.device)
+    _expect("do", do, q.shape, torch.bfloat16, q.device, contiguous=False)
+    _expect("lse", lse, (B, H, Sq), torch.float32, q.device)
+    for name, t, shape in (("dq", dq, q.shape), ("dk", dk, k.shape), ("dv", dv, k.shape)):
+        if t is not None:
+            _expect(name, t, shape, torch.bfloat16, q.device)
+    _expect_plan(plan, (B, H, Hkv, Sq, Sk), q.device)
+    lib = load()
+    size = _bytes(lib.dash_attn_sparse_work_bytes(*plan.shape[:5], D, *plan.shape[5:], 1),
+                  "dash_attn_sparse_bwd")
+    with _Launch(q.device, stream) as st:
+        def like(t, shape):
+            return torch.empty(shape, dtype=q.dtype, device=q.device) if t is None else t
+        dq, dk, dv = like(dq, q.shape), like(dk, k.shape), like(dv, k.shape)
+        work = torch.empty(max(size, 16), dtype=torch.uint8, device=q.device)
+        _check(lib.dash_attn_sparse_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
+                                        _strides(q, k, v, do), plan.buf.data_ptr(), o.data_ptr(),
+                                        lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                        dv.data_ptr(), work.data_ptr(), *plan.shape[:5], D,
+                                        *plan.shape[5:], int(plan.causal), float(scale or 0.0), st),
+               "dash_attn_sparse_bwd")
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------- 8-bit checkpoints
+def dash_ckpt8_pack(*tensors, stream=None):
+    """8-bit checkpoints of bf16 tensors (contiguous, last dimension a multiple of 32): for
+    each a pair (m, e), int8 of the tensor's shape and int8 [..., D // 32]."""
+    import torch
+    if not tensors:
+        return []
+    device = tensors[0].device
+    for j, x in enumerate(tensors):
+        _expect(f"tensor {j}", x, x.shape, torch.bfloat16, device)
+        if x.dim() < 1 or x.shape[-1] % 32 or x.data_ptr() % 16:
+            raise ValueError(f"tensor {j}: the last dimension must be a multiple of 32, 16-byte "
+                             "aligned")
+    pairs = []
+    with _Launch(device, stream) as st:
+        for x in tensors:
+            pairs.append((torch.empty(x.shape, dtype=torch.int8, device=device),
+                          torch.empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.int8,
+                                      device=device)))
+        for a in range(0, len(tensors), 4):
+            part = pairs[a:a + 4]
+            n = len(part)
+            vp = ctypes.c_void_p * n
+            _check(load().dash_ckpt8_pack(vp(*[x.data_ptr() for x in tensors[a:a + 4]]),
+                                          vp(*[m.data_ptr() for m, _ in part]),
+                                          vp(*[e.data_ptr() for _, e in part]),
+                                          (ctypes.c_longlong * n)(*[m.numel() for m, _ in part]),
+                                          n, st), "dash_ckpt8_pack")
+    return pairs
+
+
+def dash_ckpt8_unpack(*pairs, stream=None):
+    """The bf16 tensors that checkpoints (m, e) stand for, exactly."""
+    import torch
+    if not pairs:
+        return []
+    device = pairs[0][0].device
+    for j, (m, e) in enumerate(pairs):
+        _expect(f"m of checkpoint {j}", m, m.shape, torch.int8, device)
+        if m.dim() < 1 or m.shape[-1] % 32 or m.data_ptr() % 16:
+            raise ValueError(f"checkpoint {j}: the last dimension must be a multiple of 32, "
+                             "16-byte aligned")
+        _expect(f"e of checkpoint {j}", e, (*m.shape[:-1], m.shape[-1] // 32), torch.int8, device)
+    out = []
+    with _Launch(device, stream) as st:
+        out = [torch.empty(m.shape, dtype=torch.bfloat16, device=device) for m, _ in pairs]
+        for a in range(0, len(pairs), 4):
+            part = pairs[a:a + 4]
+            n = len(part)
+            vp = ctypes.c_void_p * n
+            _check(load().dash_ckpt8_unpack(vp(*[m.data_ptr() for m, _ in part]),
+                                            vp(*[e.data_ptr() for _, e in part]),
+                                            vp(*[x.data_ptr() for x in out[a:a + 4]]),
+                                            (ctypes.c_longlong * n)(*[m.numel() for m, _ in part]),
+                                            n, st), "dash_ckpt8_unpack")
+    return out
+
+
+def dash_attn_bwd_ckpt8(q8, k8, v8, o8, do, lse, causal: bool, schedule="shift", dq=None, dk=None,
+                        dv=None, stream=None):
+    """dash_attn_bwd (grouped-query where K/V have fewer heads) from the 8-bit checkpoints
+    (m, e) of Q, K, V and O: the result is bitwise that of the backward on the values the
+    checkpoints stand for."""
+    import torch
+    import contextlib
+    ctx = torch.cuda.device(do.device) if stream is None else torch.cuda.stream(stream)
+    with ctx if do.is_cuda else contextlib.nullcontext():
+        q, k, v, o = dash_ckpt8_unpack(q8, k8, v8, o8, stream=stream)
+        bwd = dash_attn_bwd if q.shape[1] == k.shape[1] else dash_attn_bwd_gqa
+        return bwd(q, k, v, o, do, lse, causal, schedule, dq, dk, dv, stream)
+
+
+def dash_attn_sparse_bwd_ckpt8(q8, k8, v8, o8, do, lse, plan, scale=None, dq=None, dk=None,
+                               dv=None, stream=None):
+    """dash_attn_sparse_bwd from the 8-bit checkpoints of Q, K, V and O."""
+    q, k, v, o = dash_ckpt8_unpack(q8, k8, v8, o8, stream=stream)
+    return dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale, dq, dk, dv, stream)

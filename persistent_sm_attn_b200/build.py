@@ -11,15 +11,16 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdash_attn.so")
-SOURCES = ["dash_api.cu", "noalloc.cu", "sched.cpp"]
+SOURCES = ["dash_api.cu", "noalloc.cu", "sparse_api.cu", "sched.cpp"]
 DEPS = SOURCES + ["sched.h", "internal.h", "ptx.cuh", "bwd_kernel.cuh", "fwd_kernel.cuh",
-                  "aux_kernels.cuh"]
+                  "aux_kernels.cuh", "block_select.cuh", "ckpt8.cuh", "sparse_plan.cuh",
+                  "sparse_fwd.cuh", "sparse_bwd.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dash_attn.h")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-Xcompiler", "-fPIC,-O2", "-shared",
+    "-Xcompiler", "-fPIC,-O2", "-shared", "--threads", "4",
 ]
 
 

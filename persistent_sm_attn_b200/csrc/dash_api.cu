@@ -1158,22 +1158,23 @@ int dash_attn_sync_status(void* stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return DASH_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
+  const int sparse = dash::sparse_take_status(dev, stream);
   unsigned* err = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto itw = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-    if (itw == g_ws.end()) return DASH_OK;
+    if (itw == g_ws.end()) return sparse;
     err = itw->second.err;
   }
   unsigned h = 0;
-  if (!err) return DASH_OK;
+  if (!err) return sparse;
   if (cudaMemcpy(&h, err, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess)
     return DASH_ERR_CUDA;
   if (h) {
     if (cudaMemset(err, 0, sizeof(unsigned)) != cudaSuccess) return DASH_ERR_CUDA;
     return (h & dash::dev::ERR_TIMEOUT) ? DASH_ERR_TIMEOUT : DASH_ERR_UNSUPPORTED;
   }
-  return DASH_OK;
+  return sparse;
 }
 
 int dash_bwd_num_ctas(int device, int D, int* num_ctas) {

@@ -15,6 +15,10 @@ int take_armed_fault();
 // The mode set with dash_set_head_interleave (0: the library's choice).
 int head_interleave_mode();
 
+// Status recorded by the block-sparse kernels' bounded waits on (device, stream), cleared by
+// this call; the stream has been waited for.
+int sparse_take_status(int dev, void* stream);
+
 // C++ exceptions (std::bad_alloc from a table, a map or a vector sized by the
 // caller's arguments) must not cross the C ABI: each entry point that
 // allocates on the host returns a status instead.

@@ -1,0 +1,123 @@
+"""Block means and block selection on the GPU against the definition, block by block and query by
+query: the picks have to be equal."""
+import pytest
+import torch
+
+from persistent_sm_attn_b200 import binding as dash
+from tests import sparse_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def normal(gen, *shape):
+    return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+
+def inputs(B, H, Hkv, Sq, Sk, D, ragged, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    q, k = normal(gen, B, H, Sq, D), normal(gen, B, Hkv, Sk, D)
+    n = s = None
+    if ragged:
+        n = torch.randint(0, Sk + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+        s = torch.randint(-2, max(1, Sk - Sq) + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    return q, k, n, s
+
+
+@pytest.mark.parametrize("B,Hkv,Sk,D,block,ragged", [
+    (1, 1, 1, 64, 64, False), (2, 3, 65, 128, 64, True), (1, 2, 1000, 64, 128, False),
+    (3, 1, 777, 128, 256, True), (2, 2, 640, 128, 320, True)])
+def test_means(B, Hkv, Sk, D, block, ragged):
+    _, k, n, _ = inputs(B, Hkv, Hkv, 1, Sk, D, ragged, 1)
+    got = dash.dash_block_means(k, block, n)
+    want = R.means(k, block, n)
+    # the sum is exact, the quotient rounds twice (fp64, fp32): half a step of fp32 and a little
+    assert (got.double() - want).abs().le(want.abs() * 2.0 ** -23.9).all()
+
+
+def test_means_update_leaves_the_other_blocks():
+    _, k, _, _ = inputs(3, 2, 2, 1, 500, 64, False, 2)
+    n = torch.tensor([500, 130, 64], device="cuda", dtype=torch.int32)
+    start = torch.tensor([300, 129, 64], device="cuda", dtype=torch.int32)
+    means = torch.full((3, 2, 8, 64), 7.0, device="cuda")
+    out = dash.dash_block_means(k, 64, n, start, out=means)
+    assert out is means
+    want = dash.dash_block_means(k, 64, n)
+    touched = {0: range(4, 8), 1: range(2, 3), 2: range(0)}
+    for b in range(3):
+        for j in range(8):
+            same = means[b, :, j] == (want[b, :, j] if j in touched[b] else 7.0)
+            assert same.all(), (b, j)
+
+
+def test_means_ignore_what_lies_past_the_sequence_and_take_strides():
+    _, k, _, _ = inputs(2, 3, 3, 1, 200, 64, False, 3)
+    n = torch.tensor([70, 199], device="cuda", dtype=torch.int32)
+    bad = k.clone()
+    bad[0, :, 70:] = float("nan")
+    bad[1, :, 199:] = float("inf")
+    view = bad.transpose(1, 2).contiguous().transpose(1, 2)  # [B,S,H,D] in memory
+    assert not view.is_contiguous()
+    assert torch.equal(dash.dash_block_means(view, 64, n), dash.dash_block_means(k, 64, n))
+
+
+SHAPES = [
+    # B, H, Hkv, Sq, Sk, D, block, topk, causal, sink, local, ragged
+    (1, 1, 1, 1, 1, 64, 64, 1, True, 1, 0, False),
+    (1, 4, 2, 130, 130, 64, 64, 2, True, 1, 1, False),
+    (2, 4, 4, 77, 1500, 128, 64, 5, True, 1, 2, True),
+    (2, 6, 2, 33, 3000, 128, 64, 16, True, 0, 0, True),
+    (1, 8, 1, 40, 2500, 64, 128, 30, False, 2, 2, True),
+    (3, 7, 1, 1, 5000, 64, 64, 8, True, 1, 1, True),
+    (1, 2, 1, 3, 70000, 64, 64, 9, True, 1, 1, False),    # more than 1024 blocks
+    (1, 2, 1, 5, 100, 128, 256, 4, True, 1, 1, False),    # fewer blocks than places
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_select_matches_the_definition(shape):
+    B, H, Hkv, Sq, Sk, D, block, topk, causal, sink, local, ragged = shape
+    q, k, n, s = inputs(B, H, Hkv, Sq, Sk, D, ragged, sum(shape))
+    means = dash.dash_block_means(k, block, n)
+    got = dash.dash_block_select(q, means, Sk, block, topk, causal, sink, local, n, s)
+    want = R.select(q, means, Sk, block, topk, causal, sink, local, n, s)
+    assert torch.equal(got.cpu(), want)
+
+
+def test_equal_scores_go_to_the_lowest_block_and_near_ones_are_told_apart():
+    # all blocks alike but for one bit of one fp32 mean: the fp32 score would not show it
+    q = torch.ones(1, 2, 300, 64, device="cuda", dtype=torch.bfloat16)
+    means = torch.full((1, 1, 40, 64), 1.0, device="cuda")
+    got = dash.dash_block_select(q, means, 40 * 64, 64, 6, False, 1, 1)
+    assert (got.cpu() == torch.tensor([0, 1, 2, 3, 4, 39], dtype=torch.int32)).all()
+    means[0, 0, 17, 5] = 1.0 + 2.0 ** -23
+    means[0, 0, 30, 9] = 1.0 - 2.0 ** -24
+    means[0, 0, 2, 9] = 1.0 - 2.0 ** -24
+    got = dash.dash_block_select(q, means, 40 * 64, 64, 6, False, 1, 1)
+    assert (got.cpu() == torch.tensor([0, 1, 3, 4, 17, 39], dtype=torch.int32)).all()
+
+
+def test_zeros_of_either_sign_tie_and_nan_ranks_last():
+    q = torch.ones(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    means = torch.zeros(1, 1, 6, 64, device="cuda")
+    means[0, 0, 0] = -0.0
+    means[0, 0, 1] = float("nan")
+    means[0, 0, 2] = float("-inf")
+    means[0, 0, 5] = float("inf")
+    pick = lambda n: dash.dash_block_select(q, means, 6 * 64, 64, n, False, 0, 0).flatten().tolist()
+    assert pick(1) == [5] and pick(2) == [0, 5] and pick(4) == [0, 3, 4, 5]
+    assert pick(5) == [0, 2, 3, 4, 5] and pick(6) == [0, 1, 2, 3, 4, 5]
+
+
+def test_select_takes_strided_queries():
+    q, k, _, _ = inputs(2, 4, 2, 50, 900, 64, False, 5)
+    means = dash.dash_block_means(k, 64)
+    view = q.transpose(1, 2).contiguous().transpose(1, 2)
+    assert not view.is_contiguous()
+    assert torch.equal(dash.dash_block_select(view, means, 900, 64, 4),
+                       dash.dash_block_select(q, means, 900, 64, 4))
