@@ -6,12 +6,14 @@
 // A query sees the blocks whose first key lies below its limit, min(kv_len, position + 1
 // if causal).  The first `sink` and the last `local` of them are always picked, the other
 // places go to the highest scores, equal scores to the lowest block.  Which blocks are
-// picked must not depend on the order of a sum, so sums and scores are held in fp64: a sum
-// of bf16 keys is then exact unless their exponents differ by over 40, and two scores
+// picked must not depend on the order of a sum, so the picks are those of fp64 scores: a sum
+// of bf16 keys is exact in fp64 unless their exponents differ by over 40, and two scores
 // closer than fp64 can tell apart do not occur but for equal blocks, which tie exactly.
+// Few queries: all scores in fp64 (dash_block_select_token_kernel).  Many: scores from
+// tensor-core products with a bound on their error, and fp64 for those the bound leaves
+// open (dash_block_select_kernel).
 #pragma once
-#include <cuda_bf16.h>
-#include <cstdint>
+#include "ptx.cuh"
 
 namespace dash {
 
@@ -78,77 +80,410 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 
-// One CTA per QT queries of a K/V head; a warp per query at a time.  Scores of the visible
-// blocks go to shared memory in fp64; the picks are then made one at a time by a warp-wide
-// maximum over (score, -block).
-template <int D, int QT>
-__global__ void __launch_bounds__(128) dash_block_select_kernel(const SelectParams p) {
-  extern __shared__ __align__(16) unsigned char select_smem[];
-  double* qs = reinterpret_cast<double*>(select_smem);             // [QT][D]
-  unsigned long long* keys = reinterpret_cast<unsigned long long*>(qs + QT * D);  // [QT][nb]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv;
-  const int i0 = blockIdx.x * QT;
+// Where query i of batch entry b stands: the number of blocks it sees.
+__device__ __forceinline__ int visible_blocks(const SelectParams& p, int b, int i) {
   const int len = p.kv_len ? min(max(p.kv_len[b], 0), p.Sk) : p.Sk;
-  const int pos0 = p.q_start ? p.q_start[b] : p.Sk - p.Sq;
-  for (int x = threadIdx.x; x < QT * D; x += 128) {
-    const int i = i0 + x / D;
-    double s = 0.0;
-    if (i < p.Sq)
-      for (int g = 0; g < p.G; ++g)
-        s += (double)__bfloat162float(
-            p.q[b * p.sb + (long long)(hk * p.G + g) * p.sh + (long long)i * p.ss + x % D]);
-    qs[x] = s;
-  }
-  __syncthreads();
-  for (int r = warp; r < QT; r += 4) {
-    const int i = i0 + r;
-    if (i >= p.Sq) break;
-    const long long pos = (long long)pos0 + i;
-    const long long limit = p.causal ? min((long long)len, pos + 1) : (long long)len;
-    const int nvis = limit <= 0 ? 0 : (int)((limit + p.block - 1) / p.block);
-    unsigned long long* key = keys + (size_t)r * p.nb;
-    for (int j = lane; j < nvis; j += 32) {
-      const float* m = p.means + ((long long)bh * p.nb + j) * D;
-      double s = 0.0;
-      for (int d = 0; d < D; ++d) s += qs[r * D + d] * (double)m[d];
-      key[j] = (j < p.sink || j >= nvis - p.local) ? ~0ull : order_key(s);
-    }
-    __syncwarp();
-    const int n = min(p.topk, nvis);
-    int* out = p.idx + ((long long)bh * p.Sq + i) * p.topk;
-    // n picks, marked by key 0 with their bit kept in the low end of the output order below
-    for (int pick = 0; pick < n; ++pick) {
-      unsigned long long best = 0;
-      int at = 0x7fffffff;
-      for (int j = lane; j < nvis; j += 32) {
-        const unsigned long long v = key[j];
-        if (v != 1ull && (v > best || at == 0x7fffffff)) {
-          best = v;
-          at = j;
+  const long long pos = (long long)(p.q_start ? p.q_start[b] : p.Sk - p.Sq) + i;
+  const long long limit = p.causal ? min((long long)len, pos + 1) : (long long)len;
+  return limit <= 0 ? 0 : (int)((limit + p.block - 1) / p.block);
+}
+
+// The fp64 score of mean row m, the warp together; the same order of sums for every row, so
+// equal rows tie.  qd: this lane's D/32 query sums.
+template <int D>
+__device__ __forceinline__ double exact_score(const double (&qd)[D / 32], const float* m, int lane) {
+  double s = 0.0;
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x) s += qd[x] * (double)m[32 * x + lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// Few queries (serving): a CTA per query reads the K/V head's means once, a warp per row
+// with 16 (D = 64: 8) bytes a lane, four rows in flight.  The r-th largest key is found by
+// halving the key range, usually in under 20 counts.  Bound by reading the means.
+template <int D>
+__global__ void __launch_bounds__(256) dash_block_select_token_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) unsigned char select_smem[];
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(select_smem);  // [nb]
+  constexpr int V = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv, i = blockIdx.x;
+  const int nvis = visible_blocks(p, b, i);
+  int* out = p.idx + ((long long)bh * p.Sq + i) * p.topk;
+  double qd[V] = {};
+  if (nvis > p.topk) {
+    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+    for (int g = 0; g < p.G; ++g)
+#pragma unroll
+      for (int x = 0; x < V; ++x)
+        qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + lane * V + x]);
+    const float* means = p.means + (long long)bh * p.nb * D + lane * V;
+    const int j1 = nvis - p.local;
+    for (int j0 = p.sink + warp * 4; j0 < j1; j0 += 32) {
+      float m[4][V];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float* src = means + (long long)min(j0 + r, j1 - 1) * D;
+        if constexpr (V == 4) {
+          const float4 w = *reinterpret_cast<const float4*>(src);
+          m[r][0] = w.x, m[r][1] = w.y, m[r][2] = w.z, m[r][3] = w.w;
+        } else {
+          const float2 w = *reinterpret_cast<const float2*>(src);
+          m[r][0] = w.x, m[r][1] = w.y;
         }
+      }
+      double s[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        s[r] = 0.0;
+#pragma unroll
+        for (int x = 0; x < V; ++x) s[r] += qd[x] * (double)m[r][x];
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long ob = __shfl_xor_sync(0xffffffffu, best, o);
-        const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-        if (oa != 0x7fffffff && (at == 0x7fffffff || ob > best || (ob == best && oa < at))) {
-          best = ob;
-          at = oa;
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+      if (lane < 4 && j0 + lane < j1)
+        keys[j0 + lane] = order_key(lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3]);
+    }
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  const int j0 = p.sink, j1 = nvis - p.local;  // the contested blocks, where nvis > topk
+  unsigned long long cut = 0;                  // taken: key > cut, and `ties` of key == cut
+  int ties = 0;
+  const int r = p.topk - p.sink - p.local;
+  if (nvis > p.topk && r > 0) {
+    // lo < the r-th largest key <= hi
+    unsigned long long lo = ~0ull, hi = 0;
+    for (int j = j0 + lane; j < j1; j += 32) lo = min(lo, keys[j]), hi = max(hi, keys[j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    bool found = false, bottom = lo == 0;  // a key 0 cannot be undercut: it stands for itself
+    if (!bottom) --lo;
+    while (!found && hi - lo > 1) {
+      const unsigned long long mid = lo + (hi - lo) / 2;
+      int c = 0;
+      for (int j = j0 + lane; j < j1; j += 32) c += keys[j] > mid;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c == r) cut = mid, found = true;
+      else if (c > r) lo = mid, bottom = false;
+      else hi = mid;
+    }
+    if (!found) {
+      cut = hi;
+      int c = 0, e = 0;
+      for (int j = j0 + lane; j < j1; j += 32) c += keys[j] > hi, e += keys[j] >= hi;
+      c = __reduce_add_sync(0xffffffffu, c);
+      e = __reduce_add_sync(0xffffffffu, e);
+      if (bottom && e < r) cut = 0, c = e;  // keys of 1 and more do not suffice
+      ties = r - c;
+    }
+  }
+  int done = 0;
+  for (int x0 = 0; x0 < nvis; x0 += 32) {
+    const int j = x0 + lane;
+    bool take = j < nvis, tie = false;
+    if (take && nvis > p.topk && j >= j0 && j < j1) {
+      take = r > 0 && keys[j] > cut;
+      tie = r > 0 && !take && keys[j] == cut;
+    }
+    const unsigned mt = __ballot_sync(0xffffffffu, tie);
+    if (tie) take = __popc(mt & ((1u << lane) - 1u)) < ties;
+    ties = max(0, ties - __popc(mt));
+    const unsigned m = __ballot_sync(0xffffffffu, take);
+    if (take) out[done + __popc(m & ((1u << lane) - 1u))] = j;
+    done += __popc(m);
+  }
+  for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo + rest with hi, lo in bf16: |rest| <= 2^-16 |x|
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = dev::pack_bf16x2(x, y);
+  lo = dev::pack_bf16x2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+template <int D, int QT>
+struct SelectCfg {
+  static constexpr int kThreads = 256;
+  static constexpr int kRows = QT < 16 ? 16 : QT;       // MMA rows
+  static constexpr int RG = kRows / 16, CG = 8 / RG;    // warps over queries, over blocks
+  static constexpr int NT = 8 / CG;                     // 8-block columns of a warp
+  static constexpr int kLd = D * 2 + 16;                // bytes of a staged row: no bank conflicts
+  static constexpr int kStage = 2 * 64 * kLd;           // 64 means, high and low parts
+  static int smem(int nb) { return kStage + QT * ((nb + 63) / 64 * 64 + 8) * 4; }
+};
+
+// Many queries: QT of one K/V head, all visible blocks, 64 at a time.
+//
+// Scores: q = q_h + q_l, m = m_h + m_l in bf16, score ~ q_h m_h + q_h m_l + q_l m_h, fp32
+// accumulators.  What is left out and rounded is at most 3 * 2^-16 sum|q||m|, the sums of
+// the heads and of 3 D products in fp32 at most (G + 3 D + 3) 2^-23 of the same; with
+// G <= 128, D <= 128 and sum|q||m| <= |q| |m| (Euclidean norms) the error is below
+//     eps = 2^-13 |q| max_j |m_j|.
+// Picks: a cut T with exactly r scores above it, by halving the range of the scores.  Where
+// the lowest score above T and the highest below are more than 2 eps apart, the picks are
+// those of the exact scores.  Otherwise the scores within 2 eps of the cut are computed in
+// fp64 and decided by those (about one query in ten on normal data).  An eps that is not
+// finite (an infinity or NaN among the operands) leaves everything to fp64.
+//
+// NL: 32-block words that a lane's share of a row has room for.
+template <int D, int QT, int NL>
+__global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectParams p) {
+  using C = SelectCfg<D, QT>;
+  extern __shared__ __align__(16) unsigned char select_smem[];
+  __shared__ float qnorm[C::kRows];
+  __shared__ int mnorm_bits;
+  constexpr int W = (NL + 31) / 32;
+  const int ld = (p.nb + 63) / 64 * 64 + 8;
+  float* sc = reinterpret_cast<float*>(select_smem + C::kStage);  // [QT][ld]
+  const uint32_t stage = dev::smem_u32(select_smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int i0 = blockIdx.x * QT;
+  const int rg = warp % C::RG, cg = warp / C::RG;
+  const int last = min(i0 + QT, p.Sq) - 1;
+  const int most = visible_blocks(p, b, last);  // of the CTA's queries (they see ever more)
+  if (tid == 0) mnorm_bits = 0;
+
+  // ---- the group's queries, summed, as MMA operands: row lane/4 (+8), columns 2*(lane%4) (+8)
+  uint32_t ah[D / 16][4], al[D / 16][4];
+  {
+    float n2[2] = {0.f, 0.f};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = rg * 16 + half * 8 + (lane >> 2);
+      const bool on = row < QT && i0 + row < p.Sq;
+      const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh +
+                               (long long)(on ? i0 + row : 0) * p.ss + (lane & 3) * 2;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        float x = 0.f, y = 0.f;
+        if (on)
+          for (int g = 0; g < p.G; ++g) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(q + (long long)g * p.sh + c * 8);
+            x += __uint_as_float(w << 16);
+            y += __uint_as_float(w & 0xffff0000u);
+          }
+        n2[half] += x * x + y * y;
+        split_bf16(x, y, ah[c >> 1][(c & 1) * 2 + half], al[c >> 1][(c & 1) * 2 + half]);
+      }
+      n2[half] += __shfl_xor_sync(0xffffffffu, n2[half], 1);
+      n2[half] += __shfl_xor_sync(0xffffffffu, n2[half], 2);
+      if ((lane & 3) == 0) qnorm[row] = sqrtf(n2[half]);  // every column group writes the same
+    }
+  }
+
+  // ---- scores
+  const float* means = p.means + (long long)bh * p.nb * D;
+  for (int j0 = 0; j0 < most; j0 += 64) {
+    __syncthreads();
+    {
+      const int row = tid >> 2, part = tid & 3;
+      float n2 = 0.f;
+      const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + row) * D) + part;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const float4 w = j0 + row < most ? src[4 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
+        n2 += w.x * w.x + w.y * w.y + w.z * w.z + w.w * w.w;
+        uint2 hi, lo;
+        split_bf16(w.x, w.y, hi.x, lo.x);
+        split_bf16(w.z, w.w, hi.y, lo.y);
+        unsigned char* at = select_smem + row * C::kLd + (4 * x + part) * 8;
+        *reinterpret_cast<uint2*>(at) = hi;
+        *reinterpret_cast<uint2*>(at + 64 * C::kLd) = lo;
+      }
+      n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
+      n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
+      // as bits, so that an infinity or NaN stays the largest
+      if (part == 0) atomicMax(&mnorm_bits, __float_as_int(n2) & 0x7fffffff);
+    }
+    __syncthreads();
+    float acc[C::NT][4] = {};
+    // matrices of one load: high k 0-7, high k 8-15, low k 0-7, low k 8-15
+    const uint32_t at = stage + (lane >> 4) * (64 * C::kLd) + ((lane >> 3) & 1) * 16 +
+                        (uint32_t)(cg * C::NT * 8 + (lane & 7)) * C::kLd;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) {
+        uint32_t m[4];
+        ldmatrix_x4(at + t * 8 * C::kLd + kk * 32, m);
+        mma_bf16(acc[t], ah[kk], m[0], m[1]);
+        mma_bf16(acc[t], ah[kk], m[2], m[3]);
+        mma_bf16(acc[t], al[kk], m[0], m[1]);
+      }
+#pragma unroll
+    for (int t = 0; t < C::NT; ++t)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int row = rg * 16 + half * 8 + (lane >> 2);
+        if (row < QT)
+          *reinterpret_cast<float2*>(sc + row * ld + j0 + (cg * C::NT + t) * 8 + (lane & 3) * 2) =
+              make_float2(acc[t][2 * half], acc[t][2 * half + 1]);
+      }
+  }
+  __syncthreads();
+
+  // ---- picks, a warp per query
+  const float mnorm = sqrtf(__int_as_float(mnorm_bits));
+  const int r = p.topk - p.sink - p.local;
+  for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += 8) {
+    const int i = i0 + rr;
+    const int nvis = visible_blocks(p, b, i);
+    float* row = sc + rr * ld;
+    uint32_t* key = reinterpret_cast<uint32_t*>(row);
+    const int j0 = p.sink, j1 = nvis - p.local;
+    const int nl = (nvis + 31) / 32;
+    uint32_t take[W], open[W];  // bit x: block 32 x + lane is taken; is to be decided in fp64
+#pragma unroll
+    for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
+    auto each = [&](auto&& f) {  // the contested blocks of this lane
+#pragma unroll (NL <= 16 ? NL : 4)
+      for (int x = 0; x < NL; ++x) {
+        if (x >= nl) break;
+        const int j = 32 * x + lane;
+        if (j >= j0 && j < j1) f(x, j);
+      }
+    };
+    const bool all = nvis <= p.topk;
+    if (!all && r > 0) {
+      const float eps2 = 2.f * (0x1p-13f * qnorm[rr] * mnorm + 1e-35f);
+      int need = r;
+      if (eps2 < 1e30f) {  // beyond, a partial sum might overflow
+        float lo = INFINITY, hi = -INFINITY;  // the r-th and the next largest lie in [lo, hi]
+        each([&](int, int j) { lo = fminf(lo, row[j]), hi = fmaxf(hi, row[j]); });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        float cut = 0.f;
+        bool found = false;
+        while (!found) {
+          const float mid = 0.5f * lo + 0.5f * hi;
+          if (!(mid > lo && mid < hi)) break;
+          int c = 0;
+          each([&](int, int j) { c += row[j] > mid; });
+          c = __reduce_add_sync(0xffffffffu, c);
+          if (c == r) cut = mid, found = true;
+          else if (c > r) lo = mid;
+          else hi = mid;
+        }
+        float a = lo, z = hi;
+        if (found) {
+          a = INFINITY, z = -INFINITY;  // lowest above the cut, highest below
+          each([&](int, int j) {
+            const float v = row[j];
+            if (v > cut) a = fminf(a, v);
+            else z = fmaxf(z, v);
+          });
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+          }
+        }
+        const bool clear = found && a - z > eps2;
+        int in = 0;
+        each([&](int x, int j) {
+          const float v = row[j];
+          if (clear ? v > cut : v > z + eps2) take[x >> 5] |= 1u << (x & 31), ++in;
+          else if (!clear && v >= a - eps2) open[x >> 5] |= 1u << (x & 31);
+        });
+        need = clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
+      } else {
+        each([&](int x, int) { open[x >> 5] |= 1u << (x & 31); });
+      }
+      if (need > 0) {
+        // exact scores of the open blocks, their keys' upper words in place of the scores;
+        // then, among those that tie in it, by the lower words; then by number
+        double qd[D / 32] = {};
+        const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+        for (int g = 0; g < p.G; ++g)
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x)
+            qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
+#pragma unroll 1
+        for (int word = 0; word < 2; ++word) {
+#pragma unroll 1
+          for (int x = 0; x < nl; ++x) {
+            unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
+            while (m) {
+              const int src = __ffs(m) - 1;
+              m &= m - 1;
+              const int j = 32 * x + src;
+              const unsigned long long k =
+                  order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+              if (lane == src) key[j] = word == 0 ? (uint32_t)(k >> 32) : (uint32_t)k;
+            }
+          }
+          uint32_t t = 0;  // the need-th largest word, bit by bit
+#pragma unroll 1
+          for (uint32_t bitv = 0x80000000u; bitv; bitv >>= 1) {
+            int c = 0;
+            each([&](int x, int j) {
+              if ((open[x >> 5] >> (x & 31)) & 1u) c += key[j] >= (t | bitv);
+            });
+            if ((int)__reduce_add_sync(0xffffffffu, c) >= need) t |= bitv;
+          }
+          int in = 0, same = 0;
+          each([&](int x, int j) {
+            const uint32_t bx = 1u << (x & 31);
+            if (!(open[x >> 5] & bx)) return;
+            if (key[j] > t) take[x >> 5] |= bx, open[x >> 5] &= ~bx, ++in;
+            else if (key[j] < t) open[x >> 5] &= ~bx;
+            else ++same;
+          });
+          need -= __reduce_add_sync(0xffffffffu, in);
+          same = __reduce_add_sync(0xffffffffu, same);
+          if (same == need) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) take[w] |= open[w], open[w] = 0u;
+            need = 0;
+            break;
+          }
+        }
+        // exact ties: the lowest numbers
+#pragma unroll 1
+        for (int x = 0; x < nl && need > 0; ++x) {
+          const bool tie = (open[x >> 5] >> (x & 31)) & 1u;
+          const unsigned m = __ballot_sync(0xffffffffu, tie);
+          if (tie && __popc(m & ((1u << lane) - 1u)) < need) take[x >> 5] |= 1u << (x & 31);
+          need -= __popc(m);
         }
       }
-      if ((at & 31) == lane) key[at] = 1ull;  // taken (no score maps to 1)
-      __syncwarp();
     }
+    int* out = p.idx + ((long long)bh * p.Sq + i) * p.topk;
     int done = 0;
-    for (int j0 = 0; j0 < nvis; j0 += 32) {
-      const bool take = j0 + lane < nvis && key[j0 + lane] == 1ull;
-      const unsigned m = __ballot_sync(0xffffffffu, take);
-      if (take) out[done + __popc(m & ((1u << lane) - 1u))] = j0 + lane;
+#pragma unroll (NL <= 16 ? NL : 4)
+    for (int x = 0; x < NL; ++x) {
+      if (x >= nl) break;
+      const int j = 32 * x + lane;
+      const bool on = j < nvis && (all || j < j0 || j >= j1 || ((take[x >> 5] >> (x & 31)) & 1u));
+      const unsigned m = __ballot_sync(0xffffffffu, on);
+      if (on) out[done + __popc(m & ((1u << lane) - 1u))] = j;
       done += __popc(m);
     }
     for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
-    __syncwarp();
   }
 }
 

@@ -375,14 +375,33 @@ unsigned ckpt_grid(const dash::CkptParams& p) {
   return (unsigned)std::min((p.groups[p.n] * 4 + 255) / 256, 148LL * 16);
 }
 
-template <int D, int QT>
-int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
-  const long long smem = (long long)QT * (D + p.nb) * 8;
-  auto kern = dash::dash_block_select_kernel<D, QT>;
-  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  kern<<<dim3((p.Sq + QT - 1) / QT, B * p.Hkv), 128, (size_t)smem, stream>>>(p);
+template <int D, int QT, int NL>
+int launch_select_tile(const dash::SelectParams& p, int B, cudaStream_t stream) {
+  using C = dash::SelectCfg<D, QT>;
+  auto kern = dash::dash_block_select_kernel<D, QT, NL>;
+  const int smem = C::smem(p.nb);
+  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  kern<<<dim3((p.Sq + QT - 1) / QT, B * p.Hkv), C::kThreads, smem, stream>>>(p);
   DASH_CUDA(cudaGetLastError());
   return DASH_OK;
+}
+
+// A CTA per query below 16 queries a head: an MMA tile would be mostly empty.  Otherwise as
+// many queries a CTA as their scores leave room for in shared memory (two CTAs an SM up to
+// 512 blocks, one beyond).
+template <int D>
+int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
+  if (p.Sq < 16) {
+    dash::dash_block_select_token_kernel<D>
+        <<<dim3(p.Sq, B * p.Hkv), 256, (size_t)p.nb * 8, stream>>>(p);
+    DASH_CUDA(cudaGetLastError());
+    return DASH_OK;
+  }
+  if (p.nb <= 256) return launch_select_tile<D, 64, 8>(p, B, stream);
+  if (p.nb <= 512) return launch_select_tile<D, 32, 16>(p, B, stream);
+  if (p.nb <= 1024) return launch_select_tile<D, 32, 32>(p, B, stream);
+  if (p.nb <= 2048) return launch_select_tile<D, 16, 64>(p, B, stream);
+  return launch_select_tile<D, 8, 128>(p, B, stream);
 }
 
 }  // namespace
@@ -458,11 +477,9 @@ int dash_block_select(const void* q, const long long* q_strides, const float* me
     p.Hkv = Hkv, p.G = H / Hkv, p.Sq = Sq, p.Sk = Sk, p.block = block, p.topk = topk;
     p.nb = (Sk + block - 1) / block;
     p.causal = causal, p.sink = sink, p.local = local;
-    if (p.nb > 4096) return DASH_ERR_UNSUPPORTED;  // four queries' scores in shared memory
+    if (p.nb > 4096) return DASH_ERR_UNSUPPORTED;  // the queries' scores lie in shared memory
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool few = p.nb > 1024;
-    if (D == 64) return few ? launch_select<64, 4>(p, B, cs) : launch_select<64, 16>(p, B, cs);
-    return few ? launch_select<128, 4>(p, B, cs) : launch_select<128, 16>(p, B, cs);
+    return D == 64 ? launch_select<64>(p, B, cs) : launch_select<128>(p, B, cs);
   }, DASH_ERR_OOM, DASH_ERR_INVALID_ARG);
 }
 

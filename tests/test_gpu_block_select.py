@@ -74,7 +74,12 @@ SHAPES = [
     (2, 6, 2, 33, 3000, 128, 64, 16, True, 0, 0, True),
     (1, 8, 1, 40, 2500, 64, 128, 30, False, 2, 2, True),
     (3, 7, 1, 1, 5000, 64, 64, 8, True, 1, 1, True),
-    (1, 2, 1, 3, 70000, 64, 64, 9, True, 1, 1, False),    # more than 1024 blocks
+    (1, 2, 1, 3, 70000, 64, 64, 9, True, 1, 1, False),
+    (2, 4, 2, 70, 20000, 64, 64, 12, True, 1, 1, True),   # 313 blocks
+    (1, 2, 1, 40, 40000, 128, 64, 20, True, 1, 1, False),   # 625
+    (1, 2, 1, 33, 70000, 64, 64, 9, True, 1, 1, False),   # 1094
+    (1, 1, 1, 20, 262144, 64, 64, 5, True, 1, 1, False),  # 4096
+    (1, 3, 1, 64, 5000, 64, 64, 2, True, 1, 1, False),    # every place is forced
     (1, 2, 1, 5, 100, 128, 256, 4, True, 1, 1, False),    # fewer blocks than places
 ]
 
@@ -89,9 +94,10 @@ def test_select_matches_the_definition(shape):
     assert torch.equal(got.cpu(), want)
 
 
-def test_equal_scores_go_to_the_lowest_block_and_near_ones_are_told_apart():
+@pytest.mark.parametrize("Sq", [1, 300])
+def test_equal_scores_go_to_the_lowest_block_and_near_ones_are_told_apart(Sq):
     # all blocks alike but for one bit of one fp32 mean: the fp32 score would not show it
-    q = torch.ones(1, 2, 300, 64, device="cuda", dtype=torch.bfloat16)
+    q = torch.ones(1, 2, Sq, 64, device="cuda", dtype=torch.bfloat16)
     means = torch.full((1, 1, 40, 64), 1.0, device="cuda")
     got = dash.dash_block_select(q, means, 40 * 64, 64, 6, False, 1, 1)
     assert (got.cpu() == torch.tensor([0, 1, 2, 3, 4, 39], dtype=torch.int32)).all()
@@ -102,16 +108,29 @@ def test_equal_scores_go_to_the_lowest_block_and_near_ones_are_told_apart():
     assert (got.cpu() == torch.tensor([0, 1, 3, 4, 17, 39], dtype=torch.int32)).all()
 
 
-def test_zeros_of_either_sign_tie_and_nan_ranks_last():
-    q = torch.ones(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+@pytest.mark.parametrize("Sq", [1, 17])
+def test_zeros_of_either_sign_tie_and_nan_ranks_last(Sq):
+    q = torch.ones(1, 1, Sq, 64, device="cuda", dtype=torch.bfloat16)
     means = torch.zeros(1, 1, 6, 64, device="cuda")
     means[0, 0, 0] = -0.0
     means[0, 0, 1] = float("nan")
     means[0, 0, 2] = float("-inf")
     means[0, 0, 5] = float("inf")
-    pick = lambda n: dash.dash_block_select(q, means, 6 * 64, 64, n, False, 0, 0).flatten().tolist()
+    pick = lambda n: dash.dash_block_select(q, means, 6 * 64, 64, n, False, 0, 0)[0, 0, -1].tolist()
     assert pick(1) == [5] and pick(2) == [0, 5] and pick(4) == [0, 3, 4, 5]
     assert pick(5) == [0, 2, 3, 4, 5] and pick(6) == [0, 1, 2, 3, 4, 5]
+
+
+@pytest.mark.parametrize("Sq", [2, 100])
+def test_zero_queries_and_large_values(Sq):
+    q, k, _, _ = inputs(1, 2, 1, Sq, 2000, 64, False, 6)
+    q[:, :, ::2] = 0  # a padding row: every block ties
+    q[:, :, 1] *= 1e30
+    k[:, :, 300:400] *= 1e8
+    means = dash.dash_block_means(k, 64)
+    got = dash.dash_block_select(q, means, 2000, 64, 5, False, 1, 1)
+    assert torch.equal(got.cpu(), R.select(q, means, 2000, 64, 5, False, 1, 1))
+    assert (got[0, 0, 0].cpu() == torch.tensor([0, 1, 2, 3, 31], dtype=torch.int32)).all()
 
 
 def test_select_takes_strided_queries():
