@@ -234,14 +234,17 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
 
 // Workspace of the backward (offsets in bytes).
 struct BwdWork {
-  long long units, slots, off_delta, off_entry, off_count, off_item, off_slot0, off_head, off_part,
-      bytes;
+  long long units, tokens, slots, off_delta, off_count, off_off, off_token, off_item, off_slot0,
+      off_head, off_part, bytes;
 };
 BwdWork bwd_work(const PlanShape& s, int D) {
   BwdWork w{};
   w.units = (long long)s.B * s.Hkv * s.nu;
-  // a cut unit of n > C entries has ceil(n / C) <= 2 n / C parts, and C >= entries / kStretches
-  const long long most = (long long)s.B * s.Hkv * s.NT * s.U;
+  // a token lists a unit at most once, and a unit of a block per pick
+  w.tokens = (long long)s.B * s.Hkv * s.Sq *
+             std::min((long long)s.nu, (long long)s.topk * (s.block / dash::kUnit));
+  // a cut unit of n > C tiles has ceil(n / C) <= 2 n / C parts, and C >= tiles / kStretches
+  const long long most = w.units + w.tokens / s.T;
   w.slots = std::min(2LL * dash::kStretches, 2 * most / dash::kMinStretch + 1);
   long long at = 0;
   auto put = [&](long long* off, long long bytes) {
@@ -249,15 +252,19 @@ BwdWork bwd_work(const PlanShape& s, int D) {
     at = align256(at + bytes);
   };
   put(&w.off_delta, (long long)s.B * s.H * s.Sq * 4);
-  put(&w.off_entry, w.units * s.NT * 8);
   put(&w.off_count, w.units * 4);
-  put(&w.off_item, (w.units + dash::kStretches) * 16);  // sum of ceil(n / C)
+  put(&w.off_off, w.units * 4);
+  put(&w.off_token, w.tokens * 4);
+  put(&w.off_item, (w.units + dash::kStretches) * (long long)sizeof(dash::SparseItem));  // sum of ceil(n / C)
   put(&w.off_slot0, w.units * 4);
   put(&w.off_head, 8);
   put(&w.off_part, w.slots * 2 * dash::kUnit * D * 4);
   w.bytes = at;
   return w;
 }
+
+template <int D>
+constexpr int kUnitElems = dash::kUnit * D;
 
 template <int D>
 int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* dout,
@@ -273,7 +280,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   int rc = words_for(dev, stream, true, &words);
   if (rc) return rc;
   const BwdWork w = bwd_work(s, D);
-  if (w.units > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
+  if (w.units > 0x7fffffffLL || w.tokens > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv, tdo;
   if ((rc = make_tmap4(&tq, q, s.B, s.H, s.Sq, D, st[0], s.T, s.G)) ||
       (rc = make_tmap4(&tk, k, s.B, s.Hkv, s.Sk, D, st[1], dash::kUnit, 1)) ||
@@ -305,24 +312,35 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
 
   dash::InverseParams iv{};
   iv.plan = view;
-  iv.entry = reinterpret_cast<int2*>(base + w.off_entry);
   iv.count = reinterpret_cast<int*>(base + w.off_count);
-  iv.nu = s.nu, iv.NW = s.NW, iv.NT = s.NT, iv.units = w.units;
-  dash::dash_sparse_inverse_kernel<<<(unsigned)((w.units + 3) / 4), 128, 0, stream>>>(iv);
+  iv.off = reinterpret_cast<int*>(base + w.off_off);
+  iv.token = reinterpret_cast<int*>(base + w.off_token);
+  iv.nu = s.nu, iv.NW = s.NW, iv.NT = s.NT, iv.T = s.T, iv.U = s.U, iv.W = s.W;
+  iv.units = w.units;
+  const unsigned inverse_grid = (unsigned)((w.units + 3) / 4);
+  dash::dash_sparse_inverse_kernel<false><<<inverse_grid, 128, 0, stream>>>(iv);
   DASH_CUDA(cudaGetLastError());
 
   dash::ItemParams im{};
   im.count = iv.count;
-  im.item = reinterpret_cast<int4*>(base + w.off_item);
+  im.off = iv.off;
+  im.item = reinterpret_cast<dash::SparseItem*>(base + w.off_item);
   im.slot0 = reinterpret_cast<int*>(base + w.off_slot0);
   im.head = reinterpret_cast<int*>(base + w.off_head);
+  im.T = s.T, im.nu = s.nu, im.Hkv = s.Hkv;
   im.units = w.units;
   dash::dash_sparse_items_kernel<<<1, 1024, 0, stream>>>(im);
+  DASH_CUDA(cudaGetLastError());
+  dash::dash_sparse_inverse_kernel<true><<<inverse_grid, 128, 0, stream>>>(iv);
   DASH_CUDA(cudaGetLastError());
 
   dash::SparseDkvParams c{};
   c.plan = view;
-  c.entry = iv.entry;
+  c.token = iv.token;
+  c.q = static_cast<const __nv_bfloat16*>(q);
+  c.dout = static_cast<const __nv_bfloat16*>(dout);
+  c.qb = st[0].b, c.qh = st[0].h, c.qs = st[0].s;
+  c.ob = st[3].b, c.oh = st[3].h, c.os = st[3].s;
   c.item = im.item;
   c.head = im.head;
   c.lse = lse;
@@ -331,14 +349,14 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   c.dv = static_cast<__nv_bfloat16*>(dv);
   c.part = reinterpret_cast<float*>(base + w.off_part);
   c.err = words;
-  c.H = s.H, c.Hkv = s.Hkv, c.Sq = s.Sq, c.Sk = s.Sk, c.G = s.G, c.T = s.T, c.W = s.W;
-  c.NT = s.NT, c.U = s.U, c.nu = s.nu, c.causal = s.causal;
+  c.Hkv = s.Hkv, c.Sq = s.Sq, c.Sk = s.Sk, c.G = s.G, c.T = s.T;
+  c.nu = s.nu, c.causal = s.causal;
   c.scale = sc;
   c.scale_log2 = a.scale_log2;
   c.spin_ns = spin;
   auto kk = dash::dash_sparse_dkdv_kernel<D>;
   DASH_CUDA(cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, Ck::kSmemBytes));
-  kk<<<sms, Ck::kThreads, Ck::kSmemBytes, stream>>>(tq, tdo, tk, tv, c);
+  kk<<<sms, Ck::kThreads, Ck::kSmemBytes, stream>>>(tk, tv, c);
   DASH_CUDA(cudaGetLastError());
 
   dash::FinishParams f{};
@@ -347,8 +365,8 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   f.head = im.head;
   f.part = c.part;
   f.dk = c.dk, f.dv = c.dv;
-  f.Sk = s.Sk, f.D = D, f.nu = s.nu;
-  dash::dash_sparse_finish_kernel<<<(unsigned)w.units, 256, 0, stream>>>(f);
+  f.Sk = s.Sk, f.D = D, f.nu = s.nu, f.T = s.T;
+  dash::dash_sparse_finish_kernel<<<dim3((unsigned)w.units, kUnitElems<D> / 1024), 256, 0, stream>>>(f);
   DASH_CUDA(cudaGetLastError());
   return DASH_OK;
 }

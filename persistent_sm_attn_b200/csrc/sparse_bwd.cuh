@@ -9,8 +9,8 @@
 //   dash_sparse_dq_kernel   a CTA per query tile walks the tile's listed units (as the
 //                           forward does) and also writes delta;
 //   dash_sparse_dkdv_kernel a persistent CTA per SM takes items: a unit of 64 keys and a
-//                           stretch of the tiles that list it.
-// A unit that many tiles list (the first block of a causal sequence) is cut into stretches;
+//                           stretch of the tokens that picked it.
+// A unit that many tokens picked (the first block of a causal sequence) is cut into stretches;
 // their fp32 partials are added in order by dash_sparse_finish_kernel.  Results are bitwise
 // reproducible.
 #pragma once
@@ -312,15 +312,19 @@ __global__ void __launch_bounds__(192, 2)
 }
 
 // ------------------------------------------------------------------ who reads a unit
-// For every unit the tiles that list it, ascending, with the place in the tile's list.
+// For every unit the tokens that picked it and see it, ascending: counted, given a place by
+// prefix sums, written.  A warp per unit, a lane per query tile.
 struct InverseParams {
   PlanView plan;
-  int2* entry;  // [B*Hkv*nu][NT] (tile, place)
-  int* count;   // [B*Hkv*nu]
-  int nu, NW, NT;
+  int* count;  // [units] tokens of the unit
+  int* off;    // [units] its first place in `token`
+  int* token;
+  int nu, NW, NT, T, U, W;
   long long units;  // B*Hkv*nu
 };
-__global__ void __launch_bounds__(128) dash_sparse_inverse_kernel(const __grid_constant__ InverseParams p) {
+template <bool kFill>
+__global__ void __launch_bounds__(128)
+    dash_sparse_inverse_kernel(const __grid_constant__ InverseParams p) {
   const long long gu = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (gu >= p.units) return;
   const int lane = threadIdx.x & 31;
@@ -328,81 +332,129 @@ __global__ void __launch_bounds__(128) dash_sparse_inverse_kernel(const __grid_c
   const int u = (int)(gu % p.nu);
   const uint32_t* pres = p.plan.pres + bh * p.NT * p.NW + (u >> 5);
   const int* pre = p.plan.pre + bh * p.NT * p.NW + (u >> 5);
+  int* out = kFill ? p.token + p.off[gu] : nullptr;
   int n = 0;
   for (int t0 = 0; t0 < p.NT; t0 += 32) {
     const int t = t0 + lane;
     const uint32_t w = t < p.NT ? pres[(long long)t * p.NW] : 0u;
     const bool on = (w >> (u & 31)) & 1u;
-    const unsigned m = __ballot_sync(0xffffffffu, on);
-    if (on)
-      p.entry[gu * p.NT + n + __popc(m & ((1u << lane) - 1u))] =
-          make_int2(t, pre[(long long)t * p.NW] + __popc(w & ((1u << (u & 31)) - 1u)));
-    n += __popc(m);
+    uint32_t m[4] = {0u, 0u, 0u, 0u};  // T <= 128 tokens
+    if (on) {
+      const int place = pre[(long long)t * p.NW] + __popc(w & ((1u << (u & 31)) - 1u));
+      const uint32_t* mask = p.plan.mask + ((bh * p.NT + t) * p.U + place) * p.W;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x < p.W) m[x] = mask[x];
+    }
+    const int mine = __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
+    if constexpr (kFill) {
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, before, 31);
+      int at = n + before - mine;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        for (uint32_t rest = m[x]; rest; rest &= rest - 1)
+          out[at++] = t * p.T + 32 * x + __ffs(rest) - 1;
+      n += all;
+    } else {
+      n += mine;
+    }
   }
-  if (lane == 0) p.count[gu] = n;
+  if constexpr (!kFill) {
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) p.count[gu] = n;
+  }
 }
 
-// Items of the dK/dV pass: every listed unit, cut into stretches of at most C entries with
-// C = max(8, total / kStretches), so that the longest item is a small part of an SM's share.
+// Items of the dK/dV pass: every picked unit, its tokens in tiles of T, cut into stretches of
+// at most C tiles with C = max(4, total / kStretches).  Whole stretches come first, so that
+// the CTAs that take items in turn get equally many of them.
 constexpr int kStretches = 148 * 8;
-constexpr int kMinStretch = 8;
+constexpr int kMinStretch = 4;
 
+struct SparseItem {
+  int unit, first, end, slot;   // unit, tiles, partial slot or -1
+  int off, tokens, bh, b;       // the unit's token list, its K/V head and batch entry
+};
 struct ItemParams {
   const int* count;  // [units]
-  int4* item;        // (unit, first entry, end entry, partial slot or -1)
-  int* slot0;        // [units] first partial slot of a cut unit, -1 uncut, -2 never listed
+  int* off;          // [units]
+  SparseItem* item;
+  int* slot0;        // [units] first partial slot of a cut unit, -1 uncut, -2 never picked
   int* head;         // [0] items, [1] C
+  int T, nu, Hkv;
   long long units;
 };
-// One CTA: sums, then exclusive prefix sums of the items and partial slots per unit.
+// One CTA: sums, then exclusive prefix sums of the tokens, items and partial slots per unit.
 __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParams p) {
   __shared__ long long sum[32];
-  __shared__ int2 pre[32];
-  __shared__ long long total;
+  __shared__ int pre[4][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long s = 0;
-  for (long long x = tid; x < p.units; x += 1024) s += p.count[x];
+  auto block_sum = [&](auto&& f) {
+    long long s = 0;
+    for (long long x = tid; x < p.units; x += 1024) s += f((p.count[x] + p.T - 1) / p.T);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) sum[warp] = s;
-  __syncthreads();
-  if (tid == 0) {
-    long long t = 0;
-    for (int w = 0; w < 32; ++w) t += sum[w];
-    total = t;
-  }
-  __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __syncthreads();
+    if (lane == 0) sum[warp] = s;
+    __syncthreads();
+    long long t = sum[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
+  };
+  const long long total = block_sum([](int n) { return n; });
   const int C = (int)max((long long)kMinStretch, (total + kStretches - 1) / kStretches);
-  int items = 0, slots = 0;
+  const int whole = (int)block_sum([&](int n) { return n / C; });
+  int base[4] = {0, whole, 0, 0};  // whole stretches, rests, slots, tokens
   for (long long x0 = 0; x0 < p.units; x0 += 1024) {
     const long long x = x0 + tid;
-    const int n = x < p.units ? p.count[x] : 0;
-    const int parts = (n + C - 1) / C, cut = parts > 1 ? parts : 0;
-    int a = parts, c = cut;  // inclusive prefix sums over the CTA
+    const int tokens = x < p.units ? p.count[x] : 0;
+    const int n = (tokens + p.T - 1) / p.T;
+    const int full = n / C, rest = n % C > 0, cut = full + rest > 1 ? full + rest : 0;
+    const int own[4] = {full, rest, cut, tokens};
+    int inc[4] = {full, rest, cut, tokens};  // inclusive prefix sums over the warp
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int ya = __shfl_up_sync(0xffffffffu, a, o), yc = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) a += ya, c += yc;
-    }
-    if (lane == 31) pre[warp] = make_int2(a, c);
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int y = __shfl_up_sync(0xffffffffu, inc[k], o);
+        if (lane >= o) inc[k] += y;
+      }
+    if (lane == 31)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pre[k][warp] = inc[k];
     __syncthreads();
-    int ba = items, bc = slots, ta = 0, tc = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) ba += pre[w].x, bc += pre[w].y;
-      ta += pre[w].x, tc += pre[w].y;
+    int at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int y = pre[k][lane];
+      at[k] = base[k] + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) + inc[k] - own[k];
+      base[k] += __reduce_add_sync(0xffffffffu, y);
     }
     if (x < p.units) {
-      const int i0 = ba + a - parts, s0 = bc + c - cut;
-      p.slot0[x] = n == 0 ? -2 : cut ? s0 : -1;
-      for (int k = 0; k < parts; ++k)
-        p.item[i0 + k] = make_int4((int)x, k * C, min(n, (k + 1) * C), cut ? s0 + k : -1);
+      p.off[x] = at[3];
+      p.slot0[x] = n == 0 ? -2 : cut ? at[2] : -1;
+      SparseItem w;
+      w.unit = (int)x;
+      w.off = at[3], w.tokens = tokens;
+      w.bh = (int)(x / p.nu);
+      w.b = w.bh / p.Hkv;
+      for (int k = 0; k < full + rest; ++k) {
+        w.first = k * C, w.end = min(n, (k + 1) * C);
+        w.slot = cut ? at[2] + k : -1;
+        p.item[k < full ? at[0] + k : at[1]] = w;
+      }
     }
-    items += ta;
-    slots += tc;
     __syncthreads();
   }
   if (tid == 0) {
-    p.head[0] = items;
+    p.head[0] = base[1];
     p.head[1] = C;
   }
 }
@@ -410,99 +462,116 @@ __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParam
 // ------------------------------------------------------------------ dK, dV
 struct SparseDkvParams {
   PlanView plan;
-  const int2* entry;
-  const int4* item;
+  const int* token;
+  const SparseItem* item;
   const int* head;
+  const __nv_bfloat16 *q, *dout;
+  long long qb, qh, qs, ob, oh, os;  // strides of q and dout in elements
   const float* lse;
   const float* delta;
   __nv_bfloat16 *dk, *dv;  // [B,Hkv,Sk,D]
   float* part;             // [slots][2][64][D] (dK, dV)
   unsigned* err;
-  int H, Hkv, Sq, Sk, G, T, W, NT, U, nu, causal;
+  int Hkv, Sq, Sk, G, T, nu, causal;
   float scale, scale_log2;
   unsigned long long spin_ns;
 };
 
 template <int D>
 struct SparseDkvCfg {
-  static constexpr int kThreads = 320;  // TMA, MMA, two softmax warpgroups
+  static constexpr int kThreads = 640;  // Q rows, dO rows (4 warps each), MMA, K/V, 8 softmax
   static constexpr int kTile = kTileRows * D * 2;
   static constexpr int kKV = kUnit * D * 2;
   static constexpr int kP = kTileRows * kUnit * 2;  // [128][64] bf16
-  static constexpr int kStages = 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int OFF_QDO = 0;  // per stage dO, then Q: at D = 64 one [dO | Q] operand
-  static constexpr int OFF_K = kStages * 2 * kTile;
-  static constexpr int OFF_V = OFF_K + kKV;
-  static constexpr int OFF_P = OFF_V + kKV;  // per warpgroup P, then dS
-  static constexpr int OFF_BAR = OFF_P + 4 * kP;
-  static constexpr int kBars = 2 * kStages + 2 + 2 * 3 + 1;
+  static constexpr int OFF_KV = kStages * 2 * kTile;  // two of K, then V
+  static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS
+  static constexpr int OFF_BAR = OFF_P + 2 * kP;
+  static constexpr int kBars = 4 * kStages + 6 + 4;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
-  static constexpr int kNeed = OFF_SLOT + 16;
-  // at least 120 KiB, so one CTA runs per SM and its 512 TMEM columns are free
-  static constexpr int kSmemBytes = kNeed > 122880 ? kNeed : 122880;
+  static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
-  static constexpr uint32_t TM_S = 0, TM_DV = 256, TM_DK = 320, kTmemCols = 512;
+  static_assert(kSmemBytes > 116 * 1024, "one CTA per SM: its 512 TMEM columns are free");
+  static constexpr uint32_t TM_S = 0, TM_ACC = 256, kTmemCols = 512;
 };
 
-// Per entry (a query tile that lists the unit): S = Q K^T and dP = dO V^T as 128 x 64, P and
-// dS in bf16 to shared memory, then dV^T += dO^T P and dK^T += Q^T dS with the head dimension
-// as the 128 MMA rows (a 64-key M would halve the rate).  At D = 64 the stacked operand
-// [dO | Q] serves both: dV^T is the upper half of one product, dK^T the lower of the other.
-// The warpgroups take entries in turn, so one's exponentials run under the other's products.
+// The rows that attend to a unit are gathered: a tile is T tokens of the unit's list with all
+// G heads, row t G + g, so that no product is spent on tokens that did not pick the unit (a
+// tile of neighbouring tokens would be 2 to 5 times too large at 16 picks of 8k keys).  16-byte
+// cp.async writes the rows in the swizzled layout the products read.
+//
+// Per tile: S = Q K^T and dP = dO V^T as 128 x 64, P and dS in bf16 to shared memory, then
+// dV^T += dO^T P and dK^T += Q^T dS with the head dimension as the 128 MMA rows (a 64-key M
+// would halve the rate).  At D = 64 the stacked operand [dO | Q] serves both: dV^T is the
+// upper half of one product, dK^T the lower of the other.  S and dP of the next tile, K and V
+// and the accumulators of the next item have buffers of their own, so that the products of
+// one tile run under the exponentials of the other, also from item to item.  The two softmax
+// warpgroups take 32 keys of every row each.
 template <int D>
-__global__ void __launch_bounds__(320, 1)
-    dash_sparse_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
-                            const __grid_constant__ CUtensorMap tmDO,
-                            const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(640, 1)
+    dash_sparse_dkdv_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV,
                             const __grid_constant__ SparseDkvParams p) {
   using namespace dev;
   using C = SparseDkvCfg<D>;
+  constexpr int ST = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sb = smem_u32(smem_raw);
   if (sb & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.err, ERR_MISALIGNED);
     return;
   }
-  const uint32_t sK = sb + C::OFF_K, sV = sb + C::OFF_V;
   auto sDO = [&](int s) { return sb + C::OFF_QDO + (uint32_t)(s * 2 * C::kTile); };
   auto sQ = [&](int s) { return sDO(s) + C::kTile; };
-  auto sP = [&](int w) { return sb + C::OFF_P + (uint32_t)(w * 2 * C::kP); };
+  auto sK = [&](int k) { return sb + C::OFF_KV + (uint32_t)((k & 1) * 2 * C::kKV); };
+  auto sV = [&](int k) { return sK(k) + C::kKV; };
+  const uint32_t sP = sb + C::OFF_P, sS = sP + C::kP;
   const uint32_t bar0 = sb + C::OFF_BAR;
-  auto Q_FULL = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-  auto Q_EMPTY = [&](int s) { return bar0 + 16u + 8u * (uint32_t)s; };
-  const uint32_t KV_FULL = bar0 + 32, ITEM_DONE = bar0 + 40, ACC_FREE = bar0 + 48;
-  auto SDP_FULL = [&](int w) { return bar0 + 56u + 8u * (uint32_t)w; };
-  auto PDS_READY = [&](int w) { return bar0 + 72u + 8u * (uint32_t)w; };
-  auto PDS_FREE = [&](int w) { return bar0 + 88u + 8u * (uint32_t)w; };
+  // per stage (Q, dO), per item parity, per tile parity
+  auto FULL = [&](int x, int s) { return bar0 + 8u * (uint32_t)(x * ST + s); };
+  auto EMPTY = [&](int x, int s) { return bar0 + 8u * (uint32_t)((2 + x) * ST + s); };
+  const uint32_t bar1 = bar0 + 32u * ST;
+  auto KV_FULL = [&](int k) { return bar1 + 8u * (uint32_t)(k & 1); };
+  auto ITEM_DONE = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
+  auto ACC_FREE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
+  auto SDP_FULL = [&](int j) { return bar1 + 48u + 8u * (uint32_t)(j & 1); };
+  const uint32_t PDS_READY = bar1 + 64, PDS_FREE = bar1 + 72;
+  auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
+  auto phS = [](int j) { return (uint32_t)((j / ST) & 1); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_SLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t phase) {
     mbar_wait(bar, phase, p.spin_ns, p.err, p.err + 1);
   };
   const int items = p.head[0];
+  const uint32_t inv_g = (65536u + p.G - 1) / p.G;  // row / G = row * inv_g >> 16 for row < 128
+  const int rows = p.G * p.T;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(Q_FULL(s), 1);
-      mbar_init(Q_EMPTY(s), 1);
-      mbar_init(SDP_FULL(s), 1);
-      mbar_init(PDS_READY(s), 128);
-      mbar_init(PDS_FREE(s), 1);
+    for (int s = 0; s < ST; ++s)
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(FULL(x, s), 128);
+        mbar_init(EMPTY(x, s), 1);
+      }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(KV_FULL(k), 1);
+      mbar_init(ITEM_DONE(k), 1);
+      mbar_init(ACC_FREE(k), 256);
+      mbar_init(SDP_FULL(k), 1);
     }
-    mbar_init(KV_FULL, 1);
-    mbar_init(ITEM_DONE, 1);
-    mbar_init(ACC_FREE, 256);
+    mbar_init(PDS_READY, 256);
+    mbar_init(PDS_FREE, 1);
     fence_mbar_init();
   }
   // rows G*T to 127 of a stage are never loaded, but the products sum over all 128 rows
-  for (int x = threadIdx.x; x < (kTileRows - p.G * p.T) * 8 * (4 * D / 64); x += C::kThreads) {
-    const int c = x & 7, rest = x >> 3, atom = rest % (4 * D / 64);
-    const int row = p.G * p.T + rest / (4 * D / 64);
+  for (int x = threadIdx.x; x < (kTileRows - rows) * 8 * (2 * ST * D / 64); x += C::kThreads) {
+    const int c = x & 7, rest = x >> 3, atom = rest % (2 * ST * D / 64);
+    const int row = rows + rest / (2 * ST * D / 64);
     st_shared_v4(sb + C::OFF_QDO + atom * 16384 + row * 128 + c * 16, 0, 0, 0, 0);
   }
   fence_proxy_async_smem();
-  if (warp == 1) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -511,74 +580,110 @@ __global__ void __launch_bounds__(320, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    int it = 0, k = 0;
+  if (warp < 8) {
+    // ---------------------------------------------------------------- row loads
+    // warps 0-3 Q, 4-7 dO; a warp fills 32 rows of each tile, D / 8 lanes a row, and takes
+    // the rows' addresses from the lanes that looked them up
+    const int x = warp >> 2, row_l = (warp & 3) * 32 + lane;
+    constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte pieces of a row, rows at a time
+    const int c = lane % CH, sub = lane / CH;
+    const int t = (int)((uint32_t)row_l * inv_g >> 16), g = row_l - t * p.G;
+    const long long sB = x ? p.ob : p.qb, sH = x ? p.oh : p.qh, sS_ = x ? p.os : p.qs;
+    const __nv_bfloat16* src = (x ? p.dout : p.q) + g * sH;
+    const uint32_t col = (uint32_t)((c >> 3) * 16384);
+    const int rows_w = min(32, rows - (warp & 3) * 32);  // rows of this warp that are loaded
+    int it = 0;
+    SparseItem w;
+    int token = 0;  // of this lane's row in the next tile
+    auto look = [&](const SparseItem& w, int e) {
+      const int at = e * p.T + t;
+      return t < p.T && at < w.tokens ? p.token[w.off + at] : -1;
+    };
+    if ((int)blockIdx.x < items) {
+      w = p.item[blockIdx.x];
+      token = look(w, w.first);
+    }
+    for (int i = blockIdx.x; i < items; i += gridDim.x) {
+      const bool more = i + (int)gridDim.x < items;
+      SparseItem nw = w;
+      if (more) nw = p.item[i + gridDim.x];
+      const int b = w.b, hk = w.bh - b * p.Hkv;
+      const __nv_bfloat16* head = src + b * sB + (long long)hk * p.G * sH;
+      for (int e = w.first; e < w.end; ++e, ++it) {
+        const int s = it % ST;
+        const unsigned on = __ballot_sync(0xffffffffu, token >= 0);
+        const unsigned long long mine =
+            reinterpret_cast<unsigned long long>(head + (long long)max(token, 0) * sS_);
+        token = e + 1 < w.end ? look(w, e + 1) : more ? look(nw, nw.first) : 0;
+        if (it >= ST) wait(EMPTY(x, s), phS(it - ST));
+        const uint32_t dst = (x ? sDO(s) : sQ(s)) + col;
+#pragma unroll 8
+        for (int y = sub; y < 32; y += RP) {
+          const unsigned long long row = __shfl_sync(0xffffffffu, mine, y);
+          const int r = (warp & 3) * 32 + y;
+          if (y < rows_w)  // rows past the list arrive as zeros
+            cp_async16(dst + (uint32_t)(r * 128 + ((c ^ r) & 7) * 16),
+                       reinterpret_cast<const void*>(row + c * 16), (on >> y) & 1u ? 16u : 0u);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        mbar_arrive(FULL(x, s));
+      }
+      w = nw;
+    }
+  } else if (warp == 9 && lane == 0) {
+    // ---------------------------------------------------------------- K and V
+    int k = 0;
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
-      const int4 w = p.item[i];
-      const int bh = w.x / p.nu, u = w.x - bh * p.nu, b = bh / p.Hkv, hk = bh - b * p.Hkv;
-      const int2* entry = p.entry + (long long)w.x * p.NT;
-      if (k > 0) wait(ITEM_DONE, (uint32_t)((k - 1) & 1));  // K and V are read to the end
-      mbar_expect_tx(KV_FULL, 2 * C::kKV);
+      const SparseItem w = p.item[i];
+      const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
+      if (k >= 2) wait(ITEM_DONE(k), ph2(k - 2));  // K and V of item k - 2 are read to the end
+      mbar_expect_tx(KV_FULL(k), 2 * C::kKV);
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb) {
-        tma_load_4d(sK + cb * 8192, &tmK, cb * 64, u * kUnit, hk, b, KV_FULL);
-        tma_load_4d(sV + cb * 8192, &tmV, cb * 64, u * kUnit, hk, b, KV_FULL);
-      }
-      int tile = entry[w.y].x;
-      for (int e = w.y; e < w.z; ++e, ++it) {
-        const int s = it & 1;
-        const int next = e + 1 < w.z ? entry[e + 1].x : 0;
-        if (it >= 2) wait(Q_EMPTY(s), (uint32_t)(((it >> 1) - 1) & 1));
-        mbar_expect_tx(Q_FULL(s), (uint32_t)(2 * p.G * p.T * D * 2));
-#pragma unroll
-        for (int cb = 0; cb < D / 64; ++cb) {
-          tma_load_4d(sQ(s) + cb * 16384, &tmQ, cb * 64, tile * p.T, hk * p.G, b, Q_FULL(s));
-          tma_load_4d(sDO(s) + cb * 16384, &tmDO, cb * 64, tile * p.T, hk * p.G, b, Q_FULL(s));
-        }
-        tile = next;
+        tma_load_4d(sK(k) + cb * 8192, &tmK, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
+        tma_load_4d(sV(k) + cb * 8192, &tmV, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
       }
     }
     // no load may land after the CTA has gone, not even when a wait ran out
-    if (k > 0) mbar_wait_drain(KV_FULL, (uint32_t)((k - 1) & 1), p.spin_ns, p.err, p.err + 1);
-    for (int j = max(0, it - 2); j < it; ++j)
-      mbar_wait_drain(Q_FULL(j & 1), (uint32_t)((j >> 1) & 1), p.spin_ns, p.err, p.err + 1);
-  } else if (warp == 1 && lane == 0) {
+    for (int j = max(0, k - 2); j < k; ++j)
+      mbar_wait_drain(KV_FULL(j), ph2(j), p.spin_ns, p.err, p.err + 1);
+  } else if (warp == 8 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
     constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
     const uint32_t hi = sdesc_hi(1024);
-    const uint32_t kK = sdesc_lo(sK, 16), kV = sdesc_lo(sV, 16);
-    int it = 0, k = 0;
-    auto issue_acc = [&](int j, bool first) {
-      const int s = j & 1;
-      const uint32_t aV = sdesc_lo(sDO(s), 16384);
-      const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
-      const uint32_t bP = sdesc_lo(sP(s), 16384), bS = sdesc_lo(sP(s) + C::kP, 16384);
-      wait(PDS_READY(s), (uint32_t)((j >> 1) & 1));
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        tc_mma_ss_w(tmem + C::TM_DV, aV + kk * 128, bP + kk * 128, hi, ID_T,
-                    (!first || kk > 0) ? 1u : 0u);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        tc_mma_ss_w(tmem + C::TM_DK, aK + kk * 128, bS + kk * 128, hi, ID_T,
-                    (!first || kk > 0) ? 1u : 0u);
-      tc_commit(PDS_FREE(s));
-      tc_commit(Q_EMPTY(s));
+    const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384);
+    // two cursors over the CTA's tiles: S and dP run up to two tiles ahead of dV and dK
+    struct Cursor {
+      int i, k, e, first, end, j;  // item, its number, tile, the item's tiles, tile number
+      bool on;
     };
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
-      const int4 w = p.item[i];
-      wait(KV_FULL, (uint32_t)(k & 1));
-      const int it0 = it;
-      for (int e = w.y; e < w.z; ++e, ++it) {
-        const int s = it & 1;
+    auto open = [&](Cursor& c) {
+      c.on = c.i < items;
+      if (c.on) c.first = c.e = p.item[c.i].first, c.end = p.item[c.i].end;
+    };
+    auto step = [&](Cursor& c) {
+      ++c.j;
+      if (++c.e == c.end) c.i += gridDim.x, ++c.k, open(c);
+    };
+    Cursor a{(int)blockIdx.x, 0, 0, 0, 0, 0, false};
+    open(a);
+    Cursor d = a;
+    int last = -1;  // the last item's number
+    uint64_t since = 0;
+    bool given_up = false;
+    while (d.on) {
+      bool did = false;
+      if (a.on && a.j <= d.j + 1 && (given_up || (mbar_test_wait(FULL(0, a.j % ST), phS(a.j)) &&
+                                                  mbar_test_wait(FULL(1, a.j % ST), phS(a.j)) &&
+                                                  mbar_test_wait(KV_FULL(a.k), ph2(a.k))))) {
+        // S and dP of tile j - 2 were read before its P and dS were ready
+        const int s = a.j % ST;
         const uint32_t kQ = sdesc_lo(sQ(s), 16), kDO = sdesc_lo(sDO(s), 16);
-        const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)s;
-        wait(Q_FULL(s), (uint32_t)((it >> 1) & 1));
+        const uint32_t kK = sdesc_lo(sK(a.k), 16), kV = sdesc_lo(sV(a.k), 16);
+        const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(a.j & 1);
         tc_fence_after();
-        // S and dP of entry it - 2 were read before its P and dS were ready
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
@@ -589,150 +694,179 @@ __global__ void __launch_bounds__(320, 1)
           tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                       kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
                       kk > 0 ? 1u : 0u);
-        tc_commit(SDP_FULL(s));
-        if (it > it0) {
-          // the accumulators are written first here: the last item's must have been read
-          if (it == it0 + 1 && k > 0) {
-            wait(ACC_FREE, (uint32_t)((k - 1) & 1));
-            tc_fence_after();
-          }
-          issue_acc(it - 1, it - 1 == it0);
+        tc_commit(SDP_FULL(a.j));
+        step(a);
+        did = true;
+      }
+      if (d.j < a.j && (given_up || mbar_test_wait(PDS_READY, (uint32_t)(d.j & 1)))) {
+        const int s = d.j % ST;
+        const bool first = d.e == d.first;
+        // the accumulators of item k - 2 must have been read
+        if (first && d.k >= 2) wait(ACC_FREE(d.k), ph2(d.k - 2));
+        const uint32_t aV = sdesc_lo(sDO(s), 16384);
+        const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
+        const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(d.k & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (!first || kk > 0) ? 1u : 0u);
+        if (D == 128) tc_commit(EMPTY(1, s));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
+                      (!first || kk > 0) ? 1u : 0u);
+        if (D == 64) tc_commit(EMPTY(1, s));
+        tc_commit(EMPTY(0, s));
+        tc_commit(PDS_FREE);
+        last = d.k;
+        if (d.e + 1 == d.end) tc_commit(ITEM_DONE(d.k));
+        step(d);
+        did = true;
+      }
+      if (did) {
+        since = 0;
+      } else {
+        const uint64_t now = globaltimer();
+        if (since == 0) {
+          since = now;
+        } else if (now - since > p.spin_ns || aborted(p.err + 1)) {
+          // go on without waiting, so that every other wait of the CTA ends
+          if (!given_up) raise_timeout(p.err, p.err + 1, ERR_WHERE_PIPE);
+          given_up = true;
         }
       }
-      if (it == it0 + 1 && k > 0) {
-        wait(ACC_FREE, (uint32_t)((k - 1) & 1));
-        tc_fence_after();
-      }
-      issue_acc(it - 1, it - 1 == it0);
-      tc_commit(ITEM_DONE);
     }
-    if (k > 0)
-      mbar_wait_drain(ITEM_DONE, (uint32_t)((k - 1) & 1), p.spin_ns, p.err, p.err + 1);
-  } else if (warp >= 2) {
+    if (last >= 0) mbar_wait_drain(ITEM_DONE(last), ph2(last), p.spin_ns, p.err, p.err + 1);
+  } else if (warp >= 12) {
     // ---------------------------------------------------------------- softmax gradient
-    const int wg = (warp - 2) >> 2, quarter = warp & 3;
+    const int wg = (warp - 12) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const int g = r / p.T, t = r - g * p.T;
+    const int t = (int)((uint32_t)r * inv_g >> 16), g = r - t * p.G;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)wg;
-    const uint32_t rowP = sP(wg) + r * 128, rowS = rowP + C::kP;
+    const uint32_t rowP = sP + r * 128, rowS = sS + r * 128;
     const float sl2 = p.scale_log2;
-    const int bit = t & 31, wsel = min(t >> 5, p.W - 1);
+    // what this thread's row of a tile needs, fetched one tile ahead
+    float lse2 = 0.f, delta = 0.f;
+    int vis = 0;  // keys below it are attended to
+    auto fetch = [&](const SparseItem& w, int e) {
+      const int base = (w.unit - w.bh * p.nu) * kUnit;
+      const int kvlen = p.plan.len[w.b];
+      // a row without a token has Q = dO = 0: P dO and dS Q are 0 whatever P and a finite
+      // dS are; keys past the sequence, which may be anything, are left out for it too
+      lse2 = delta = 0.f;
+      vis = kvlen - base;
+      const int at = e * p.T + t;
+      if (t >= p.T || at >= w.tokens) return;
+      const int token = p.token[w.off + at];
+      const long long row = ((long long)w.bh * p.G + g) * p.Sq + token;
+      lse2 = p.lse[row] * 1.4426950408889634f;
+      delta = p.delta[row];
+      if (p.causal) vis = (int)min((long long)kvlen, (long long)p.plan.start[w.b] + token + 1) - base;
+    };
     int it = 0, k = 0;
+    SparseItem w;
+    if ((int)blockIdx.x < items) {
+      w = p.item[blockIdx.x];
+      fetch(w, w.first);
+    }
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
-      const int4 w = p.item[i];
-      const int bh = w.x / p.nu, u = w.x - bh * p.nu, b = bh / p.Hkv, hk = bh - b * p.Hkv;
-      const int2* entry = p.entry + (long long)w.x * p.NT;
-      const int base = u * kUnit;
-      const int kvlen = p.plan.len[b];
-      const long long start = p.plan.start[b];
-      const long long row0 = ((long long)b * p.H + hk * p.G + g) * p.Sq;
-      // what this thread's row of entry e needs, fetched one entry of its own ahead
-      float lse2 = 0.f, delta = 0.f;
-      int vis = 0;
-      auto fetch = [&](int e, float& f_lse, float& f_delta, int& f_vis) {
-        f_lse = f_delta = 0.f;
-        f_vis = 0;
-        if (e >= w.z) return;
-        const int2 at = entry[e];
-        const int token = at.x * p.T + t;
-        if (g >= p.G || token >= p.Sq) return;
-        const long long gt = (long long)bh * p.NT + at.x;
-        const uint32_t word = p.plan.mask[(gt * p.U + at.y) * p.W + wsel];
-        f_lse = p.lse[row0 + token] * 1.4426950408889634f;
-        f_delta = p.delta[row0 + token];
-        const long long limit = p.causal ? min((long long)kvlen, max(start + token + 1, 0ll))
-                                         : (long long)kvlen;
-        f_vis = ((word >> bit) & 1u) ? (int)(limit - base) : 0;
-      };
-      int e = w.y + ((it ^ wg) & 1);  // this warpgroup takes the steps of its own parity
-      fetch(e, lse2, delta, vis);
-      for (; e < w.z; e += 2) {
-        const int step = it + (e - w.y);
-        float n_lse, n_delta;
-        int n_vis;
-        fetch(e + 2, n_lse, n_delta, n_vis);
-        wait(SDP_FULL(wg), (uint32_t)((step >> 1) & 1));
+      const bool more = i + (int)gridDim.x < items;
+      SparseItem nw = w;
+      if (more) nw = p.item[i + gridDim.x];
+      for (int e = w.first; e < w.end; ++e, ++it) {
+        const float l2 = lse2, dl = delta;
+        const int v = vis - 32 * wg;
+        if (e + 1 < w.end) fetch(w, e + 1);
+        else if (more) fetch(nw, nw.first);
+        const bool whole = __all_sync(0xffffffffu, v >= 32);
+        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(it & 1) + 32u * wg;
+        wait(SDP_FULL(it), ph2(it));
         tc_fence_after();
-        if (step >= 2) wait(PDS_FREE(wg), (uint32_t)(((step >> 1) - 1) & 1));
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32], dp[32];
-          tmem_ld32x2(tS + 32 * c, tS + 64 + 32 * c, sv, dp);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t sv[16], dp[16];
+          tmem_ld16_async(tS + 16 * h, sv);
+          tmem_ld16_async(tS + 64 + 16 * h, dp);
+          tmem_wait_ld();
+          uint32_t pp[8], ds[8];
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t pp[4], ds[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int key = 8 * c4 + 2 * x;
-              float p0 = 0.f, p1 = 0.f, d0 = 0.f, d1 = 0.f;
-              // selected, not multiplied: S and dP of a masked key may be anything
-              if (32 * c + key < vis) {
-                p0 = ex2_approx(__uint_as_float(sv[key]) * sl2 - lse2);
-                d0 = p0 * (__uint_as_float(dp[key]) - delta);
-              }
-              if (32 * c + key + 1 < vis) {
-                p1 = ex2_approx(__uint_as_float(sv[key + 1]) * sl2 - lse2);
-                d1 = p1 * (__uint_as_float(dp[key + 1]) - delta);
-              }
-              pp[x] = pack_bf16x2(p0, p1);
-              ds[x] = pack_bf16x2(d0, d1);
+          for (int x = 0; x < 8; ++x) {
+            float p0, p1, d0, d1;
+            fma_f32x2(p0, p1, __uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]), sl2, -l2);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add_f32x2(d0, d1, __uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), -dl);
+            mul_f32x2(d0, d1, p0, p1, d0, d1);
+            if (!whole) {  // selected, not multiplied: S and dP of a masked key may be anything
+              if (16 * h + 2 * x >= v) p0 = d0 = 0.f;
+              if (16 * h + 2 * x + 1 >= v) p1 = d1 = 0.f;
             }
-            const uint32_t off = (uint32_t)(((4 * c + c4) ^ (r & 7)) << 4);
-            st_shared_v4(rowP + off, pp[0], pp[1], pp[2], pp[3]);
-            st_shared_v4(rowS + off, ds[0], ds[1], ds[2], ds[3]);
+            pp[x] = pack_bf16x2(p0, p1);
+            ds[x] = pack_bf16x2(d0, d1);
+          }
+          if (h == 0 && it > 0) wait(PDS_FREE, (uint32_t)((it - 1) & 1));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t off = (uint32_t)(((4 * wg + 2 * h + x) ^ (r & 7)) << 4);
+            st_shared_v4(rowP + off, pp[4 * x], pp[4 * x + 1], pp[4 * x + 2], pp[4 * x + 3]);
+            st_shared_v4(rowS + off, ds[4 * x], ds[4 * x + 1], ds[4 * x + 2], ds[4 * x + 3]);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(PDS_READY(wg));
-        lse2 = n_lse, delta = n_delta, vis = n_vis;
+        mbar_arrive(PDS_READY);
       }
-      it += w.z - w.y;
       // epilogue: warpgroup 0 writes dV, warpgroup 1 dK; lane = head dimension, column = key
-      wait(ITEM_DONE, (uint32_t)(k & 1));
+      wait(ITEM_DONE(k), ph2(k));
       tc_fence_after();
-      uint32_t acc[2][32];
-      const uint32_t ta = tmem + lane_off + (wg == 0 ? C::TM_DV : C::TM_DK);
-      tmem_ld32x2(ta, ta + 32, acc[0], acc[1]);
-      tc_fence_before();
-      mbar_arrive(ACC_FREE);
+      const uint32_t ta = tmem + lane_off + C::TM_ACC + 128u * (uint32_t)(k & 1) + 64u * wg;
+      const int base = (w.unit - w.bh * p.nu) * kUnit;
       // at D = 64 dV^T is in lanes 0-63 of its product, dK^T in lanes 64-127 of its own
       const int d = D == 128 ? r : r - (wg == 0 ? 0 : 64);
-      if (d >= 0 && d < D) {
-        const float f = wg == 0 ? 1.f : p.scale;
-        if (w.w >= 0) {
-          float* out = p.part + ((long long)w.w * 2 + (wg == 0 ? 1 : 0)) * kUnit * D + d;
+      const float f = wg == 0 ? 1.f : p.scale;
 #pragma unroll
-          for (int key = 0; key < kUnit; ++key)
-            out[key * D] = __uint_as_float(acc[key >> 5][key & 31]) * f;
+      for (int c = 0; c < 2; ++c) {
+        uint32_t acc[32];
+        tmem_ld32(ta + 32 * c, acc);
+        if (c == 1) {
+          tc_fence_before();
+          mbar_arrive(ACC_FREE(k));
+        }
+        if (d < 0 || d >= D) continue;
+        if (w.slot >= 0) {
+          float* out =
+              p.part + (((long long)w.slot * 2 + (wg == 0 ? 1 : 0)) * kUnit + 32 * c) * D + d;
+#pragma unroll
+          for (int key = 0; key < 32; ++key) out[key * D] = __uint_as_float(acc[key]) * f;
         } else {
-          __nv_bfloat16* out = (wg == 0 ? p.dv : p.dk) + ((long long)bh * p.Sk + base) * D + d;
-          const int keys = min(kUnit, p.Sk - base);
+          __nv_bfloat16* out =
+              (wg == 0 ? p.dv : p.dk) + ((long long)w.bh * p.Sk + base + 32 * c) * D + d;
+          const int keys = p.Sk - base - 32 * c;
 #pragma unroll
-          for (int key = 0; key < kUnit; ++key)
-            if (key < keys)
-              out[key * D] = __float2bfloat16_rn(__uint_as_float(acc[key >> 5][key & 31]) * f);
+          for (int key = 0; key < 32; ++key)
+            if (key < keys) out[key * D] = __float2bfloat16_rn(__uint_as_float(acc[key]) * f);
         }
       }
+      w = nw;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// Units that no tile lists get zeros; the partials of cut units are added in ascending order.
+// Units that no token picked get zeros; the partials of cut units are added in ascending
+// order.  A CTA takes 1024 elements of a unit's dK and dV (blockIdx.y).
 struct FinishParams {
   const int* slot0;
   const int* count;
   const int* head;
   const float* part;
   __nv_bfloat16 *dk, *dv;
-  int Sk, D, nu;
+  int Sk, D, nu, T;
 };
 __global__ void __launch_bounds__(256) dash_sparse_finish_kernel(const FinishParams p) {
   const int gu = blockIdx.x;
@@ -740,19 +874,24 @@ __global__ void __launch_bounds__(256) dash_sparse_finish_kernel(const FinishPar
   if (s0 == -1) return;
   const int bh = gu / p.nu, base = (gu - bh * p.nu) * kUnit;
   const int n = min(kUnit, p.Sk - base) * p.D;
-  const int parts = s0 < 0 ? 0 : (p.count[gu] + p.head[1] - 1) / p.head[1];
-  const long long at = ((long long)bh * p.Sk + base) * p.D;
-  for (int x = threadIdx.x * 2; x < n; x += 512) {
-    float2 a = make_float2(0.f, 0.f), c = a;
-    for (int k = 0; k < parts; ++k) {
-      const float* src = p.part + (long long)(s0 + k) * 2 * kUnit * p.D + x;
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      const float2 z = *reinterpret_cast<const float2*>(src + kUnit * p.D);
-      a.x += y.x, a.y += y.y, c.x += z.x, c.y += z.y;
-    }
-    *reinterpret_cast<uint32_t*>(p.dk + at + x) = dev::pack_bf16x2(a.x, a.y);
-    *reinterpret_cast<uint32_t*>(p.dv + at + x) = dev::pack_bf16x2(c.x, c.y);
+  const int tiles = (p.count[gu] + p.T - 1) / p.T, C = p.head[1];
+  const int parts = s0 < 0 ? 0 : (tiles + C - 1) / C;
+  const int x = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 4;
+  if (x >= n) return;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
+  const float* src = p.part + (long long)max(s0, 0) * 2 * kUnit * p.D + x;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k, src += 2 * kUnit * p.D) {
+    const float4 y = *reinterpret_cast<const float4*>(src);
+    const float4 z = *reinterpret_cast<const float4*>(src + kUnit * p.D);
+    a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
+    c.x += z.x, c.y += z.y, c.z += z.z, c.w += z.w;
   }
+  const long long at = ((long long)bh * p.Sk + base) * p.D + x;
+  *reinterpret_cast<uint2*>(p.dk + at) =
+      make_uint2(dev::pack_bf16x2(a.x, a.y), dev::pack_bf16x2(a.z, a.w));
+  *reinterpret_cast<uint2*>(p.dv + at) =
+      make_uint2(dev::pack_bf16x2(c.x, c.y), dev::pack_bf16x2(c.z, c.w));
 }
 
 }  // namespace dash
