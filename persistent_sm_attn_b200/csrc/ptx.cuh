@@ -18,6 +18,19 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// the warp's number as a value the compiler knows to be the same in all lanes
+__device__ __forceinline__ int warp_uniform() {
+  return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+}
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -27,6 +40,11 @@ __device__ __forceinline__ void fence_mbar_init() {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// one arrival for the whole warp: arrivals on one barrier are served one at a time
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
@@ -91,6 +109,31 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
       return false;
     }
   }
+}
+
+// mbar_wait with everything but the first polls out of line.  A thread that issues products
+// runs its loop once a tile, through cold instruction caches: there the time goes by the code
+// it has to fetch.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                   unsigned* err) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (aborted(err + 1)) return false;
+    if (globaltimer() - t0 > limit_ns) {
+      raise_timeout(err, err + 1, ERR_WHERE_PIPE);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                               unsigned* err) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_long(bar, parity, limit_ns, err);
 }
 
 // ---------------------------------------------------------------- clusters

@@ -177,6 +177,21 @@ int make_tmap4(CUtensorMap* m, const void* base, int B, int H, int S, int D, con
   return r == CUDA_SUCCESS ? DASH_OK : DASH_ERR_CUDA;
 }
 
+// The same with boxes of 64 columns x heads x rows: row t G + g of a tile is row t, head g.
+int make_tmap4_rows(CUtensorMap* m, const void* base, int B, int H, int S, int D, const Strides& st,
+                    int rows, int heads) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return DASH_ERR_CUDA;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)st.h * 2, (cuuint64_t)st.s * 2, (cuuint64_t)st.b * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DASH_OK : DASH_ERR_CUDA;
+}
+
 // Parts that a tile's list is split into: enough CTAs for two on each of 148 SMs, and at
 // least two units a part.
 int fwd_splits(const PlanShape& s) {
@@ -282,32 +297,42 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   const BwdWork w = bwd_work(s, D);
   if (w.units > 0x7fffffffLL || w.tokens > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv, tdo;
-  if ((rc = make_tmap4(&tq, q, s.B, s.H, s.Sq, D, st[0], s.T, s.G)) ||
+  if ((rc = make_tmap4_rows(&tq, q, s.B, s.H, s.Sq, D, st[0], s.T, s.G)) ||
       (rc = make_tmap4(&tk, k, s.B, s.Hkv, s.Sk, D, st[1], dash::kUnit, 1)) ||
       (rc = make_tmap4(&tv, v, s.B, s.Hkv, s.Sk, D, st[2], dash::kUnit, 1)) ||
-      (rc = make_tmap4(&tdo, dout, s.B, s.H, s.Sq, D, st[3], s.T, s.G)))
+      (rc = make_tmap4_rows(&tdo, dout, s.B, s.H, s.Sq, D, st[3], s.T, s.G)))
     return rc;
   char* base = static_cast<char*>(work);
   const PlanView view = plan_view(s, plan);
   const float sc = scale_or_default(scale, D);
   const unsigned long long spin = (unsigned long long)dash::spin_limit_us() * 1000ull;
 
+  dash::SparseDeltaParams dl{};
+  dl.o = static_cast<const __nv_bfloat16*>(o);
+  dl.dout = static_cast<const __nv_bfloat16*>(dout);
+  dl.ob = st[3].b, dl.oh = st[3].h, dl.os = st[3].s;
+  dl.delta = reinterpret_cast<float*>(base + w.off_delta);
+  dl.H = s.H, dl.Sq = s.Sq, dl.rows = (long long)s.B * s.H * s.Sq;
+  constexpr int kDeltaRows = 4 * 256 / (D / 8);
+  dash::dash_sparse_delta_kernel<D>
+      <<<(unsigned)((dl.rows + kDeltaRows - 1) / kDeltaRows), 256, 0, stream>>>(dl);
+  DASH_CUDA(cudaGetLastError());
+
   dash::SparseDqParams a{};
   a.plan = view;
-  a.o = static_cast<const __nv_bfloat16*>(o);
   a.lse = lse;
   a.dq = static_cast<__nv_bfloat16*>(dq);
-  a.delta = reinterpret_cast<float*>(base + w.off_delta);
+  a.delta = dl.delta;
   a.err = words;
-  a.H = s.H, a.Hkv = s.Hkv, a.Sq = s.Sq, a.Sk = s.Sk, a.G = s.G, a.T = s.T, a.W = s.W;
+  a.Hkv = s.Hkv, a.Sq = s.Sq, a.Sk = s.Sk, a.G = s.G, a.T = s.T, a.W = s.W;
   a.NT = s.NT, a.U = s.U, a.causal = s.causal;
+  a.tiles = s.B * s.Hkv * s.NT;
   a.scale = sc;
   a.scale_log2 = sc * 1.4426950408889634f;
   a.spin_ns = spin;
   auto kq = dash::dash_sparse_dq_kernel<D>;
   DASH_CUDA(cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, Cq::kSmemBytes));
-  kq<<<(unsigned)((long long)s.B * s.Hkv * s.NT), Cq::kThreads, Cq::kSmemBytes, stream>>>(tq, tdo, tk,
-                                                                                       tv, a);
+  kq<<<std::min(sms, a.tiles), Cq::kThreads, Cq::kSmemBytes, stream>>>(tq, tdo, tk, tv, a);
   DASH_CUDA(cudaGetLastError());
 
   dash::InverseParams iv{};

@@ -20,40 +20,89 @@
 
 namespace dash {
 
+// ------------------------------------------------------------------ delta
+// delta = rowsum(dO o O) of every row, D / 8 lanes a row, four rows in flight a lane.  Bound
+// by reading O and dO.
+struct SparseDeltaParams {
+  const __nv_bfloat16 *o, *dout;
+  long long ob, oh, os;  // strides of dout in elements
+  float* delta;
+  int H, Sq;
+  long long rows;
+};
+template <int D>
+__global__ void __launch_bounds__(256) dash_sparse_delta_kernel(const SparseDeltaParams p) {
+  constexpr int CH = D / 8, RP = 256 / CH;
+  const int c = threadIdx.x % CH;
+  const long long row0 = (long long)blockIdx.x * (4 * RP) + threadIdx.x / CH;
+  uint4 x[4], z[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const long long row = min(row0 + y * RP, p.rows - 1);
+    const int bh = (int)(row / p.Sq), i = (int)(row - (long long)bh * p.Sq);
+    const int b = bh / p.H, h = bh - b * p.H;
+    x[y] = __ldcs(reinterpret_cast<const uint4*>(p.o + row * D) + c);
+    z[y] = *reinterpret_cast<const uint4*>(p.dout + b * p.ob + h * p.oh + i * p.os + c * 8);
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const uint32_t xs[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+    const uint32_t zs[4] = {z[y].x, z[y].y, z[y].z, z[y].w};
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      sum = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(zs[q] << 16), sum);
+      sum = fmaf(__uint_as_float(xs[q] & 0xffff0000u), __uint_as_float(zs[q] & 0xffff0000u), sum);
+    }
+#pragma unroll
+    for (int o = CH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const long long row = row0 + y * RP;
+    if (c == 0 && row < p.rows) p.delta[row] = sum;
+  }
+}
+
 // ------------------------------------------------------------------ dQ
 struct SparseDqParams {
   PlanView plan;
-  const __nv_bfloat16* o;  // [B,H,Sq,D]
-  const float* lse;        // [B,H,Sq]
-  __nv_bfloat16* dq;       // [B,H,Sq,D]
-  float* delta;            // [B,H,Sq]
+  const float* lse;    // [B,H,Sq]
+  const float* delta;  // [B,H,Sq]
+  __nv_bfloat16* dq;   // [B,H,Sq,D]
   unsigned* err;
-  int H, Hkv, Sq, Sk, G, T, W, NT, U, causal;
+  int Hkv, Sq, Sk, G, T, W, NT, U, tiles, causal;
   float scale, scale_log2;
   unsigned long long spin_ns;
 };
 
 template <int D>
 struct SparseDqCfg {
-  static constexpr int kThreads = 192;
-  static constexpr int kQ = kTileRows * D * 2;
-  static constexpr int kKV = kUnit * D * 2;
-  static constexpr int kKSt = 2;                  // K is read by S and by dQ
-  static constexpr int kVSt = D == 128 ? 1 : 2;   // V is free again after dP
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_DO = kQ;
-  static constexpr int OFF_K = 2 * kQ;
-  static constexpr int OFF_V = OFF_K + kKSt * kKV;
-  static constexpr int OFF_BAR = OFF_V + kVSt * kKV;
-  static constexpr int kBars = 6 + 2 * kKSt + 2 * kVSt;
+  static constexpr int kThreads = 640;  // TMA, S and dP, dQ, -, 16 warps of softmax
+  static constexpr int kTile = kTileRows * D * 2;
+  static constexpr int kPair = 2 * kUnit * D * 2;
+  // tiles of Q and dO, pairs of K and of V: K is read twice and stays longer than V
+  static constexpr int kQ = D == 128 ? 1 : 2, kK = D == 128 ? 3 : 4, kV = D == 128 ? 2 : 4;
+  static constexpr int OFF_Q = 0;  // Q, then dO
+  static constexpr int OFF_K = kQ * 2 * kTile;
+  static constexpr int OFF_V = OFF_K + kK * kPair;
+  static constexpr int OFF_BAR = OFF_V + kV * kPair;
+  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 7;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
-  static_assert(kSmemBytes <= 115712, "two CTAs per SM");
-  static constexpr uint32_t TM_S = 0, TM_DP = 64, TM_DQ = 128, kTmemCols = 256;
+  static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
+  static_assert(kSmemBytes > 116 * 1024, "one CTA per SM: its 512 TMEM columns are free");
+  static constexpr int kAcc = D == 128 ? 1 : 2;  // accumulators
+  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DS = 256, TM_DQ = 384, kTmemCols = 512;
 };
 
+// A persistent CTA per SM takes query tiles, those with the longest lists (the last, under a
+// causal mask) first, and walks a tile's list in pairs of units: S = Q K^T, dP = dO V^T
+// (128 x 128, TMEM), dS in bf16 to TMEM, dQ += dS K.  A product of 128 keys reads a third less
+// shared memory a key than one of 64, which it would be bound by.  Four softmax warpgroups take
+// 32 keys of the pair each.  S and dP have a buffer each, free again as soon as they are read: the
+// next S runs under this pair's exponentials, the next dP and this dQ under the next pair's.
+// Row t G + g of a tile is token t, head g, so a warp holds few tokens and skips the
+// exponentials of units that none of them picked.
 template <int D>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(640, 1)
     dash_sparse_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmDO,
                           const __grid_constant__ CUtensorMap tmK,
@@ -67,40 +116,68 @@ __global__ void __launch_bounds__(192, 2)
     if (threadIdx.x == 0) atomicOr(p.err, ERR_MISALIGNED);
     return;
   }
-  const uint32_t sQ = sb + C::OFF_Q, sDO = sb + C::OFF_DO, sK = sb + C::OFF_K, sV = sb + C::OFF_V;
+  auto sQ = [&](int k) { return sb + C::OFF_Q + (uint32_t)((k % C::kQ) * 2 * C::kTile); };
+  auto sDO = [&](int k) { return sQ(k) + C::kTile; };
+  auto sK = [&](int j) { return sb + C::OFF_K + (uint32_t)((j % C::kK) * C::kPair); };
+  auto sV = [&](int j) { return sb + C::OFF_V + (uint32_t)((j % C::kV) * C::kPair); };
   const uint32_t bar0 = sb + C::OFF_BAR;
-  const uint32_t Q_FULL = bar0, S_FULL = bar0 + 8, DP_FULL = bar0 + 16, DS_READY = bar0 + 24;
-  const uint32_t DQ_DONE = bar0 + 32, FINAL = bar0 + 40;
-  auto K_FULL = [&](int j) { return bar0 + 48u + 8u * (uint32_t)(j % C::kKSt); };
-  auto K_EMPTY = [&](int j) { return bar0 + 48u + 8u * (uint32_t)(C::kKSt + j % C::kKSt); };
-  auto V_FULL = [&](int j) { return bar0 + 48u + 8u * (uint32_t)(2 * C::kKSt + j % C::kVSt); };
-  auto V_EMPTY = [&](int j) {
-    return bar0 + 48u + 8u * (uint32_t)(2 * C::kKSt + C::kVSt + j % C::kVSt);
-  };
-  auto phK = [&](int j) { return (uint32_t)((j / C::kKSt) & 1); };
-  auto phV = [&](int j) { return (uint32_t)((j / C::kVSt) & 1); };
+  // per stage of K or V (j: number of the pair)
+  auto K_FULL = [&](int j) { return bar0 + 8u * (uint32_t)(j % C::kK); };
+  auto K_EMPTY = [&](int j) { return bar0 + 8u * (uint32_t)(C::kK + j % C::kK); };
+  auto V_FULL = [&](int j) { return bar0 + 8u * (uint32_t)(2 * C::kK + j % C::kV); };
+  auto V_EMPTY = [&](int j) { return bar0 + 8u * (uint32_t)(2 * C::kK + C::kV + j % C::kV); };
+  const uint32_t bar1 = bar0 + 16u * (C::kK + C::kV);
+  // per tile parity (k: number of the tile)
+  auto Q_FULL = [&](int k) { return bar1 + 8u * (uint32_t)(k & 1); };
+  auto Q_EMPTY = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
+  auto DONE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
+  auto ACC_FREE = [&](int k) { return bar1 + 48u + 8u * (uint32_t)(k & 1); };
+  // one phase per pair
+  const uint32_t bar2 = bar1 + 64u;
+  const uint32_t S_FULL = bar2, S_READ = bar2 + 8, DP_FULL = bar2 + 16, DP_READ = bar2 + 24;
+  auto DS_READY = [&](int j) { return bar2 + 32u + 8u * (uint32_t)(j & 1); };
+  const uint32_t FINAL = bar2 + 48;
+  auto ph1 = [](int j) { return (uint32_t)(j & 1); };
+  auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
+  auto phK = [](int j) { return (uint32_t)((j / C::kK) & 1); };
+  auto phV = [](int j) { return (uint32_t)((j / C::kV) & 1); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_SLOT);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(), lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t phase) {
-    mbar_wait(bar, phase, p.spin_ns, p.err, p.err + 1);
+    return mbar_wait_lean(bar, phase, p.spin_ns, p.err);
   };
-  const int BHk = (int)(gridDim.x / (unsigned)p.NT);
-  const int tile = p.NT - 1 - (int)(blockIdx.x / (unsigned)BHk);
-  const int bh = (int)(blockIdx.x % (unsigned)BHk);
-  const int b = bh / p.Hkv, hk = bh % p.Hkv, t0 = tile * p.T;
-  const long long gt = (long long)bh * p.NT + tile;
-  const int n = p.plan.count[gt];
-  const int* units = p.plan.unit + gt * p.U;
-  const int kvlen = p.plan.len[b];
+  // the i-th tile in the order they are taken: K/V head bh, first token t0, plan row gt
+  struct Tile {
+    int bh, b, hk, t0, n;
+    long long gt;
+  };
+  const int BHk = p.tiles / p.NT;
+  auto tile_at = [&](int i) {
+    Tile w;
+    const int y = i / BHk;
+    w.bh = i - y * BHk;
+    w.b = w.bh / p.Hkv, w.hk = w.bh - w.b * p.Hkv;
+    w.t0 = (p.NT - 1 - y) * p.T;
+    w.gt = (long long)w.bh * p.NT + (p.NT - 1 - y);
+    w.n = p.plan.count[w.gt];
+    return w;
+  };
 
   if (threadIdx.x == 0) {
-    mbar_init(Q_FULL, 1);
+    for (int s = 0; s < 2 * (C::kK + C::kV); ++s) mbar_init(bar0 + 8u * s, 1);
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(Q_FULL(k), 1);
+      mbar_init(Q_EMPTY(k), 1);
+      mbar_init(DONE(k), 1);
+      mbar_init(ACC_FREE(k), 16);
+    }
     mbar_init(S_FULL, 1);
+    mbar_init(S_READ, 16);
     mbar_init(DP_FULL, 1);
-    mbar_init(DS_READY, 128);
-    mbar_init(DQ_DONE, 1);
-    mbar_init(FINAL, 1);
-    for (int i = 0; i < 2 * C::kKSt + 2 * C::kVSt; ++i) mbar_init(bar0 + 48u + 8u * i, 1);
+    mbar_init(DP_READ, 16);
+    mbar_init(DS_READY(0), 16);
+    mbar_init(DS_READY(1), 16);
+    mbar_init(FINAL, 2);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -112,195 +189,272 @@ __global__ void __launch_bounds__(192, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // Tiles without a unit take no part in the numbering k of tiles and j of pairs.
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-    mbar_expect_tx(Q_FULL, (uint32_t)(2 * p.G * p.T * D * 2));
+    auto next_tile = [&](int& i, Tile& w) {
+      for (i += gridDim.x; i < p.tiles; i += gridDim.x) {
+        w = tile_at(i);
+        if (w.n > 0) return true;
+      }
+      return false;
+    };
+    bool ok = true;                 // no wait has run out: else nothing more is loaded
+    int nq = 0, nk = 0, nv = 0;     // loads issued
+    // G x T rows of 128 bytes per column half; tokens past Sq arrive as zeros.  Rows G*T to
+    // 127 are never written: each row's result stays in its own row
+    auto load_q = [&](const Tile& w, int k) {
+      if (k >= C::kQ) ok = ok && wait(Q_EMPTY(k - C::kQ), ph2(k - C::kQ));
+      if (!ok) return;
+      mbar_expect_tx(Q_FULL(k), (uint32_t)(2 * p.G * p.T * D * 2));
 #pragma unroll
-    for (int cb = 0; cb < D / 64; ++cb) {
-      tma_load_4d(sQ + cb * 16384, &tmQ, cb * 64, t0, hk * p.G, b, Q_FULL);
-      tma_load_4d(sDO + cb * 16384, &tmDO, cb * 64, t0, hk * p.G, b, Q_FULL);
-    }
-    int u = n > 0 ? units[0] : 0;
-    for (int j = 0; j < n; ++j) {
-      const int next = j + 1 < n ? units[j + 1] : 0;
-      if (j >= C::kKSt) wait(K_EMPTY(j), phK(j - C::kKSt));
-      mbar_expect_tx(K_FULL(j), C::kKV);
+      for (int cb = 0; cb < D / 64; ++cb) {
+        tma_load_4d(sQ(k) + cb * 16384, &tmQ, cb * 64, w.hk * p.G, w.t0, w.b, Q_FULL(k));
+        tma_load_4d(sDO(k) + cb * 16384, &tmDO, cb * 64, w.hk * p.G, w.t0, w.b, Q_FULL(k));
+      }
+      nq = k + 1;
+    };
+    auto load_pair = [&](uint32_t dst, const CUtensorMap* map, int u0, int u1, const Tile& w,
+                         uint32_t bar) {
+      mbar_expect_tx(bar, C::kPair);
 #pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb)
-        tma_load_4d(sK + (j % C::kKSt) * C::kKV + cb * 8192, &tmK, cb * 64, u * kUnit, hk, b,
-                    K_FULL(j));
-      if (j >= C::kVSt) wait(V_EMPTY(j), phV(j - C::kVSt));
-      mbar_expect_tx(V_FULL(j), C::kKV);
-#pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb)
-        tma_load_4d(sV + (j % C::kVSt) * C::kKV + cb * 8192, &tmV, cb * 64, u * kUnit, hk, b,
-                    V_FULL(j));
-      u = next;
+      for (int cb = 0; cb < D / 64; ++cb) {
+        tma_load_4d(dst + cb * 16384, map, cb * 64, u0 * kUnit, w.hk, w.b, bar);
+        tma_load_4d(dst + cb * 16384 + 8192, map, cb * 64, u1 * kUnit, w.hk, w.b, bar);
+      }
+    };
+    const int none = (p.Sk + kUnit - 1) / kUnit;  // past the keys: zeros
+    int i = (int)blockIdx.x - (int)gridDim.x, k = 0, j = 0;
+    Tile w, nw;
+    bool on = next_tile(i, w);
+    if (on && C::kQ == 2) load_q(w, 0);
+    while (on) {
+      const int* units = p.plan.unit + w.gt * p.U;
+      const bool more = next_tile(i, nw);
+      int u0 = units[0], u1 = w.n > 1 ? units[1] : none;
+      for (int e = 0; e < w.n; e += 2, ++j) {
+        const int n0 = e + 2 < w.n ? units[e + 2] : none, n1 = e + 3 < w.n ? units[e + 3] : none;
+        if (j >= C::kK) ok = ok && wait(K_EMPTY(j), phK(j - C::kK));
+        if (ok) load_pair(sK(j), &tmK, u0, u1, w, K_FULL(j)), nk = j + 1;
+        if (j >= C::kV) ok = ok && wait(V_EMPTY(j), phV(j - C::kV));
+        if (!ok) break;
+        load_pair(sV(j), &tmV, u0, u1, w, V_FULL(j));
+        nv = j + 1;
+        u0 = n0, u1 = n1;
+        if (C::kQ == 1 && e == 0) load_q(w, k);
+        if (C::kQ == 2 && more && (e == 2 || (e == 0 && w.n <= 2))) load_q(nw, k + 1);
+      }
+      w = nw;
+      on = more && ok;
+      ++k;
     }
     // no load may land after the CTA has gone, not even when a wait ran out
-    mbar_wait_drain(Q_FULL, 0, p.spin_ns, p.err, p.err + 1);
-    for (int j = max(0, n - 2); j < n; ++j) {
-      mbar_wait_drain(K_FULL(j), phK(j), p.spin_ns, p.err, p.err + 1);
-      if (j >= n - C::kVSt) mbar_wait_drain(V_FULL(j), phV(j), p.spin_ns, p.err, p.err + 1);
-    }
-  } else if (warp == 1 && lane == 0) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);  // S, dP
-    constexpr uint32_t ID_Q = idesc_bf16_f32(128, D, 0, 1);      // dQ, K MN-major
+    for (int x = max(0, nq - C::kQ); x < nq; ++x)
+      mbar_wait_drain(Q_FULL(x), ph2(x), p.spin_ns, p.err, p.err + 1);
+    for (int x = max(0, nk - C::kK); x < nk; ++x)
+      mbar_wait_drain(K_FULL(x), phK(x), p.spin_ns, p.err, p.err + 1);
+    for (int x = max(0, nv - C::kV); x < nv; ++x)
+      mbar_wait_drain(V_FULL(x), phV(x), p.spin_ns, p.err, p.err + 1);
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------------------------------- product issuers
+    // Two of them, S and dP and beside them dQ: one thread's instructions take longer than
+    // the products it issues.  The whole warp walks the loop, one lane issues
+    const bool leader = elect_one();
     const uint32_t hi = sdesc_hi(1024);
-    const uint32_t kQ = sdesc_lo(sQ, 16), kDO = sdesc_lo(sDO, 16);
-    const uint32_t tS = tmem + C::TM_S, tDP = tmem + C::TM_DP, tDQ = tmem + C::TM_DQ;
-    // dS_i lies packed in dP's columns
-    auto issue_dq = [&](int i) {
-      const uint32_t mK = sdesc_lo(sK + (i % C::kKSt) * C::kKV, 8192);
-#pragma unroll
-      for (int kk = 0; kk < kUnit / 16; ++kk)
-        tc_mma_ts_w(tDQ, tDP + 32 * (kk >> 1) + 8 * (kk & 1), mK + kk * 128, hi, ID_Q,
-                    (i > 0 || kk > 0) ? 1u : 0u);
-      tc_commit(K_EMPTY(i));
-      tc_commit(DQ_DONE);
-    };
-    if (n > 0) wait(Q_FULL, 0);
-    for (int j = 0; j < n; ++j) {
-      const uint32_t kK = sdesc_lo(sK + (j % C::kKSt) * C::kKV, 16);
-      const uint32_t kV = sdesc_lo(sV + (j % C::kVSt) * C::kKV, 16);
-      wait(K_FULL(j), phK(j));
-      if (j > 0) wait(DS_READY, (uint32_t)((j - 1) & 1));  // S_{j-1} and dP_{j-1} are read
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                    kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                    kk > 0 ? 1u : 0u);
-      tc_commit(S_FULL);
-      if (j > 0) {
-        issue_dq(j - 1);
-        wait(DQ_DONE, (uint32_t)((j - 1) & 1));  // dP_j overwrites dS_{j-1}
-      }
-      wait(V_FULL(j), phV(j));
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        tc_mma_ss_w(tDP, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                    kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                    kk > 0 ? 1u : 0u);
-      tc_commit(V_EMPTY(j));
-      tc_commit(DP_FULL);
-    }
-    if (n > 0) {
-      wait(DS_READY, (uint32_t)((n - 1) & 1));
-      tc_fence_after();
-      issue_dq(n - 1);
-    }
-    tc_commit(FINAL);
-    mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
-  } else if (warp >= 2) {
-    // ---------------------------------------------------------------- softmax gradient
-    const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;
-    const int g = r / p.T, t = r - g * p.T, token = t0 + t;
-    const bool valid = g < p.G && token < p.Sq;
-    const long long row = ((long long)b * p.H + hk * p.G + g) * p.Sq + token;
-    const long long pos = (long long)p.plan.start[b] + token;
-    const int limit = !valid ? 0
-                      : p.causal ? (int)min((long long)kvlen, max(pos + 1, 0ll)) : kvlen;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::TM_S, tDP = tmem + lane_off + C::TM_DP;
-    const float sl2 = p.scale_log2;
-    const uint32_t* masks = p.plan.mask + gt * p.U * p.W + min(t >> 5, p.W - 1);
-    const int bit = t & 31;
-    const float lse2 = valid ? p.lse[row] * 1.4426950408889634f : 0.f;
-    // delta: dO from shared memory (16-byte pieces, swizzled by row), O from memory
-    float delta = 0.f;
-    wait(Q_FULL, 0);
-    if (valid) {
-      const uint4* orow = reinterpret_cast<const uint4*>(p.o + row * D);
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = orow[c];
-        const float4 y = ld_shared_f4(sDO + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-        const uint32_t ys[4] = {__float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z),
-                                __float_as_uint(y.w)};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          delta = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), delta);
-          delta = fmaf(__uint_as_float(xs[k] & 0xffff0000u),
-                       __uint_as_float(ys[k] & 0xffff0000u), delta);
-        }
-      }
-      p.delta[row] = delta;
-    }
-    int u = n > 0 ? units[0] : 0;
-    uint32_t word = n > 0 ? masks[0] : 0u;
-    for (int j = 0; j < n; ++j) {
-      const int base = u * kUnit;
-      const int vis = ((word >> bit) & 1u) ? limit - base : 0;
-      if (j + 1 < n) {
-        u = units[j + 1];
-        word = masks[(long long)(j + 1) * p.W];
-      }
-      wait(S_FULL, (uint32_t)(j & 1));
-      tc_fence_after();
-      uint32_t sv[2][32];
-      tmem_ld32x2(tS, tS + 32, sv[0], sv[1]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          sv[c][k] = __float_as_uint(
-              32 * c + k < vis ? ex2_approx(__uint_as_float(sv[c][k]) * sl2 - lse2) : 0.f);
-      wait(DP_FULL, (uint32_t)(j & 1));
-      tc_fence_after();
-      if (base + kUnit > kvlen && kvlen < p.Sk) {
-        // K rows past the sequence hold whatever the cache holds: 0 * NaN would reach dQ
-        const int first = kvlen - base;
-        const uint32_t sKj = sK + (j % C::kKSt) * C::kKV;
-        for (int x = r; x < (kUnit - first) * (D / 8); x += 128) {
-          const int kr = first + x / (D / 8), c = x % (D / 8);
-          st_shared_v4(sKj + (c >> 3) * 8192 + kr * 128 + (c & 7) * 16, 0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t dp[32], pk[16];
-        tmem_ld32(tDP + 32 * c, dp);
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          // selected, not multiplied: dP of a masked key may be anything
-          const float d0 = 32 * c + k < vis
-                               ? __uint_as_float(sv[c][k]) * (__uint_as_float(dp[k]) - delta) : 0.f;
-          const float d1 = 32 * c + k + 1 < vis
-                               ? __uint_as_float(sv[c][k + 1]) * (__uint_as_float(dp[k + 1]) - delta)
-                               : 0.f;
-          pk[k >> 1] = pack_bf16x2(d0, d1);
-        }
-        tmem_st16(tDP + 32 * c, pk);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(DS_READY);
-    }
-    wait(FINAL, 0);
-    tc_fence_after();
-    const uint32_t tDQ = tmem + lane_off + C::TM_DQ;
+    bool ok = true;  // no wait has run out: else no more products
+    int k = 0, j = 0, ks = 0, vs = 0;  // ks, vs: stages of K and V
+    uint32_t kph = 0, vph = 0;
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t ov[32];
-      tmem_ld32(tDQ + 32 * c, ov);
-      if (!valid) continue;
-      const float f = n > 0 ? p.scale : 0.f;
-      float x[32];
+    for (int i = blockIdx.x; i < p.tiles && ok; i += gridDim.x) {
+      const int y = i / BHk;
+      const int n = p.plan.count[(long long)(i - y * BHk) * p.NT + (p.NT - 1 - y)];
+      if (n == 0) continue;
+      if (warp == 1) {
+        constexpr uint32_t ID_S = idesc_bf16_f32(128, 2 * kUnit, 0, 0);
+        const uint32_t kQ = sdesc_lo(sQ(k), 16), kDO = sdesc_lo(sDO(k), 16);
+        ok = wait(Q_FULL(k), ph2(k));
+#pragma unroll 1
+        for (int e = 0; e < n && ok; e += 2, ++j) {
+          const uint32_t kK = sdesc_lo(sb + C::OFF_K + ks * C::kPair, 16);
+          const uint32_t kV = sdesc_lo(sb + C::OFF_V + vs * C::kPair, 16);
+          ok = wait(bar0 + 8u * ks, kph) && (j == 0 || wait(S_READ, ph1(j - 1)));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) x[k] = n > 0 ? __uint_as_float(ov[k]) * f : 0.f;
-      uint4* out = reinterpret_cast<uint4*>(p.dq + row * D + 32 * c);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              tc_mma_ss_w(tmem + C::TM_S, kQ + at, kK + at, hi, ID_S, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(S_FULL);
+          }
+          ok = wait(bar0 + 8u * (2 * C::kK + vs), vph) && (j == 0 || wait(DP_READ, ph1(j - 1)));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        out[k] = make_uint4(pack_bf16x2(x[8 * k], x[8 * k + 1]),
-                            pack_bf16x2(x[8 * k + 2], x[8 * k + 3]),
-                            pack_bf16x2(x[8 * k + 4], x[8 * k + 5]),
-                            pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+              tc_mma_ss_w(tmem + C::TM_DP, kDO + at, kV + at, hi, ID_S, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(DP_FULL);
+            tc_commit(bar0 + 8u * (2 * C::kK + C::kV + vs));  // V_EMPTY
+            if (e + 2 >= n) tc_commit(Q_EMPTY(k));
+          }
+          if (++ks == C::kK) ks = 0, kph ^= 1u;
+          if (++vs == C::kV) vs = 0, vph ^= 1u;
+        }
+      } else {
+        constexpr uint32_t ID_Q = idesc_bf16_f32(128, D, 0, 1);  // K MN-major
+        const uint32_t tDQ = tmem + C::TM_DQ + (uint32_t)(D * (k % C::kAcc));
+        // the accumulator's last tile must have been read
+        if (k >= C::kAcc) ok = wait(ACC_FREE(k - C::kAcc), ph2(k - C::kAcc));
+#pragma unroll 1
+        for (int e = 0; e < n && ok; e += 2, ++j) {
+          const uint32_t mK = sdesc_lo(sb + C::OFF_K + ks * C::kPair, 16384);
+          const uint32_t tDS = tmem + C::TM_DS + 64u * (uint32_t)(j & 1);
+          ok = wait(DS_READY(j), ph2(j));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 2 * kUnit / 16; ++kk)
+              tc_mma_ts_w(tDQ, tDS + 8 * kk, mK + kk * 128, hi, ID_Q, (uint32_t)(e + kk));
+            tc_commit(bar0 + 8u * (C::kK + ks));  // K_EMPTY
+            if (e + 2 >= n) tc_commit(DONE(k));
+          }
+          if (++ks == C::kK) ks = 0;
+        }
+      }
+      ++k;
+    }
+    if (leader) tc_commit(FINAL);  // the CTA does not go before its products
+    mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- softmax gradient
+    // warpgroup wg takes keys 32 half to 32 half + 31 of the pair's unit h
+    const int wg = (warp - 4) >> 2, h = wg >> 1, half = wg & 1, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const int t = r / p.G, g = r - t * p.G;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const float sl2 = p.scale_log2;
+    const int bit = t & 31, wsel = min(t >> 5, p.W - 1);
+    int j = 0, k = 0;
+    for (int i = blockIdx.x; i < p.tiles; i += gridDim.x) {
+      const Tile w = tile_at(i);
+      const int token = w.t0 + t;
+      const bool valid = t < p.T && token < p.Sq;
+      __nv_bfloat16* out =
+          p.dq + (((long long)w.bh * p.G + g) * p.Sq + token) * D + wg * (D / 4);
+      if (w.n == 0) {
+        if (valid)
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x)
+            reinterpret_cast<uint4*>(out)[x] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const int kvlen = p.plan.len[w.b];
+      const long long pos = (long long)p.plan.start[w.b] + token;
+      const int limit = !valid ? 0
+                        : p.causal ? (int)min((long long)kvlen, max(pos + 1, 0ll)) : kvlen;
+      const int* units = p.plan.unit + w.gt * p.U;
+      const uint32_t* masks = p.plan.mask + w.gt * p.U * p.W + wsel;
+      int u = 0;
+      uint32_t word = 0u;  // nobody picks the missing half of an odd list's last pair
+      if (h < w.n) u = units[h], word = masks[(long long)h * p.W];
+      const long long row = ((long long)w.bh * p.G + g) * p.Sq + token;
+      const float lse2 = valid ? p.lse[row] * 1.4426950408889634f : 0.f;
+      const float delta = valid ? p.delta[row] : 0.f;
+      for (int e = h; e < w.n + h; e += 2, ++j) {
+        const int base = u * kUnit;
+        const int v = ((word >> bit) & 1u) ? limit - base - 32 * half : 0;  // keys below it count
+        const bool partial = half == 0 && e < w.n && base + kUnit > kvlen && kvlen < p.Sk;
+        word = 0u;
+        if (e + 2 < w.n) {
+          u = units[e + 2];
+          word = masks[(long long)(e + 2) * p.W];
+        }
+        const bool any = __any_sync(0xffffffffu, v > 0);
+        const bool clean = __all_sync(0xffffffffu, v >= 32 || v <= 0);
+        const uint32_t keep = v > 0 ? 0xffffffffu : 0u;
+        const uint32_t tS = tmem + lane_off + C::TM_S + 32u * wg, tDP = tS + 128;
+        const uint32_t tDS = tmem + lane_off + C::TM_DS + 64u * (uint32_t)(j & 1) + 16u * wg;
+        float pr[32];
+        wait(S_FULL, ph1(j));
+        tc_fence_after();
+        if (any) {
+          uint32_t sv[32];
+          tmem_ld32(tS, sv);
+          tc_fence_before();
+          warp_arrive(S_READ, lane);
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            fma_f32x2(pr[x], pr[x + 1], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), sl2,
+                      -lse2);
+            pr[x] = ex2_approx(pr[x]);
+            pr[x + 1] = ex2_approx(pr[x + 1]);
+          }
+        } else {
+          warp_arrive(S_READ, lane);
+        }
+        if (partial) {
+          // K rows past the sequence hold whatever the cache holds: 0 * NaN would reach dQ
+          const int first = max(kvlen - base, 0);
+          for (int x = r; x < (kUnit - first) * (D / 8); x += 128) {
+            const int kr = first + x / (D / 8), c = x % (D / 8);
+            st_shared_v4(sK(j) + (c >> 3) * 16384 + h * 8192 + kr * 128 + (c & 7) * 16, 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (j >= 2) wait(K_EMPTY(j - 2), phK(j - 2));  // dS of pair j - 2 has been used
+        wait(DP_FULL, ph1(j));
+        tc_fence_after();
+        if (any) {
+          uint32_t dp[32], pk[16];
+          tmem_ld32(tDP, dp);
+          tc_fence_before();
+          warp_arrive(DP_READ, lane);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float d0, d1;
+            add_f32x2(d0, d1, __uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), -delta);
+            mul_f32x2(d0, d1, pr[2 * x], pr[2 * x + 1], d0, d1);
+            if (!clean) {  // selected, not multiplied: S and dP of a masked key may be anything
+              if (2 * x >= v) d0 = 0.f;
+              if (2 * x + 1 >= v) d1 = 0.f;
+            }
+            pk[x] = pack_bf16x2(d0, d1) & keep;
+          }
+          tmem_st16(tDS, pk);
+        } else {
+          warp_arrive(DP_READ, lane);
+          const uint32_t zero[16] = {};
+          tmem_st16(tDS, zero);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(DS_READY(j), lane);
+      }
+      wait(DONE(k), ph2(k));
+      tc_fence_after();
+      const uint32_t tDQ =
+          tmem + lane_off + C::TM_DQ + (uint32_t)(D * (k % C::kAcc) + wg * (D / 4));
+      uint32_t ov[D / 4];
+      if constexpr (D == 128) tmem_ld32(tDQ, ov);
+      else tmem_ld16(tDQ, ov);
+      tc_fence_before();
+      warp_arrive(ACC_FREE(k), lane);
+      if (valid) {
+        auto val = [&](int x) { return __uint_as_float(ov[x]) * p.scale; };
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q)
+          reinterpret_cast<uint4*>(out)[q] =
+              make_uint4(pack_bf16x2(val(8 * q), val(8 * q + 1)),
+                         pack_bf16x2(val(8 * q + 2), val(8 * q + 3)),
+                         pack_bf16x2(val(8 * q + 4), val(8 * q + 5)),
+                         pack_bf16x2(val(8 * q + 6), val(8 * q + 7)));
+      }
+      ++k;
     }
   }
   tc_fence_before();
@@ -479,7 +633,7 @@ struct SparseDkvParams {
 
 template <int D>
 struct SparseDkvCfg {
-  static constexpr int kThreads = 640;  // Q rows, dO rows (4 warps each), MMA, K/V, 8 softmax
+  static constexpr int kThreads = 640;  // Q rows, dO rows (4 warps each), S and dP, K/V, dV and dK, -, 8 softmax
   static constexpr int kTile = kTileRows * D * 2;
   static constexpr int kKV = kUnit * D * 2;
   static constexpr int kP = kTileRows * kUnit * 2;  // [128][64] bf16
@@ -488,7 +642,7 @@ struct SparseDkvCfg {
   static constexpr int OFF_KV = kStages * 2 * kTile;  // two of K, then V
   static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS
   static constexpr int OFF_BAR = OFF_P + 2 * kP;
-  static constexpr int kBars = 4 * kStages + 6 + 4;
+  static constexpr int kBars = 4 * kStages + 6 + 7;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
@@ -536,13 +690,14 @@ __global__ void __launch_bounds__(640, 1)
   auto ITEM_DONE = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
   auto SDP_FULL = [&](int j) { return bar1 + 48u + 8u * (uint32_t)(j & 1); };
-  const uint32_t PDS_READY = bar1 + 64, PDS_FREE = bar1 + 72;
+  const uint32_t PDS_READY = bar1 + 64, PDS_FREE = bar1 + 72, FINAL = bar1 + 96;
+  auto SDP_READ = [&](int j) { return bar1 + 80u + 8u * (uint32_t)(j & 1); };
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phS = [](int j) { return (uint32_t)((j / ST) & 1); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_SLOT);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(), lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t phase) {
-    mbar_wait(bar, phase, p.spin_ns, p.err, p.err + 1);
+    return mbar_wait_lean(bar, phase, p.spin_ns, p.err);
   };
   const int items = p.head[0];
   const uint32_t inv_g = (65536u + p.G - 1) / p.G;  // row / G = row * inv_g >> 16 for row < 128
@@ -551,17 +706,19 @@ __global__ void __launch_bounds__(640, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s)
       for (int x = 0; x < 2; ++x) {
-        mbar_init(FULL(x, s), 128);
+        mbar_init(FULL(x, s), 4);
         mbar_init(EMPTY(x, s), 1);
       }
     for (int k = 0; k < 2; ++k) {
       mbar_init(KV_FULL(k), 1);
       mbar_init(ITEM_DONE(k), 1);
-      mbar_init(ACC_FREE(k), 256);
+      mbar_init(ACC_FREE(k), 8);
       mbar_init(SDP_FULL(k), 1);
+      mbar_init(SDP_READ(k), 8);
     }
-    mbar_init(PDS_READY, 256);
+    mbar_init(PDS_READY, 8);
     mbar_init(PDS_FREE, 1);
+    mbar_init(FINAL, 2);
     fence_mbar_init();
   }
   // rows G*T to 127 of a stage are never loaded, but the products sum over all 128 rows
@@ -627,7 +784,7 @@ __global__ void __launch_bounds__(640, 1)
         }
         cp_async_wait_all();
         fence_proxy_async_smem();
-        mbar_arrive(FULL(x, s));
+        warp_arrive(FULL(x, s), lane);
       }
       w = nw;
     }
@@ -637,7 +794,8 @@ __global__ void __launch_bounds__(640, 1)
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
       const SparseItem w = p.item[i];
       const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
-      if (k >= 2) wait(ITEM_DONE(k), ph2(k - 2));  // K and V of item k - 2 are read to the end
+      // K and V of item k - 2 are read to the end; nothing is loaded once a wait has run out
+      if (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2))) break;
       mbar_expect_tx(KV_FULL(k), 2 * C::kKV);
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb) {
@@ -648,95 +806,80 @@ __global__ void __launch_bounds__(640, 1)
     // no load may land after the CTA has gone, not even when a wait ran out
     for (int j = max(0, k - 2); j < k; ++j)
       mbar_wait_drain(KV_FULL(j), ph2(j), p.spin_ns, p.err, p.err + 1);
-  } else if (warp == 8 && lane == 0) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
-    constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
+  } else if (warp == 8 || warp == 10) {
+    // ---------------------------------------------------------------- product issuers
+    // Two of them, S and dP and beside them dV and dK (see the dQ kernel)
+    const bool leader = elect_one();
     const uint32_t hi = sdesc_hi(1024);
-    const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384);
-    // two cursors over the CTA's tiles: S and dP run up to two tiles ahead of dV and dK
-    struct Cursor {
-      int i, k, e, first, end, j;  // item, its number, tile, the item's tiles, tile number
-      bool on;
-    };
-    auto open = [&](Cursor& c) {
-      c.on = c.i < items;
-      if (c.on) c.first = c.e = p.item[c.i].first, c.end = p.item[c.i].end;
-    };
-    auto step = [&](Cursor& c) {
-      ++c.j;
-      if (++c.e == c.end) c.i += gridDim.x, ++c.k, open(c);
-    };
-    Cursor a{(int)blockIdx.x, 0, 0, 0, 0, 0, false};
-    open(a);
-    Cursor d = a;
-    int last = -1;  // the last item's number
-    uint64_t since = 0;
-    bool given_up = false;
-    while (d.on) {
-      bool did = false;
-      if (a.on && a.j <= d.j + 1 && (given_up || (mbar_test_wait(FULL(0, a.j % ST), phS(a.j)) &&
-                                                  mbar_test_wait(FULL(1, a.j % ST), phS(a.j)) &&
-                                                  mbar_test_wait(KV_FULL(a.k), ph2(a.k))))) {
-        // S and dP of tile j - 2 were read before its P and dS were ready
-        const int s = a.j % ST;
-        const uint32_t kQ = sdesc_lo(sQ(s), 16), kDO = sdesc_lo(sDO(s), 16);
-        const uint32_t kK = sdesc_lo(sK(a.k), 16), kV = sdesc_lo(sV(a.k), 16);
-        const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(a.j & 1);
-        tc_fence_after();
+    bool ok = true;  // no wait has run out: else no more products
+    int j = 0, k = 0, s = 0;
+    uint32_t sph = 0;
+#pragma unroll 1
+    for (int i = blockIdx.x; i < items && ok; i += gridDim.x, ++k) {
+      const int first = p.item[i].first, end = p.item[i].end;
+      if (warp == 8) {
+        constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
+        const uint32_t kK = sdesc_lo(sK(k), 16), kV = sdesc_lo(sV(k), 16);
+        ok = wait(KV_FULL(k), ph2(k));
+#pragma unroll 1
+        for (int e = first; e < end && ok; ++e, ++j) {
+          const uint32_t kQ = sdesc_lo(sQ(s), 16), kDO = sdesc_lo(sDO(s), 16);
+          const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(j & 1);
+          ok = wait(FULL(0, s), sph) && (j < 2 || wait(SDP_READ(j), ph2(j - 2)));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                      kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                      kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                          kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                          kk > 0 ? 1u : 0u);
+          ok = wait(FULL(1, s), sph);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                      kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                      kk > 0 ? 1u : 0u);
-        tc_commit(SDP_FULL(a.j));
-        step(a);
-        did = true;
-      }
-      if (d.j < a.j && (given_up || mbar_test_wait(PDS_READY, (uint32_t)(d.j & 1)))) {
-        const int s = d.j % ST;
-        const bool first = d.e == d.first;
-        // the accumulators of item k - 2 must have been read
-        if (first && d.k >= 2) wait(ACC_FREE(d.k), ph2(d.k - 2));
-        const uint32_t aV = sdesc_lo(sDO(s), 16384);
-        const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
-        const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(d.k & 1);
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (!first || kk > 0) ? 1u : 0u);
-        if (D == 128) tc_commit(EMPTY(1, s));
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
-                      (!first || kk > 0) ? 1u : 0u);
-        if (D == 64) tc_commit(EMPTY(1, s));
-        tc_commit(EMPTY(0, s));
-        tc_commit(PDS_FREE);
-        last = d.k;
-        if (d.e + 1 == d.end) tc_commit(ITEM_DONE(d.k));
-        step(d);
-        did = true;
-      }
-      if (did) {
-        since = 0;
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                          kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                          kk > 0 ? 1u : 0u);
+            tc_commit(SDP_FULL(j));
+          }
+          if (++s == ST) s = 0, sph ^= 1u;
+        }
       } else {
-        const uint64_t now = globaltimer();
-        if (since == 0) {
-          since = now;
-        } else if (now - since > p.spin_ns || aborted(p.err + 1)) {
-          // go on without waiting, so that every other wait of the CTA ends
-          if (!given_up) raise_timeout(p.err, p.err + 1, ERR_WHERE_PIPE);
-          given_up = true;
+        constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
+        const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384);
+        const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
+        // the accumulators of item k - 2 must have been read
+        if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
+#pragma unroll 1
+        for (int e = first; e < end && ok; ++e, ++j) {
+          const uint32_t aV = sdesc_lo(sDO(s), 16384);
+          const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
+          ok = wait(PDS_READY, (uint32_t)(j & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (uint32_t)(e - first + kk));
+            if (D == 128) tc_commit(EMPTY(1, s));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
+                          (uint32_t)(e - first + kk));
+            if (D == 64) tc_commit(EMPTY(1, s));
+            tc_commit(EMPTY(0, s));
+            tc_commit(PDS_FREE);
+            if (e + 1 == end) tc_commit(ITEM_DONE(k));
+          }
+          if (++s == ST) s = 0;
         }
       }
     }
-    if (last >= 0) mbar_wait_drain(ITEM_DONE(last), ph2(last), p.spin_ns, p.err, p.err + 1);
+    if (leader) tc_commit(FINAL);  // the CTA does not go before its products
+    mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
   } else if (warp >= 12) {
     // ---------------------------------------------------------------- softmax gradient
     const int wg = (warp - 12) >> 2, quarter = warp & 3;
@@ -788,6 +931,10 @@ __global__ void __launch_bounds__(640, 1)
           tmem_ld16_async(tS + 16 * h, sv);
           tmem_ld16_async(tS + 64 + 16 * h, dp);
           tmem_wait_ld();
+          if (h == 1) {
+            tc_fence_before();
+            warp_arrive(SDP_READ(it), lane);
+          }
           uint32_t pp[8], ds[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
@@ -814,7 +961,7 @@ __global__ void __launch_bounds__(640, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(PDS_READY);
+        warp_arrive(PDS_READY, lane);
       }
       // epilogue: warpgroup 0 writes dV, warpgroup 1 dK; lane = head dimension, column = key
       wait(ITEM_DONE(k), ph2(k));
@@ -830,7 +977,7 @@ __global__ void __launch_bounds__(640, 1)
         tmem_ld32(ta + 32 * c, acc);
         if (c == 1) {
           tc_fence_before();
-          mbar_arrive(ACC_FREE(k));
+          warp_arrive(ACC_FREE(k), lane);
         }
         if (d < 0 || d >= D) continue;
         if (w.slot >= 0) {

@@ -112,3 +112,34 @@ def test_forward_without_a_plan(shape):
     o, lse = run_fwd(c)
     check_fwd(c, o, lse)
     assert dash.dash_attn_sync_status() == 0
+
+
+LARGE = [
+    # more query tiles than SMs, lists of odd and even length, tiles without a unit
+    (2, 8, 4, 3001, 3001, 128, 64, 5, True, False),
+    (3, 4, 4, 6400, 6500, 64, 128, 3, True, True),
+    (1, 3, 1, 9000, 300, 64, 64, 1, False, False),
+]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_many_tiles_of_a_cta(shape):
+    c = case(*shape[:9], ragged=shape[9], seed=7)
+    if shape[3] % 2 == 0:
+        c["idx"][:, 1:, 1000:1700] = -1
+    plan = make_plan(c)
+    o, lse = run_fwd(c, plan=plan)
+    grads = dash.dash_attn_sparse_bwd(c["q"], c["k"], c["v"], o, c["do"], lse, plan)
+    assert dash.dash_attn_sync_status() == 0
+    m = ref_mask(c)
+    got = dict(o=o, lse=lse, dq=grads[0], dk=grads[1], dv=grads[2])
+    G = shape[1] // shape[2]
+    for b in range(shape[0]):  # the 64-bit form, a K/V head at a time
+        for h in range(shape[2]):
+            hs = slice(h * G, h * G + G)
+            one = dict(q=c["q"][b:b + 1, hs], k=c["k"][b:b + 1, h:h + 1], v=c["v"][b:b + 1, h:h + 1],
+                       do=c["do"][b:b + 1, hs])
+            mm = m[b:b + 1, h:h + 1]
+            check_fwd(one, o[b:b + 1, hs], lse[b:b + 1, hs], mm)
+            check_bwd(one, o[b:b + 1, hs], lse[b:b + 1, hs],
+                      (got["dq"][b:b + 1, hs], got["dk"][b:b + 1, h:h + 1], got["dv"][b:b + 1, h:h + 1]), mm)
