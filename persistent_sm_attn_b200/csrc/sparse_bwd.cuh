@@ -75,34 +75,36 @@ struct SparseDqParams {
 
 template <int D>
 struct SparseDqCfg {
-  static constexpr int kThreads = 640;  // TMA, S and dP, dQ, -, 16 warps of softmax
+  static constexpr int kThreads = 384;  // TMA, S and dP of either stream, dQ, 8 warps of softmax
   static constexpr int kTile = kTileRows * D * 2;
-  static constexpr int kPair = 2 * kUnit * D * 2;
-  // tiles of Q and dO, pairs of K and of V: K is read twice and stays longer than V
-  static constexpr int kQ = D == 128 ? 1 : 2, kK = D == 128 ? 3 : 4, kV = D == 128 ? 2 : 4;
+  static constexpr int kKV = kUnit * D * 2;
+  // tiles of Q and dO, units of K and of V (even: a stage belongs to one stream): K is read
+  // twice and stays longer than V
+  static constexpr int kQ = D == 128 ? 1 : 2, kK = D == 128 ? 6 : 8, kV = D == 128 ? 4 : 8;
   static constexpr int OFF_Q = 0;  // Q, then dO
   static constexpr int OFF_K = kQ * 2 * kTile;
-  static constexpr int OFF_V = OFF_K + kK * kPair;
-  static constexpr int OFF_BAR = OFF_V + kV * kPair;
-  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 7;
+  static constexpr int OFF_V = OFF_K + kK * kKV;
+  static constexpr int OFF_BAR = OFF_V + kV * kKV;
+  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 2 * 4 + 4 + 1;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
   static_assert(kSmemBytes > 116 * 1024, "one CTA per SM: its 512 TMEM columns are free");
   static constexpr int kAcc = D == 128 ? 1 : 2;  // accumulators
-  static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DS = 256, TM_DQ = 384, kTmemCols = 512;
+  static constexpr uint32_t TM_S = 0, TM_DS = 256, TM_DQ = 384, kTmemCols = 512;
 };
 
 // A persistent CTA per SM takes query tiles, those with the longest lists (the last, under a
-// causal mask) first, and walks a tile's list in pairs of units: S = Q K^T, dP = dO V^T
-// (128 x 128, TMEM), dS in bf16 to TMEM, dQ += dS K.  A product of 128 keys reads a third less
-// shared memory a key than one of 64, which it would be bound by.  Four softmax warpgroups take
-// 32 keys of the pair each.  S and dP have a buffer each, free again as soon as they are read: the
-// next S runs under this pair's exponentials, the next dP and this dQ under the next pair's.
-// Row t G + g of a tile is token t, head g, so a warp holds few tokens and skips the
-// exponentials of units that none of them picked.
+// causal mask) first.  Per listed unit j: S = Q K^T, dP = dO V^T (128 x 64, TMEM), dS in bf16
+// to TMEM, dQ += dS K.  Even and odd units are two streams, each with its buffers, its issuer
+// of S and dP and its softmax warpgroup, so that one stream's exponentials run beside the
+// other's dS; S and dP are free again as soon as they are read.  (One stream of 128-key
+// products, both warpgroups on the same pair, measured 231 us at 16 heads of 8k, D = 128, 16
+// picks of 64, and 408 us at 8 heads of 16k, D = 64, 8 picks of 128: exponentials and the
+// rest took turns.)  Row t G + g of a tile is token t, head g, so a warp holds few tokens and
+// skips the exponentials of units that none of them picked.
 template <int D>
-__global__ void __launch_bounds__(640, 1)
+__global__ void __launch_bounds__(384, 1)
     dash_sparse_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmDO,
                           const __grid_constant__ CUtensorMap tmK,
@@ -118,10 +120,10 @@ __global__ void __launch_bounds__(640, 1)
   }
   auto sQ = [&](int k) { return sb + C::OFF_Q + (uint32_t)((k % C::kQ) * 2 * C::kTile); };
   auto sDO = [&](int k) { return sQ(k) + C::kTile; };
-  auto sK = [&](int j) { return sb + C::OFF_K + (uint32_t)((j % C::kK) * C::kPair); };
-  auto sV = [&](int j) { return sb + C::OFF_V + (uint32_t)((j % C::kV) * C::kPair); };
+  auto sK = [&](int j) { return sb + C::OFF_K + (uint32_t)((j % C::kK) * C::kKV); };
+  auto sV = [&](int j) { return sb + C::OFF_V + (uint32_t)((j % C::kV) * C::kKV); };
   const uint32_t bar0 = sb + C::OFF_BAR;
-  // per stage of K or V (j: number of the pair)
+  // per stage of K or V (j: number of the unit)
   auto K_FULL = [&](int j) { return bar0 + 8u * (uint32_t)(j % C::kK); };
   auto K_EMPTY = [&](int j) { return bar0 + 8u * (uint32_t)(C::kK + j % C::kK); };
   auto V_FULL = [&](int j) { return bar0 + 8u * (uint32_t)(2 * C::kK + j % C::kV); };
@@ -132,12 +134,15 @@ __global__ void __launch_bounds__(640, 1)
   auto Q_EMPTY = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto DONE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 48u + 8u * (uint32_t)(k & 1); };
-  // one phase per pair
+  // per stream
   const uint32_t bar2 = bar1 + 64u;
-  const uint32_t S_FULL = bar2, S_READ = bar2 + 8, DP_FULL = bar2 + 16, DP_READ = bar2 + 24;
-  auto DS_READY = [&](int j) { return bar2 + 32u + 8u * (uint32_t)(j & 1); };
-  const uint32_t FINAL = bar2 + 48;
-  auto ph1 = [](int j) { return (uint32_t)(j & 1); };
+  auto S_FULL = [&](int j) { return bar2 + 8u * (uint32_t)(j & 1); };
+  auto S_READ = [&](int j) { return bar2 + 16u + 8u * (uint32_t)(j & 1); };
+  auto DP_FULL = [&](int j) { return bar2 + 32u + 8u * (uint32_t)(j & 1); };
+  auto DP_READ = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j & 1); };
+  // four buffers of dS: unit j + 4 waits for the product of unit j
+  auto DS_READY = [&](int j) { return bar2 + 64u + 8u * (uint32_t)(j & 3); };
+  const uint32_t FINAL = bar2 + 96;
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phK = [](int j) { return (uint32_t)((j / C::kK) & 1); };
   auto phV = [](int j) { return (uint32_t)((j / C::kV) & 1); };
@@ -167,17 +172,18 @@ __global__ void __launch_bounds__(640, 1)
     for (int s = 0; s < 2 * (C::kK + C::kV); ++s) mbar_init(bar0 + 8u * s, 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(Q_FULL(k), 1);
-      mbar_init(Q_EMPTY(k), 1);
+      mbar_init(Q_EMPTY(k), 2);
       mbar_init(DONE(k), 1);
-      mbar_init(ACC_FREE(k), 16);
+      mbar_init(ACC_FREE(k), 8);
     }
-    mbar_init(S_FULL, 1);
-    mbar_init(S_READ, 16);
-    mbar_init(DP_FULL, 1);
-    mbar_init(DP_READ, 16);
-    mbar_init(DS_READY(0), 16);
-    mbar_init(DS_READY(1), 16);
-    mbar_init(FINAL, 2);
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(S_FULL(j), 1);
+      mbar_init(S_READ(j), 4);
+      mbar_init(DP_FULL(j), 1);
+      mbar_init(DP_READ(j), 4);
+    }
+    for (int j = 0; j < 4; ++j) mbar_init(DS_READY(j), 4);
+    mbar_init(FINAL, 3);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(640, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Tiles without a unit take no part in the numbering k of tiles and j of pairs.
+  // Tiles without a unit take no part in the numbering k of tiles and j of units.
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
     auto next_tile = [&](int& i, Tile& w) {
@@ -214,16 +220,12 @@ __global__ void __launch_bounds__(640, 1)
       }
       nq = k + 1;
     };
-    auto load_pair = [&](uint32_t dst, const CUtensorMap* map, int u0, int u1, const Tile& w,
-                         uint32_t bar) {
-      mbar_expect_tx(bar, C::kPair);
+    auto load_unit = [&](uint32_t dst, const CUtensorMap* map, int u, const Tile& w, uint32_t bar) {
+      mbar_expect_tx(bar, C::kKV);
 #pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb) {
-        tma_load_4d(dst + cb * 16384, map, cb * 64, u0 * kUnit, w.hk, w.b, bar);
-        tma_load_4d(dst + cb * 16384 + 8192, map, cb * 64, u1 * kUnit, w.hk, w.b, bar);
-      }
+      for (int cb = 0; cb < D / 64; ++cb)
+        tma_load_4d(dst + cb * 8192, map, cb * 64, u * kUnit, w.hk, w.b, bar);
     };
-    const int none = (p.Sk + kUnit - 1) / kUnit;  // past the keys: zeros
     int i = (int)blockIdx.x - (int)gridDim.x, k = 0, j = 0;
     Tile w, nw;
     bool on = next_tile(i, w);
@@ -231,18 +233,19 @@ __global__ void __launch_bounds__(640, 1)
     while (on) {
       const int* units = p.plan.unit + w.gt * p.U;
       const bool more = next_tile(i, nw);
-      int u0 = units[0], u1 = w.n > 1 ? units[1] : none;
-      for (int e = 0; e < w.n; e += 2, ++j) {
-        const int n0 = e + 2 < w.n ? units[e + 2] : none, n1 = e + 3 < w.n ? units[e + 3] : none;
+      int u = units[0];
+      for (int e = 0; e < w.n; ++e, ++j) {
+        const int next = e + 1 < w.n ? units[e + 1] : 0;
         if (j >= C::kK) ok = ok && wait(K_EMPTY(j), phK(j - C::kK));
-        if (ok) load_pair(sK(j), &tmK, u0, u1, w, K_FULL(j)), nk = j + 1;
+        if (ok) load_unit(sK(j), &tmK, u, w, K_FULL(j)), nk = j + 1;
         if (j >= C::kV) ok = ok && wait(V_EMPTY(j), phV(j - C::kV));
         if (!ok) break;
-        load_pair(sV(j), &tmV, u0, u1, w, V_FULL(j));
+        load_unit(sV(j), &tmV, u, w, V_FULL(j));
         nv = j + 1;
-        u0 = n0, u1 = n1;
-        if (C::kQ == 1 && e == 0) load_q(w, k);
-        if (C::kQ == 2 && more && (e == 2 || (e == 0 && w.n <= 2))) load_q(nw, k + 1);
+        u = next;
+        const bool second = e == min(w.n - 1, 1);
+        if (C::kQ == 1 && second) load_q(w, k);
+        if (C::kQ == 2 && more && second) load_q(nw, k + 1);
       }
       w = nw;
       on = more && ok;
@@ -255,101 +258,99 @@ __global__ void __launch_bounds__(640, 1)
       mbar_wait_drain(K_FULL(x), phK(x), p.spin_ns, p.err, p.err + 1);
     for (int x = max(0, nv - C::kV); x < nv; ++x)
       mbar_wait_drain(V_FULL(x), phV(x), p.spin_ns, p.err, p.err + 1);
-  } else if (warp == 1 || warp == 2) {
+  } else if (warp >= 1 && warp < 4) {
     // ---------------------------------------------------------------- product issuers
-    // Two of them, S and dP and beside them dQ: one thread's instructions take longer than
-    // the products it issues.  The whole warp walks the loop, one lane issues
+    // Three of them: warps 1 and 2 S and dP of a stream, warp 3 dQ.  One thread's instructions
+    // take longer than the products it issues.  The whole warp walks the loop, one lane issues
     const bool leader = elect_one();
     const uint32_t hi = sdesc_hi(1024);
     bool ok = true;  // no wait has run out: else no more products
-    int k = 0, j = 0, ks = 0, vs = 0;  // ks, vs: stages of K and V
-    uint32_t kph = 0, vph = 0;
+    int k = 0, j0 = 0;
 #pragma unroll 1
     for (int i = blockIdx.x; i < p.tiles && ok; i += gridDim.x) {
       const int y = i / BHk;
       const int n = p.plan.count[(long long)(i - y * BHk) * p.NT + (p.NT - 1 - y)];
       if (n == 0) continue;
-      if (warp == 1) {
-        constexpr uint32_t ID_S = idesc_bf16_f32(128, 2 * kUnit, 0, 0);
+      if (warp < 3) {
+        constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
         const uint32_t kQ = sdesc_lo(sQ(k), 16), kDO = sdesc_lo(sDO(k), 16);
+        const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(warp - 1);
         ok = wait(Q_FULL(k), ph2(k));
 #pragma unroll 1
-        for (int e = 0; e < n && ok; e += 2, ++j) {
-          const uint32_t kK = sdesc_lo(sb + C::OFF_K + ks * C::kPair, 16);
-          const uint32_t kV = sdesc_lo(sb + C::OFF_V + vs * C::kPair, 16);
-          ok = wait(bar0 + 8u * ks, kph) && (j == 0 || wait(S_READ, ph1(j - 1)));
+        for (int e = (j0 ^ (warp - 1)) & 1; e < n && ok; e += 2) {
+          const int j = j0 + e;
+          const uint32_t kK = sdesc_lo(sK(j), 16), kV = sdesc_lo(sV(j), 16);
+          ok = wait(K_FULL(j), phK(j)) && (j < 2 || wait(S_READ(j), ph2(j - 2)));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              tc_mma_ss_w(tmem + C::TM_S, kQ + at, kK + at, hi, ID_S, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(S_FULL);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                          kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                          kk > 0 ? 1u : 0u);
+            tc_commit(S_FULL(j));
           }
-          ok = wait(bar0 + 8u * (2 * C::kK + vs), vph) && (j == 0 || wait(DP_READ, ph1(j - 1)));
+          ok = wait(V_FULL(j), phV(j)) && (j < 2 || wait(DP_READ(j), ph2(j - 2)));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-              tc_mma_ss_w(tmem + C::TM_DP, kDO + at, kV + at, hi, ID_S, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(DP_FULL);
-            tc_commit(bar0 + 8u * (2 * C::kK + C::kV + vs));  // V_EMPTY
-            if (e + 2 >= n) tc_commit(Q_EMPTY(k));
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                          kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                          kk > 0 ? 1u : 0u);
+            tc_commit(DP_FULL(j));
+            tc_commit(V_EMPTY(j));
           }
-          if (++ks == C::kK) ks = 0, kph ^= 1u;
-          if (++vs == C::kV) vs = 0, vph ^= 1u;
         }
+        if (leader && ok) tc_commit(Q_EMPTY(k));
       } else {
         constexpr uint32_t ID_Q = idesc_bf16_f32(128, D, 0, 1);  // K MN-major
         const uint32_t tDQ = tmem + C::TM_DQ + (uint32_t)(D * (k % C::kAcc));
         // the accumulator's last tile must have been read
         if (k >= C::kAcc) ok = wait(ACC_FREE(k - C::kAcc), ph2(k - C::kAcc));
 #pragma unroll 1
-        for (int e = 0; e < n && ok; e += 2, ++j) {
-          const uint32_t mK = sdesc_lo(sb + C::OFF_K + ks * C::kPair, 16384);
-          const uint32_t tDS = tmem + C::TM_DS + 64u * (uint32_t)(j & 1);
-          ok = wait(DS_READY(j), ph2(j));
+        for (int e = 0; e < n && ok; ++e) {
+          const int j = j0 + e;
+          const uint32_t mK = sdesc_lo(sK(j), 8192);
+          const uint32_t tDS = tmem + C::TM_DS + 32u * (uint32_t)(j & 3);
+          ok = wait(DS_READY(j), (uint32_t)((j >> 2) & 1));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 2 * kUnit / 16; ++kk)
+            for (int kk = 0; kk < kUnit / 16; ++kk)
               tc_mma_ts_w(tDQ, tDS + 8 * kk, mK + kk * 128, hi, ID_Q, (uint32_t)(e + kk));
-            tc_commit(bar0 + 8u * (C::kK + ks));  // K_EMPTY
-            if (e + 2 >= n) tc_commit(DONE(k));
+            tc_commit(K_EMPTY(j));
+            if (e + 1 == n) tc_commit(DONE(k));
           }
-          if (++ks == C::kK) ks = 0;
         }
       }
+      j0 += n;
       ++k;
     }
     if (leader) tc_commit(FINAL);  // the CTA does not go before its products
     mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax gradient
-    // warpgroup wg takes keys 32 half to 32 half + 31 of the pair's unit h
-    const int wg = (warp - 4) >> 2, h = wg >> 1, half = wg & 1, quarter = warp & 3;
+    const int h = (warp - 4) >> 2, quarter = warp & 3;  // warpgroup h takes units j = h mod 2
     const int r = quarter * 32 + lane;
     const int t = r / p.G, g = r - t * p.G;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const float sl2 = p.scale_log2;
     const int bit = t & 31, wsel = min(t >> 5, p.W - 1);
-    int j = 0, k = 0;
+    int j0 = 0, k = 0;
     for (int i = blockIdx.x; i < p.tiles; i += gridDim.x) {
       const Tile w = tile_at(i);
       const int token = w.t0 + t;
       const bool valid = t < p.T && token < p.Sq;
       __nv_bfloat16* out =
-          p.dq + (((long long)w.bh * p.G + g) * p.Sq + token) * D + wg * (D / 4);
+          p.dq + (((long long)w.bh * p.G + g) * p.Sq + token) * D + h * (D / 2);
       if (w.n == 0) {
         if (valid)
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x)
+          for (int x = 0; x < D / 16; ++x)
             reinterpret_cast<uint4*>(out)[x] = make_uint4(0, 0, 0, 0);
         continue;
       }
@@ -359,77 +360,84 @@ __global__ void __launch_bounds__(640, 1)
                         : p.causal ? (int)min((long long)kvlen, max(pos + 1, 0ll)) : kvlen;
       const int* units = p.plan.unit + w.gt * p.U;
       const uint32_t* masks = p.plan.mask + w.gt * p.U * p.W + wsel;
+      int e = (j0 ^ h) & 1;  // this stream's first unit of the tile
       int u = 0;
-      uint32_t word = 0u;  // nobody picks the missing half of an odd list's last pair
-      if (h < w.n) u = units[h], word = masks[(long long)h * p.W];
+      uint32_t word = 0u;
+      if (e < w.n) u = units[e], word = masks[(long long)e * p.W];
       const long long row = ((long long)w.bh * p.G + g) * p.Sq + token;
       const float lse2 = valid ? p.lse[row] * 1.4426950408889634f : 0.f;
       const float delta = valid ? p.delta[row] : 0.f;
-      for (int e = h; e < w.n + h; e += 2, ++j) {
+      for (; e < w.n; e += 2) {
+        const int j = j0 + e;
         const int base = u * kUnit;
-        const int v = ((word >> bit) & 1u) ? limit - base - 32 * half : 0;  // keys below it count
-        const bool partial = half == 0 && e < w.n && base + kUnit > kvlen && kvlen < p.Sk;
-        word = 0u;
+        const int v = ((word >> bit) & 1u) ? limit - base : 0;  // keys below it count
+        const bool partial = base + kUnit > kvlen && kvlen < p.Sk;
         if (e + 2 < w.n) {
           u = units[e + 2];
           word = masks[(long long)(e + 2) * p.W];
         }
         const bool any = __any_sync(0xffffffffu, v > 0);
-        const bool clean = __all_sync(0xffffffffu, v >= 32 || v <= 0);
+        const bool clean = __all_sync(0xffffffffu, v >= kUnit || v <= 0);
         const uint32_t keep = v > 0 ? 0xffffffffu : 0u;
-        const uint32_t tS = tmem + lane_off + C::TM_S + 32u * wg, tDP = tS + 128;
-        const uint32_t tDS = tmem + lane_off + C::TM_DS + 64u * (uint32_t)(j & 1) + 16u * wg;
-        float pr[32];
-        wait(S_FULL, ph1(j));
+        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * h, tDP = tS + 64;
+        const uint32_t tDS = tmem + lane_off + C::TM_DS + 32u * (uint32_t)(j & 3);
+        float pr[kUnit];
+        wait(S_FULL(j), ph2(j));
         tc_fence_after();
         if (any) {
-          uint32_t sv[32];
-          tmem_ld32(tS, sv);
+          uint32_t sv[2][32];
+          tmem_ld32x2(tS, tS + 32, sv[0], sv[1]);
           tc_fence_before();
-          warp_arrive(S_READ, lane);
+          warp_arrive(S_READ(j), lane);
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            fma_f32x2(pr[x], pr[x + 1], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]), sl2,
-                      -lse2);
+          for (int x = 0; x < kUnit; x += 2) {
+            fma_f32x2(pr[x], pr[x + 1], __uint_as_float(sv[x >> 5][x & 31]),
+                      __uint_as_float(sv[x >> 5][(x & 31) + 1]), sl2, -lse2);
             pr[x] = ex2_approx(pr[x]);
             pr[x + 1] = ex2_approx(pr[x + 1]);
           }
         } else {
-          warp_arrive(S_READ, lane);
+          warp_arrive(S_READ(j), lane);
         }
         if (partial) {
           // K rows past the sequence hold whatever the cache holds: 0 * NaN would reach dQ
           const int first = max(kvlen - base, 0);
           for (int x = r; x < (kUnit - first) * (D / 8); x += 128) {
             const int kr = first + x / (D / 8), c = x % (D / 8);
-            st_shared_v4(sK(j) + (c >> 3) * 16384 + h * 8192 + kr * 128 + (c & 7) * 16, 0, 0, 0, 0);
+            st_shared_v4(sK(j) + (c >> 3) * 8192 + kr * 128 + (c & 7) * 16, 0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        if (j >= 2) wait(K_EMPTY(j - 2), phK(j - 2));  // dS of pair j - 2 has been used
-        wait(DP_FULL, ph1(j));
+        if (j >= 4) wait(K_EMPTY(j - 4), phK(j - 4));  // dS of unit j - 4 has been used
+        wait(DP_FULL(j), ph2(j));
         tc_fence_after();
         if (any) {
-          uint32_t dp[32], pk[16];
-          tmem_ld32(tDP, dp);
-          tc_fence_before();
-          warp_arrive(DP_READ, lane);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float d0, d1;
-            add_f32x2(d0, d1, __uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), -delta);
-            mul_f32x2(d0, d1, pr[2 * x], pr[2 * x + 1], d0, d1);
-            if (!clean) {  // selected, not multiplied: S and dP of a masked key may be anything
-              if (2 * x >= v) d0 = 0.f;
-              if (2 * x + 1 >= v) d1 = 0.f;
+          for (int c = 0; c < 2; ++c) {
+            uint32_t dp[32], pk[16];
+            tmem_ld32(tDP + 32 * c, dp);
+            if (c == 1) {
+              tc_fence_before();
+              warp_arrive(DP_READ(j), lane);
             }
-            pk[x] = pack_bf16x2(d0, d1) & keep;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              float d0, d1;
+              add_f32x2(d0, d1, __uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), -delta);
+              mul_f32x2(d0, d1, pr[32 * c + 2 * x], pr[32 * c + 2 * x + 1], d0, d1);
+              if (!clean) {  // selected, not multiplied: S and dP of a masked key may be anything
+                if (32 * c + 2 * x >= v) d0 = 0.f;
+                if (32 * c + 2 * x + 1 >= v) d1 = 0.f;
+              }
+              pk[x] = pack_bf16x2(d0, d1) & keep;
+            }
+            tmem_st16(tDS + 16 * c, pk);
           }
-          tmem_st16(tDS, pk);
         } else {
-          warp_arrive(DP_READ, lane);
+          warp_arrive(DP_READ(j), lane);
           const uint32_t zero[16] = {};
           tmem_st16(tDS, zero);
+          tmem_st16(tDS + 16, zero);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -438,22 +446,23 @@ __global__ void __launch_bounds__(640, 1)
       wait(DONE(k), ph2(k));
       tc_fence_after();
       const uint32_t tDQ =
-          tmem + lane_off + C::TM_DQ + (uint32_t)(D * (k % C::kAcc) + wg * (D / 4));
-      uint32_t ov[D / 4];
-      if constexpr (D == 128) tmem_ld32(tDQ, ov);
-      else tmem_ld16(tDQ, ov);
+          tmem + lane_off + C::TM_DQ + (uint32_t)(D * (k % C::kAcc) + h * (D / 2));
+      uint32_t ov[D / 64][32];
+      if constexpr (D == 128) tmem_ld32x2(tDQ, tDQ + 32, ov[0], ov[1]);
+      else tmem_ld32(tDQ, ov[0]);
       tc_fence_before();
       warp_arrive(ACC_FREE(k), lane);
       if (valid) {
-        auto val = [&](int x) { return __uint_as_float(ov[x]) * p.scale; };
+        auto val = [&](int x) { return __uint_as_float(ov[x >> 5][x & 31]) * p.scale; };
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q)
+        for (int q = 0; q < D / 16; ++q)
           reinterpret_cast<uint4*>(out)[q] =
               make_uint4(pack_bf16x2(val(8 * q), val(8 * q + 1)),
                          pack_bf16x2(val(8 * q + 2), val(8 * q + 3)),
                          pack_bf16x2(val(8 * q + 4), val(8 * q + 5)),
                          pack_bf16x2(val(8 * q + 6), val(8 * q + 7)));
       }
+      j0 += w.n;
       ++k;
     }
   }
