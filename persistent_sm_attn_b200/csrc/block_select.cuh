@@ -247,7 +247,7 @@ struct SelectCfg {
 //
 // NL: 32-block words that a lane's share of a row has room for.
 template <int D, int QT, int NL>
-__global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kernel(const SelectParams p) {
   using C = SelectCfg<D, QT>;
   extern __shared__ __align__(16) unsigned char select_smem[];
   __shared__ float qnorm[C::kRows];
@@ -258,65 +258,94 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
   const uint32_t stage = dev::smem_u32(select_smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv;
-  const int i0 = blockIdx.x * QT;
+  const int i0 = (int)(gridDim.x - 1 - blockIdx.x) * QT;  // the longest rows first
   const int rg = warp % C::RG, cg = warp / C::RG;
   const int last = min(i0 + QT, p.Sq) - 1;
   const int most = visible_blocks(p, b, last);  // of the CTA's queries (they see ever more)
   if (tid == 0) mnorm_bits = 0;
 
-  // ---- the group's queries, summed, as MMA operands: row lane/4 (+8), columns 2*(lane%4) (+8)
+  // ---- the group's queries, summed, split and staged as the means are; then as MMA operands
   uint32_t ah[D / 16][4], al[D / 16][4];
   {
-    float n2[2] = {0.f, 0.f};
+    constexpr int CH = D / 8;  // 16-byte pieces of a row
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = rg * 16 + half * 8 + (lane >> 2);
+    for (int x = tid; x < C::kRows * CH; x += C::kThreads) {
+      const int row = x / CH, c = x % CH;
       const bool on = row < QT && i0 + row < p.Sq;
       const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh +
-                               (long long)(on ? i0 + row : 0) * p.ss + (lane & 3) * 2;
+                               (long long)(on ? i0 + row : 0) * p.ss + c * 8;
+      float v[8] = {};
+      if (on) {
+#pragma unroll 4
+        for (int g = 0; g < p.G; ++g) {
+          const uint4 w = *reinterpret_cast<const uint4*>(q + (long long)g * p.sh);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        float x = 0.f, y = 0.f;
-        if (on)
-          for (int g = 0; g < p.G; ++g) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(q + (long long)g * p.sh + c * 8);
-            x += __uint_as_float(w << 16);
-            y += __uint_as_float(w & 0xffff0000u);
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] += __uint_as_float(u[k] << 16);
+            v[2 * k + 1] += __uint_as_float(u[k] & 0xffff0000u);
           }
-        n2[half] += x * x + y * y;
-        split_bf16(x, y, ah[c >> 1][(c & 1) * 2 + half], al[c >> 1][(c & 1) * 2 + half]);
+        }
       }
-      n2[half] += __shfl_xor_sync(0xffffffffu, n2[half], 1);
-      n2[half] += __shfl_xor_sync(0xffffffffu, n2[half], 2);
-      if ((lane & 3) == 0) qnorm[row] = sqrtf(n2[half]);  // every column group writes the same
+      float n2 = 0.f;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        n2 += v[2 * k] * v[2 * k] + v[2 * k + 1] * v[2 * k + 1];
+        split_bf16(v[2 * k], v[2 * k + 1], hi[k], lo[k]);
+      }
+      unsigned char* at = select_smem + row * C::kLd + c * 16;
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(at + 64 * C::kLd) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      // the pieces of a row lie in consecutive lanes
+#pragma unroll
+      for (int o = CH / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      if (c == 0) qnorm[row] = sqrtf(n2);
+    }
+    __syncthreads();
+    // matrices of one load: rows 0-7, rows 8-15, rows 0-7 of the next 8 columns, rows 8-15
+    const uint32_t at = stage + (uint32_t)(rg * 16 + (lane & 15)) * C::kLd + (lane >> 4) * 16;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      ldmatrix_x4(at + kk * 32, ah[kk]);
+      ldmatrix_x4(at + 64 * C::kLd + kk * 32, al[kk]);
     }
   }
 
-  // ---- scores
+  // ---- scores; the next 64 means are on their way while these are multiplied
   const float* means = p.means + (long long)bh * p.nb * D;
+  float4 next[D / 16];
+  const int mrow = tid >> 2, part = tid & 3;
+  auto fetch = [&](int j0) {
+    const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + mrow) * D) + part;
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x)
+      next[x] = j0 + mrow < most ? src[4 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(0);
   for (int j0 = 0; j0 < most; j0 += 64) {
     __syncthreads();
     {
-      const int row = tid >> 2, part = tid & 3;
       float n2 = 0.f;
-      const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + row) * D) + part;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {
-        const float4 w = j0 + row < most ? src[4 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 w = next[x];
         n2 += w.x * w.x + w.y * w.y + w.z * w.z + w.w * w.w;
         uint2 hi, lo;
         split_bf16(w.x, w.y, hi.x, lo.x);
         split_bf16(w.z, w.w, hi.y, lo.y);
-        unsigned char* at = select_smem + row * C::kLd + (4 * x + part) * 8;
+        unsigned char* at = select_smem + mrow * C::kLd + (4 * x + part) * 8;
         *reinterpret_cast<uint2*>(at) = hi;
         *reinterpret_cast<uint2*>(at + 64 * C::kLd) = lo;
       }
       n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
       n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
       // as bits, so that an infinity or NaN stays the largest
-      if (part == 0) atomicMax(&mnorm_bits, __float_as_int(n2) & 0x7fffffff);
+      const int most_n2 = __reduce_max_sync(0xffffffffu, __float_as_int(n2) & 0x7fffffff);
+      if (lane == 0) atomicMax(&mnorm_bits, most_n2);
     }
     __syncthreads();
+    if (j0 + 64 < most) fetch(j0 + 64);
     float acc[C::NT][4] = {};
     // matrices of one load: high k 0-7, high k 8-15, low k 0-7, low k 8-15
     const uint32_t at = stage + (lane >> 4) * (64 * C::kLd) + ((lane >> 3) & 1) * 16 +
@@ -356,10 +385,17 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
     uint32_t take[W], open[W];  // bit x: block 32 x + lane is taken; is to be decided in fp64
 #pragma unroll
     for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
+    // this lane's scores: in registers for up to 512 blocks
+    constexpr bool kHeld = NL <= 16;
+    float held[kHeld ? NL : 1];
+    if constexpr (kHeld)
+#pragma unroll
+      for (int x = 0; x < NL; ++x) held[x] = x < nl ? row[32 * x + lane] : 0.f;
+    auto score = [&](int x, int j) { return kHeld ? held[kHeld ? x : 0] : row[j]; };
     auto each = [&](auto&& f) {  // the contested blocks of this lane
 #pragma unroll (NL <= 16 ? NL : 4)
       for (int x = 0; x < NL; ++x) {
-        if (x >= nl) break;
+        if (!kHeld && x >= nl) break;
         const int j = 32 * x + lane;
         if (j >= j0 && j < j1) f(x, j);
       }
@@ -370,7 +406,14 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
       int need = r;
       if (eps2 < 1e30f) {  // beyond, a partial sum might overflow
         float lo = INFINITY, hi = -INFINITY;  // the r-th and the next largest lie in [lo, hi]
-        each([&](int, int j) { lo = fminf(lo, row[j]), hi = fmaxf(hi, row[j]); });
+        each([&](int x, int j) {
+          const float v = score(x, j);
+          lo = fminf(lo, v), hi = fmaxf(hi, v);
+        });
+        if constexpr (kHeld)  // what is not contested counts as below everything
+#pragma unroll
+          for (int x = 0; x < NL; ++x)
+            if (32 * x + lane < j0 || 32 * x + lane >= j1) held[x] = -INFINITY;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -378,21 +421,39 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
         }
         float cut = 0.f;
         bool found = false;
+        // the range falls to a quarter (a third) with each count: up to 512 blocks leave
+        // room for three counts in a word
+        constexpr int kBits = kHeld ? 10 : 16;
         while (!found) {
-          const float mid = 0.5f * lo + 0.5f * hi;
-          if (!(mid > lo && mid < hi)) break;
-          int c = 0;
-          each([&](int, int j) { c += row[j] > mid; });
+          const float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
+          const float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
+          if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
+          unsigned c = 0;
+          if constexpr (kHeld) {
+#pragma unroll
+            for (int x = 0; x < NL; ++x)
+              c += (held[x] > m1 ? 1u : 0u) + (held[x] > m2 ? 1u << kBits : 0u) +
+                   (held[x] > m3 ? 1u << (2 * kBits) : 0u);
+          } else {
+            each([&](int, int j) { c += (row[j] > m1 ? 1u : 0u) + (row[j] > m2 ? 1u << kBits : 0u); });
+          }
           c = __reduce_add_sync(0xffffffffu, c);
-          if (c == r) cut = mid, found = true;
-          else if (c > r) lo = mid;
-          else hi = mid;
+          const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
+          const int c3 = kHeld ? (int)(c >> (2 * kBits)) : 0;
+          if (c1 == r) cut = m1, found = true;
+          else if (c2 == r) cut = m2, found = true;
+          else if (kHeld && c3 == r) cut = m3, found = true;
+          else if (c1 < r) hi = m1;
+          else if (c2 < r) lo = m1, hi = m2;
+          else if (!kHeld) lo = m2;
+          else if (c3 < r) lo = m2, hi = m3;
+          else lo = m3;
         }
         float a = lo, z = hi;
         if (found) {
           a = INFINITY, z = -INFINITY;  // lowest above the cut, highest below
-          each([&](int, int j) {
-            const float v = row[j];
+          each([&](int x, int j) {
+            const float v = score(x, j);
             if (v > cut) a = fminf(a, v);
             else z = fmaxf(z, v);
           });
@@ -405,7 +466,7 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
         const bool clear = found && a - z > eps2;
         int in = 0;
         each([&](int x, int j) {
-          const float v = row[j];
+          const float v = score(x, j);
           if (clear ? v > cut : v > z + eps2) take[x >> 5] |= 1u << (x & 31), ++in;
           else if (!clear && v >= a - eps2) open[x >> 5] |= 1u << (x & 31);
         });
@@ -413,15 +474,55 @@ __global__ void __launch_bounds__(256) dash_block_select_kernel(const SelectPara
       } else {
         each([&](int x, int) { open[x >> 5] |= 1u << (x & 31); });
       }
+      int undecided = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) undecided += __popc(open[w]);
+      undecided = __reduce_add_sync(0xffffffffu, undecided);
+      double qd[D / 32] = {};
       if (need > 0) {
-        // exact scores of the open blocks, their keys' upper words in place of the scores;
-        // then, among those that tie in it, by the lower words; then by number
-        double qd[D / 32] = {};
         const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+#pragma unroll 4
         for (int g = 0; g < p.G; ++g)
 #pragma unroll
           for (int x = 0; x < D / 32; ++x)
             qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
+      }
+      if (need > 0 && undecided <= 32) {
+        // the usual case: one open block a lane (ascending), its place among them by 64-bit keys
+        int mine = -1, n = 0;
+#pragma unroll 1
+        for (int x = 0; x < nl; ++x) {
+          unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
+          for (; m; m &= m - 1, ++n)
+            if (lane == n) mine = 32 * x + __ffs(m) - 1;
+        }
+        unsigned long long key64 = 0;
+#pragma unroll 2
+        for (int t = 0; t < n; ++t) {
+          const int j = __shfl_sync(0xffffffffu, mine, t);
+          const unsigned long long k = order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+          if (lane == t) key64 = k;
+        }
+        int place = 0;
+#pragma unroll 2
+        for (int t = 0; t < n; ++t) {
+          const unsigned long long k = __shfl_sync(0xffffffffu, key64, t);
+          place += k > key64 || (k == key64 && t < lane);
+        }
+        const bool in = lane < n && place < need;
+#pragma unroll 2
+        for (int t = 0; t < n; ++t) {
+          const int j = __shfl_sync(0xffffffffu, in ? mine : -1, t);
+          if (j >= 0 && (j & 31) == lane)
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+              if (w == j >> 10) take[w] |= 1u << ((j >> 5) & 31);
+        }
+        need = 0;
+      }
+      if (need > 0) {
+        // exact scores of the open blocks, their keys' upper words in place of the scores;
+        // then, among those that tie in it, by the lower words; then by number
 #pragma unroll 1
         for (int word = 0; word < 2; ++word) {
 #pragma unroll 1
