@@ -80,6 +80,13 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 
+// fp32 bits as an integer that orders like the value, and back
+__device__ __forceinline__ int ordered_int(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ int ordered_int_inverse(int k) { return k ^ ((k >> 31) & 0x7fffffff); }
+
 // Where query i of batch entry b stands: the number of blocks it sees.
 __device__ __forceinline__ int visible_blocks(const SelectParams& p, int b, int i) {
   const int len = p.kv_len ? min(max(p.kv_len[b], 0), p.Sk) : p.Sk;
@@ -242,7 +249,7 @@ struct SelectCfg {
 // Picks: a cut T with exactly r scores above it, by halving the range of the scores.  Where
 // the lowest score above T and the highest below are more than 2 eps apart, the picks are
 // those of the exact scores.  Otherwise the scores within 2 eps of the cut are computed in
-// fp64 and decided by those (about one query in ten on normal data).  An eps that is not
+// fp64 and decided by those.  An eps that is not
 // finite (an infinity or NaN among the operands) leaves everything to fp64.
 //
 // NL: 32-block words that a lane's share of a row has room for.
@@ -251,7 +258,9 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
   using C = SelectCfg<D, QT>;
   extern __shared__ __align__(16) unsigned char select_smem[];
   __shared__ float qnorm[C::kRows];
-  __shared__ int mnorm_bits;
+  __shared__ int mnorm_bits, todo_n;
+  __shared__ int2 todo[QT];
+  __shared__ int nv[QT];  // blocks that each query sees
   constexpr int W = (NL + 31) / 32;
   const int ld = (p.nb + 63) / 64 * 64 + 8;
   float* sc = reinterpret_cast<float*>(select_smem + C::kStage);  // [QT][ld]
@@ -262,7 +271,8 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
   const int rg = warp % C::RG, cg = warp / C::RG;
   const int last = min(i0 + QT, p.Sq) - 1;
   const int most = visible_blocks(p, b, last);  // of the CTA's queries (they see ever more)
-  if (tid == 0) mnorm_bits = 0;
+  if (tid == 0) mnorm_bits = todo_n = 0;
+  if (tid < QT) nv[tid] = visible_blocks(p, b, i0 + tid);
 
   // ---- the group's queries, summed, split and staged as the means are; then as MMA operands
   uint32_t ah[D / 16][4], al[D / 16][4];
@@ -372,208 +382,15 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
   }
   __syncthreads();
 
-  // ---- picks, a warp per query
+  // ---- picks, a warp per query.  Queries whose picks the bound leaves open are put off, so
+  // that the warps share them (one in fifteen on normal data, two blocks each)
   const float mnorm = sqrtf(__int_as_float(mnorm_bits));
   const int r = p.topk - p.sink - p.local;
-  for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += 8) {
-    const int i = i0 + rr;
-    const int nvis = visible_blocks(p, b, i);
-    float* row = sc + rr * ld;
-    uint32_t* key = reinterpret_cast<uint32_t*>(row);
-    const int j0 = p.sink, j1 = nvis - p.local;
-    const int nl = (nvis + 31) / 32;
-    uint32_t take[W], open[W];  // bit x: block 32 x + lane is taken; is to be decided in fp64
-#pragma unroll
-    for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
-    // this lane's scores: in registers for up to 512 blocks
-    constexpr bool kHeld = NL <= 16;
-    float held[kHeld ? NL : 1];
-    if constexpr (kHeld)
-#pragma unroll
-      for (int x = 0; x < NL; ++x) held[x] = x < nl ? row[32 * x + lane] : 0.f;
-    auto score = [&](int x, int j) { return kHeld ? held[kHeld ? x : 0] : row[j]; };
-    auto each = [&](auto&& f) {  // the contested blocks of this lane
-#pragma unroll (NL <= 16 ? NL : 4)
-      for (int x = 0; x < NL; ++x) {
-        if (!kHeld && x >= nl) break;
-        const int j = 32 * x + lane;
-        if (j >= j0 && j < j1) f(x, j);
-      }
-    };
+  uint32_t* saved = reinterpret_cast<uint32_t*>(select_smem);  // [QT][2 W][32], over the means
+  auto put_out = [&](int rr, int nvis, const uint32_t(&take)[W]) {
     const bool all = nvis <= p.topk;
-    if (!all && r > 0) {
-      const float eps2 = 2.f * (0x1p-13f * qnorm[rr] * mnorm + 1e-35f);
-      int need = r;
-      if (eps2 < 1e30f) {  // beyond, a partial sum might overflow
-        float lo = INFINITY, hi = -INFINITY;  // the r-th and the next largest lie in [lo, hi]
-        each([&](int x, int j) {
-          const float v = score(x, j);
-          lo = fminf(lo, v), hi = fmaxf(hi, v);
-        });
-        if constexpr (kHeld)  // what is not contested counts as below everything
-#pragma unroll
-          for (int x = 0; x < NL; ++x)
-            if (32 * x + lane < j0 || 32 * x + lane >= j1) held[x] = -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        float cut = 0.f;
-        bool found = false;
-        // the range falls to a quarter (a third) with each count: up to 512 blocks leave
-        // room for three counts in a word
-        constexpr int kBits = kHeld ? 10 : 16;
-        while (!found) {
-          const float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
-          const float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
-          if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
-          unsigned c = 0;
-          if constexpr (kHeld) {
-#pragma unroll
-            for (int x = 0; x < NL; ++x)
-              c += (held[x] > m1 ? 1u : 0u) + (held[x] > m2 ? 1u << kBits : 0u) +
-                   (held[x] > m3 ? 1u << (2 * kBits) : 0u);
-          } else {
-            each([&](int, int j) { c += (row[j] > m1 ? 1u : 0u) + (row[j] > m2 ? 1u << kBits : 0u); });
-          }
-          c = __reduce_add_sync(0xffffffffu, c);
-          const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
-          const int c3 = kHeld ? (int)(c >> (2 * kBits)) : 0;
-          if (c1 == r) cut = m1, found = true;
-          else if (c2 == r) cut = m2, found = true;
-          else if (kHeld && c3 == r) cut = m3, found = true;
-          else if (c1 < r) hi = m1;
-          else if (c2 < r) lo = m1, hi = m2;
-          else if (!kHeld) lo = m2;
-          else if (c3 < r) lo = m2, hi = m3;
-          else lo = m3;
-        }
-        float a = lo, z = hi;
-        if (found) {
-          a = INFINITY, z = -INFINITY;  // lowest above the cut, highest below
-          each([&](int x, int j) {
-            const float v = score(x, j);
-            if (v > cut) a = fminf(a, v);
-            else z = fmaxf(z, v);
-          });
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
-          }
-        }
-        const bool clear = found && a - z > eps2;
-        int in = 0;
-        each([&](int x, int j) {
-          const float v = score(x, j);
-          if (clear ? v > cut : v > z + eps2) take[x >> 5] |= 1u << (x & 31), ++in;
-          else if (!clear && v >= a - eps2) open[x >> 5] |= 1u << (x & 31);
-        });
-        need = clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
-      } else {
-        each([&](int x, int) { open[x >> 5] |= 1u << (x & 31); });
-      }
-      int undecided = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) undecided += __popc(open[w]);
-      undecided = __reduce_add_sync(0xffffffffu, undecided);
-      double qd[D / 32] = {};
-      if (need > 0) {
-        const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
-#pragma unroll 4
-        for (int g = 0; g < p.G; ++g)
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
-      }
-      if (need > 0 && undecided <= 32) {
-        // the usual case: one open block a lane (ascending), its place among them by 64-bit keys
-        int mine = -1, n = 0;
-#pragma unroll 1
-        for (int x = 0; x < nl; ++x) {
-          unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
-          for (; m; m &= m - 1, ++n)
-            if (lane == n) mine = 32 * x + __ffs(m) - 1;
-        }
-        unsigned long long key64 = 0;
-#pragma unroll 2
-        for (int t = 0; t < n; ++t) {
-          const int j = __shfl_sync(0xffffffffu, mine, t);
-          const unsigned long long k = order_key(exact_score<D>(qd, means + (long long)j * D, lane));
-          if (lane == t) key64 = k;
-        }
-        int place = 0;
-#pragma unroll 2
-        for (int t = 0; t < n; ++t) {
-          const unsigned long long k = __shfl_sync(0xffffffffu, key64, t);
-          place += k > key64 || (k == key64 && t < lane);
-        }
-        const bool in = lane < n && place < need;
-#pragma unroll 2
-        for (int t = 0; t < n; ++t) {
-          const int j = __shfl_sync(0xffffffffu, in ? mine : -1, t);
-          if (j >= 0 && (j & 31) == lane)
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-              if (w == j >> 10) take[w] |= 1u << ((j >> 5) & 31);
-        }
-        need = 0;
-      }
-      if (need > 0) {
-        // exact scores of the open blocks, their keys' upper words in place of the scores;
-        // then, among those that tie in it, by the lower words; then by number
-#pragma unroll 1
-        for (int word = 0; word < 2; ++word) {
-#pragma unroll 1
-          for (int x = 0; x < nl; ++x) {
-            unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
-            while (m) {
-              const int src = __ffs(m) - 1;
-              m &= m - 1;
-              const int j = 32 * x + src;
-              const unsigned long long k =
-                  order_key(exact_score<D>(qd, means + (long long)j * D, lane));
-              if (lane == src) key[j] = word == 0 ? (uint32_t)(k >> 32) : (uint32_t)k;
-            }
-          }
-          uint32_t t = 0;  // the need-th largest word, bit by bit
-#pragma unroll 1
-          for (uint32_t bitv = 0x80000000u; bitv; bitv >>= 1) {
-            int c = 0;
-            each([&](int x, int j) {
-              if ((open[x >> 5] >> (x & 31)) & 1u) c += key[j] >= (t | bitv);
-            });
-            if ((int)__reduce_add_sync(0xffffffffu, c) >= need) t |= bitv;
-          }
-          int in = 0, same = 0;
-          each([&](int x, int j) {
-            const uint32_t bx = 1u << (x & 31);
-            if (!(open[x >> 5] & bx)) return;
-            if (key[j] > t) take[x >> 5] |= bx, open[x >> 5] &= ~bx, ++in;
-            else if (key[j] < t) open[x >> 5] &= ~bx;
-            else ++same;
-          });
-          need -= __reduce_add_sync(0xffffffffu, in);
-          same = __reduce_add_sync(0xffffffffu, same);
-          if (same == need) {
-#pragma unroll
-            for (int w = 0; w < W; ++w) take[w] |= open[w], open[w] = 0u;
-            need = 0;
-            break;
-          }
-        }
-        // exact ties: the lowest numbers
-#pragma unroll 1
-        for (int x = 0; x < nl && need > 0; ++x) {
-          const bool tie = (open[x >> 5] >> (x & 31)) & 1u;
-          const unsigned m = __ballot_sync(0xffffffffu, tie);
-          if (tie && __popc(m & ((1u << lane) - 1u)) < need) take[x >> 5] |= 1u << (x & 31);
-          need -= __popc(m);
-        }
-      }
-    }
-    int* out = p.idx + ((long long)bh * p.Sq + i) * p.topk;
+    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
+    int* out = p.idx + ((long long)bh * p.Sq + i0 + rr) * p.topk;
     int done = 0;
 #pragma unroll (NL <= 16 ? NL : 4)
     for (int x = 0; x < NL; ++x) {
@@ -585,6 +402,237 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
       done += __popc(m);
     }
     for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
+  };
+  float guess = 0.f;  // the last cut, of the largest score that could be
+  for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += 8) {
+    const int nvis = nv[rr];
+    const float* row = sc + rr * ld;
+    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
+    uint32_t take[W], open[W];  // bit x: block 32 x + lane is taken; is to be decided in fp64
+#pragma unroll
+    for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
+    int need = 0;
+    if (nvis > p.topk && r > 0) {
+      // this lane's scores, -inf where not contested: in registers for up to 512 blocks
+      constexpr bool kHeld = NL <= 16;
+      float held[kHeld ? NL : 1] = {};
+      if constexpr (kHeld)
+#pragma unroll
+        for (int x = 0; x < NL; ++x) {
+          if (x % 2 == 0 && x >= nl) break;
+          const int j = 32 * x + lane;
+          held[x] = j >= j0 && j < j1 ? row[j] : -INFINITY;
+        }
+      auto each = [&](auto&& f) {
+        if constexpr (kHeld) {
+#pragma unroll
+          for (int x = 0; x < NL; ++x) {
+            if (x > 0 && x % 2 == 0 && x >= nl) break;
+            f(x, held[x]);
+          }
+        } else {
+#pragma unroll 4
+          for (int x = 0; x < nl; ++x) {
+            const int j = 32 * x + lane;
+            f(x, j >= j0 && j < j1 ? row[j] : -INFINITY);
+          }
+        }
+      };
+      const float most_score = qnorm[rr] * mnorm;
+      const float eps2 = 2.f * (0x1p-13f * most_score + 1e-35f);
+      need = r;
+      if (eps2 < 1e30f) {  // beyond, a partial sum might overflow
+        // the r-th and the next largest lie in (lo, hi]: no score is beyond |q| max|m|
+        float lo = -1.01f * most_score - 1e-30f, hi = -lo, cut = 0.f;
+        bool found = false;
+        // the range falls to a quarter (a third) with each count: up to 512 blocks leave
+        // room for three counts in a word
+        constexpr int kBits = kHeld ? 10 : 16;
+        // and the first counts are taken around where the last query's cut was
+        float near = guess * most_score;
+        while (!found && hi - lo > eps2) {
+          float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
+          float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
+          if (near != 0.f) {
+            d = 0.1f * fabsf(near);
+            m1 = near - d, m2 = kHeld ? near : near + d, m3 = near + d;
+            near = 0.f;
+          }
+          if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
+          unsigned c = 0;
+          each([&](int, float v) {
+            c += (v > m1 ? 1u : 0u) + (v > m2 ? 1u << kBits : 0u);
+            if constexpr (kHeld) c += v > m3 ? 1u << (2 * kBits) : 0u;
+          });
+          c = __reduce_add_sync(0xffffffffu, c);
+          const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
+          int c3 = 0;
+          if constexpr (kHeld) c3 = (int)(c >> (2 * kBits));
+          if (c1 == r) cut = m1, found = true;
+          else if (c2 == r) cut = m2, found = true;
+          else if (kHeld && c3 == r) cut = m3, found = true;
+          else if (c1 < r) hi = m1;
+          else if (c2 < r) lo = m1, hi = m2;
+          else if (!kHeld) lo = m2;
+          else if (c3 < r) lo = m2, hi = m3;
+          else lo = m3;
+        }
+        if (found && most_score > 1e-20f) guess = cut / most_score;
+        float a = lo, z = hi;
+        if (found) {  // lowest above the cut, highest below
+          int ka = 0x7f800000, kz = (int)0x807fffff;  // as integers that order like the floats
+          each([&](int, float v) {
+            const int k = ordered_int(v);
+            if (v > cut) ka = min(ka, k);
+            else kz = max(kz, k);
+          });
+          a = __int_as_float(ordered_int_inverse(__reduce_min_sync(0xffffffffu, ka)));
+          z = __int_as_float(ordered_int_inverse(__reduce_max_sync(0xffffffffu, kz)));
+        }
+        const bool clear = found && a - z > eps2;
+        const float in_at = clear ? cut : z + eps2, open_at = clear ? INFINITY : a - eps2;
+        int in = 0;
+        each([&](int x, float v) {
+          if (v > in_at) take[x >> 5] |= 1u << (x & 31), ++in;
+          else if (v >= open_at) open[x >> 5] |= 1u << (x & 31);
+        });
+        need = clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
+      } else {
+        for (int x = 0; x < nl; ++x) {
+          const int j = 32 * x + lane;
+          if (j >= j0 && j < j1) open[x >> 5] |= 1u << (x & 31);
+        }
+      }
+    }
+    if (need > 0) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        saved[(rr * 2 * W + w) * 32 + lane] = take[w];
+        saved[(rr * 2 * W + W + w) * 32 + lane] = open[w];
+      }
+      if (lane == 0) {
+        const int t = atomicAdd(&todo_n, 1);
+        todo[t] = make_int2(rr, need);
+      }
+    } else {
+      put_out(rr, nvis, take);
+    }
+  }
+  __syncthreads();
+  for (int t0 = warp; t0 < todo_n; t0 += 8) {
+    const int rr = todo[t0].x, i = i0 + rr, nvis = nv[rr];
+    int need = todo[t0].y;
+    uint32_t* key = reinterpret_cast<uint32_t*>(sc + rr * ld);
+    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
+    uint32_t take[W], open[W];
+    int undecided = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      take[w] = saved[(rr * 2 * W + w) * 32 + lane];
+      open[w] = saved[(rr * 2 * W + W + w) * 32 + lane];
+      undecided += __popc(open[w]);
+    }
+    undecided = __reduce_add_sync(0xffffffffu, undecided);
+    auto each = [&](auto&& f) {
+#pragma unroll 1
+      for (int x = 0; x < nl; ++x) {
+        const int j = 32 * x + lane;
+        if (j >= j0 && j < j1) f(x, j);
+      }
+    };
+    double qd[D / 32] = {};
+    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g)
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+        qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
+    if (undecided <= 32) {
+      // the usual case: one open block a lane (ascending), its place among them by 64-bit keys
+      int mine = -1, n = 0;
+#pragma unroll 1
+      for (int x = 0; x < nl; ++x) {
+        unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
+        for (; m; m &= m - 1, ++n)
+          if (lane == n) mine = 32 * x + __ffs(m) - 1;
+      }
+      unsigned long long key64 = 0;
+#pragma unroll 2
+      for (int t = 0; t < n; ++t) {
+        const int j = __shfl_sync(0xffffffffu, mine, t);
+        const unsigned long long k = order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+        if (lane == t) key64 = k;
+      }
+      int place = 0;
+#pragma unroll 2
+      for (int t = 0; t < n; ++t) {
+        const unsigned long long k = __shfl_sync(0xffffffffu, key64, t);
+        place += k > key64 || (k == key64 && t < lane);
+      }
+      const bool in = lane < n && place < need;
+#pragma unroll 2
+      for (int t = 0; t < n; ++t) {
+        const int j = __shfl_sync(0xffffffffu, in ? mine : -1, t);
+        if (j >= 0 && (j & 31) == lane)
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (w == j >> 10) take[w] |= 1u << ((j >> 5) & 31);
+      }
+      need = 0;
+    }
+    if (need > 0) {  // many open blocks (equal ones, operands that are not finite)
+      // exact scores of the open blocks, their keys' upper words in place of the scores;
+      // then, among those that tie in it, by the lower words; then by number
+#pragma unroll 1
+      for (int word = 0; word < 2; ++word) {
+#pragma unroll 1
+        for (int x = 0; x < nl; ++x) {
+          unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
+          while (m) {
+            const int src = __ffs(m) - 1;
+            m &= m - 1;
+            const int j = 32 * x + src;
+            const unsigned long long k =
+                order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+            if (lane == src) key[j] = word == 0 ? (uint32_t)(k >> 32) : (uint32_t)k;
+          }
+        }
+        uint32_t t = 0;  // the need-th largest word, bit by bit
+#pragma unroll 1
+        for (uint32_t bitv = 0x80000000u; bitv; bitv >>= 1) {
+          int c = 0;
+          each([&](int x, int j) {
+            if ((open[x >> 5] >> (x & 31)) & 1u) c += key[j] >= (t | bitv);
+          });
+          if ((int)__reduce_add_sync(0xffffffffu, c) >= need) t |= bitv;
+        }
+        int in = 0, same = 0;
+        each([&](int x, int j) {
+          const uint32_t bx = 1u << (x & 31);
+          if (!(open[x >> 5] & bx)) return;
+          if (key[j] > t) take[x >> 5] |= bx, open[x >> 5] &= ~bx, ++in;
+          else if (key[j] < t) open[x >> 5] &= ~bx;
+          else ++same;
+        });
+        need -= __reduce_add_sync(0xffffffffu, in);
+        same = __reduce_add_sync(0xffffffffu, same);
+        if (same == need) {
+#pragma unroll
+          for (int w = 0; w < W; ++w) take[w] |= open[w], open[w] = 0u;
+          need = 0;
+          break;
+        }
+      }
+      // exact ties: the lowest numbers
+#pragma unroll 1
+      for (int x = 0; x < nl && need > 0; ++x) {
+        const bool tie = (open[x >> 5] >> (x & 31)) & 1u;
+        const unsigned m = __ballot_sync(0xffffffffu, tie);
+        if (tie && __popc(m & ((1u << lane) - 1u)) < need) take[x >> 5] |= 1u << (x & 31);
+        need -= __popc(m);
+      }
+    }
+    put_out(rr, nvis, take);
   }
 }
 

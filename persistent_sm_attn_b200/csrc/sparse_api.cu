@@ -440,6 +440,7 @@ int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
   }
+  if (p.nb <= 64) return launch_select_tile<D, 64, 2>(p, B, stream);
   if (p.nb <= 256) return launch_select_tile<D, 64, 8>(p, B, stream);
   if (p.nb <= 512) return launch_select_tile<D, 32, 16>(p, B, stream);
   if (p.nb <= 1024) return launch_select_tile<D, 32, 32>(p, B, stream);
