@@ -230,12 +230,12 @@ __device__ __forceinline__ void split_bf16(float x, float y, uint32_t& hi, uint3
 
 template <int D, int QT>
 struct SelectCfg {
-  static constexpr int kThreads = 256;
-  static constexpr int kRows = QT < 16 ? 16 : QT;       // MMA rows
-  static constexpr int RG = kRows / 16, CG = 8 / RG;    // warps over queries, over blocks
-  static constexpr int NT = 8 / CG;                     // 8-block columns of a warp
-  static constexpr int kLd = D * 2 + 16;                // bytes of a staged row: no bank conflicts
-  static constexpr int kStage = 2 * 64 * kLd;           // 64 means, high and low parts
+  static constexpr int kThreads = 512;
+  static constexpr int kRows = QT < 16 ? 16 : QT;  // MMA rows
+  static constexpr int RG = kRows / 16;            // 16-row groups; 8 warps over the 64 blocks each
+  static constexpr int kLd = D * 2 + 16;           // bytes of a staged row: no bank conflicts
+  static constexpr int kQ = 2 * kRows * kLd;       // queries, high and low parts
+  static constexpr int kStage = kQ + 2 * 64 * kLd; // and 64 means
   static int smem(int nb) { return kStage + QT * ((nb + 63) / 64 * 64 + 8) * 4; }
 };
 
@@ -254,7 +254,7 @@ struct SelectCfg {
 //
 // NL: 32-block words that a lane's share of a row has room for.
 template <int D, int QT, int NL>
-__global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectParams p) {
   using C = SelectCfg<D, QT>;
   extern __shared__ __align__(16) unsigned char select_smem[];
   __shared__ float qnorm[C::kRows];
@@ -268,69 +268,57 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv;
   const int i0 = (int)(gridDim.x - 1 - blockIdx.x) * QT;  // the longest rows first
-  const int rg = warp % C::RG, cg = warp / C::RG;
+  const int rg = warp / 8, cg = warp % 8;  // one 16 x 8 product a warp
   const int last = min(i0 + QT, p.Sq) - 1;
   const int most = visible_blocks(p, b, last);  // of the CTA's queries (they see ever more)
   if (tid == 0) mnorm_bits = todo_n = 0;
   if (tid < QT) nv[tid] = visible_blocks(p, b, i0 + tid);
 
-  // ---- the group's queries, summed, split and staged as the means are; then as MMA operands
-  uint32_t ah[D / 16][4], al[D / 16][4];
-  {
-    constexpr int CH = D / 8;  // 16-byte pieces of a row
-#pragma unroll
-    for (int x = tid; x < C::kRows * CH; x += C::kThreads) {
-      const int row = x / CH, c = x % CH;
-      const bool on = row < QT && i0 + row < p.Sq;
-      const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh +
-                               (long long)(on ? i0 + row : 0) * p.ss + c * 8;
-      float v[8] = {};
-      if (on) {
+  // ---- the group's queries, summed, split and staged
+  constexpr int CH = D / 8;  // 16-byte pieces of a row, in consecutive lanes
+  for (int x = tid; x < C::kRows * CH; x += C::kThreads) {
+    const int row = x / CH, c = x % CH;
+    const bool on = row < QT && i0 + row < p.Sq;
+    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh +
+                             (long long)(on ? i0 + row : 0) * p.ss + c * 8;
+    float v[8] = {};
+    if (on) {
 #pragma unroll 4
-        for (int g = 0; g < p.G; ++g) {
-          const uint4 w = *reinterpret_cast<const uint4*>(q + (long long)g * p.sh);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int g = 0; g < p.G; ++g) {
+        const uint4 w = *reinterpret_cast<const uint4*>(q + (long long)g * p.sh);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[2 * k] += __uint_as_float(u[k] << 16);
-            v[2 * k + 1] += __uint_as_float(u[k] & 0xffff0000u);
-          }
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] += __uint_as_float(u[k] << 16);
+          v[2 * k + 1] += __uint_as_float(u[k] & 0xffff0000u);
         }
       }
-      float n2 = 0.f;
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        n2 += v[2 * k] * v[2 * k] + v[2 * k + 1] * v[2 * k + 1];
-        split_bf16(v[2 * k], v[2 * k + 1], hi[k], lo[k]);
-      }
-      unsigned char* at = select_smem + row * C::kLd + c * 16;
-      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(at + 64 * C::kLd) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      // the pieces of a row lie in consecutive lanes
-#pragma unroll
-      for (int o = CH / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-      if (c == 0) qnorm[row] = sqrtf(n2);
     }
-    __syncthreads();
-    // matrices of one load: rows 0-7, rows 8-15, rows 0-7 of the next 8 columns, rows 8-15
-    const uint32_t at = stage + (uint32_t)(rg * 16 + (lane & 15)) * C::kLd + (lane >> 4) * 16;
+    float n2 = 0.f;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      ldmatrix_x4(at + kk * 32, ah[kk]);
-      ldmatrix_x4(at + 64 * C::kLd + kk * 32, al[kk]);
+    for (int k = 0; k < 4; ++k) {
+      n2 += v[2 * k] * v[2 * k] + v[2 * k + 1] * v[2 * k + 1];
+      split_bf16(v[2 * k], v[2 * k + 1], hi[k], lo[k]);
     }
+    unsigned char* at = select_smem + row * C::kLd + c * 16;
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + C::kRows * C::kLd) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+    for (int o = CH / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    if (c == 0) qnorm[row] = sqrtf(n2);
   }
 
   // ---- scores; the next 64 means are on their way while these are multiplied
   const float* means = p.means + (long long)bh * p.nb * D;
-  float4 next[D / 16];
-  const int mrow = tid >> 2, part = tid & 3;
+  unsigned char* const mstage = select_smem + C::kQ;
+  float4 next[D / 32];
+  const int mrow = tid >> 3, part = tid & 7;
   auto fetch = [&](int j0) {
     const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + mrow) * D) + part;
 #pragma unroll
-    for (int x = 0; x < D / 16; ++x)
-      next[x] = j0 + mrow < most ? src[4 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < D / 32; ++x)
+      next[x] = j0 + mrow < most ? src[8 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   fetch(0);
   for (int j0 = 0; j0 < most; j0 += 64) {
@@ -338,47 +326,49 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
     {
       float n2 = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
+      for (int x = 0; x < D / 32; ++x) {
         const float4 w = next[x];
         n2 += w.x * w.x + w.y * w.y + w.z * w.z + w.w * w.w;
         uint2 hi, lo;
         split_bf16(w.x, w.y, hi.x, lo.x);
         split_bf16(w.z, w.w, hi.y, lo.y);
-        unsigned char* at = select_smem + mrow * C::kLd + (4 * x + part) * 8;
+        unsigned char* at = mstage + mrow * C::kLd + (8 * x + part) * 8;
         *reinterpret_cast<uint2*>(at) = hi;
         *reinterpret_cast<uint2*>(at + 64 * C::kLd) = lo;
       }
-      n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
-      n2 += __shfl_xor_sync(0xffffffffu, n2, 2);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
       // as bits, so that an infinity or NaN stays the largest
       const int most_n2 = __reduce_max_sync(0xffffffffu, __float_as_int(n2) & 0x7fffffff);
       if (lane == 0) atomicMax(&mnorm_bits, most_n2);
     }
     __syncthreads();
     if (j0 + 64 < most) fetch(j0 + 64);
-    float acc[C::NT][4] = {};
-    // matrices of one load: high k 0-7, high k 8-15, low k 0-7, low k 8-15
-    const uint32_t at = stage + (lane >> 4) * (64 * C::kLd) + ((lane >> 3) & 1) * 16 +
-                        (uint32_t)(cg * C::NT * 8 + (lane & 7)) * C::kLd;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int t = 0; t < C::NT; ++t) {
-        uint32_t m[4];
-        ldmatrix_x4(at + t * 8 * C::kLd + kk * 32, m);
-        mma_bf16(acc[t], ah[kk], m[0], m[1]);
-        mma_bf16(acc[t], ah[kk], m[2], m[3]);
-        mma_bf16(acc[t], al[kk], m[0], m[1]);
+    if (rg < C::RG) {
+      float acc[4] = {};
+      // queries: rows 0-7, rows 8-15, rows 0-7 of the next 8 columns, rows 8-15
+      const uint32_t qat = stage + (uint32_t)(rg * 16 + (lane & 15)) * C::kLd + (lane >> 4) * 16;
+      // means: high k 0-7, high k 8-15, low k 0-7, low k 8-15
+      const uint32_t mat = stage + C::kQ + (lane >> 4) * (64 * C::kLd) + ((lane >> 3) & 1) * 16 +
+                           (uint32_t)(cg * 8 + (lane & 7)) * C::kLd;
+#pragma unroll 4
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t qh[4], ql[4], m[4];
+        ldmatrix_x4(qat + kk * 32, qh);
+        ldmatrix_x4(qat + C::kRows * C::kLd + kk * 32, ql);
+        ldmatrix_x4(mat + kk * 32, m);
+        mma_bf16(acc, qh, m[0], m[1]);
+        mma_bf16(acc, qh, m[2], m[3]);
+        mma_bf16(acc, ql, m[0], m[1]);
       }
-#pragma unroll
-    for (int t = 0; t < C::NT; ++t)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int row = rg * 16 + half * 8 + (lane >> 2);
         if (row < QT)
-          *reinterpret_cast<float2*>(sc + row * ld + j0 + (cg * C::NT + t) * 8 + (lane & 3) * 2) =
-              make_float2(acc[t][2 * half], acc[t][2 * half + 1]);
+          *reinterpret_cast<float2*>(sc + row * ld + j0 + cg * 8 + (lane & 3) * 2) =
+              make_float2(acc[2 * half], acc[2 * half + 1]);
       }
+    }
   }
   __syncthreads();
 
@@ -386,7 +376,7 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
   // that the warps share them (one in fifteen on normal data, two blocks each)
   const float mnorm = sqrtf(__int_as_float(mnorm_bits));
   const int r = p.topk - p.sink - p.local;
-  uint32_t* saved = reinterpret_cast<uint32_t*>(select_smem);  // [QT][2 W][32], over the means
+  uint32_t* saved = reinterpret_cast<uint32_t*>(mstage);  // [QT][2 W][32], over the means
   auto put_out = [&](int rr, int nvis, const uint32_t(&take)[W]) {
     const bool all = nvis <= p.topk;
     const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
@@ -404,7 +394,7 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
     for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
   };
   float guess = 0.f;  // the last cut, of the largest score that could be
-  for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += 8) {
+  for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += C::kThreads / 32) {
     const int nvis = nv[rr];
     const float* row = sc + rr * ld;
     const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
@@ -519,7 +509,7 @@ __global__ void __launch_bounds__(256, NL <= 16 ? 2 : 1) dash_block_select_kerne
     }
   }
   __syncthreads();
-  for (int t0 = warp; t0 < todo_n; t0 += 8) {
+  for (int t0 = warp; t0 < todo_n; t0 += C::kThreads / 32) {
     const int rr = todo[t0].x, i = i0 + rr, nvis = nv[rr];
     int need = todo[t0].y;
     uint32_t* key = reinterpret_cast<uint32_t*>(sc + rr * ld);

@@ -440,8 +440,8 @@ int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
   }
-  if (p.nb <= 64) return launch_select_tile<D, 64, 2>(p, B, stream);
-  if (p.nb <= 256) return launch_select_tile<D, 64, 8>(p, B, stream);
+  if (p.nb <= 64) return launch_select_tile<D, 32, 2>(p, B, stream);
+  if (p.nb <= 256) return launch_select_tile<D, 32, 8>(p, B, stream);
   if (p.nb <= 512) return launch_select_tile<D, 32, 16>(p, B, stream);
   if (p.nb <= 1024) return launch_select_tile<D, 32, 32>(p, B, stream);
   if (p.nb <= 2048) return launch_select_tile<D, 16, 64>(p, B, stream);
