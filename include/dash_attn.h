@@ -547,6 +547,17 @@ int dash_attn_sparse_fwd(const void* q, const void* k, const void* v, const long
                          void* stream);
 
 /*
+ * Block-sparse forward without a plan, for single tokens and other short runs of queries: each
+ * query reads its picked keys for itself.  idx as dash_sparse_plan takes it; at most 1024
+ * picks and 65536 blocks.  One launch, no workspace.  The other arguments are those of
+ * dash_attn_sparse_fwd.
+ */
+int dash_attn_sparse_tokens(const void* q, const void* k, const void* v, const long long* strides,
+                            const int* idx, const int* kv_len, const int* q_start, void* o,
+                            float* lse, int B, int H, int Hkv, int Sq, int Sk, int D, int block,
+                            int topk, int causal, float scale, void* stream);
+
+/*
  * Block-sparse backward: dq, dk, dv (fully overwritten; zeros where nothing was attended to)
  * from the forward's o (contiguous) and lse.  strides: q, k, v, dout.
  * work: dash_attn_sparse_work_bytes(..., backward = 1) bytes.

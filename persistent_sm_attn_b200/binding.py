@@ -33,7 +33,8 @@ EXPORTS = ("dash_attn_fwd", "dash_attn_bwd", "dash_attn_sync_status", "dash_stat
            "dash_slot_placement_by_smid", "dash_sched_table_pairs",
            "dash_block_means", "dash_block_select", "dash_sparse_plan_bytes",
            "dash_sparse_plan", "dash_attn_sparse_work_bytes", "dash_attn_sparse_fwd",
-           "dash_attn_sparse_bwd", "dash_ckpt8_pack", "dash_ckpt8_unpack")
+           "dash_attn_sparse_bwd", "dash_attn_sparse_tokens", "dash_ckpt8_pack",
+           "dash_ckpt8_unpack")
 
 
 class DashError(RuntimeError):
@@ -104,6 +105,7 @@ def load(path: str | None = None):
     lib.dash_sparse_plan.argtypes = [vp] * 4 + [i] * 8 + [vp]
     lib.dash_attn_sparse_work_bytes.argtypes = [i] * 9
     lib.dash_attn_sparse_fwd.argtypes = [vp] * 8 + [i] * 9 + [f, vp]
+    lib.dash_attn_sparse_tokens.argtypes = [vp] * 9 + [i] * 9 + [f, vp]
     lib.dash_attn_sparse_bwd.argtypes = [vp] * 12 + [i] * 9 + [f, vp]
     lib.dash_ckpt8_pack.argtypes = [vp, vp, vp, vp, i, vp]
     lib.dash_ckpt8_unpack.argtypes = [vp, vp, vp, vp, i, vp]
@@ -690,6 +692,9 @@ def _expect_plan(plan, shape, device):
         raise ValueError(f"the plan must be on {device}")
 
 
+_TOKEN_RUN = 4  # queries up to which each reads its keys for itself
+
+
 def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=None, scale=None,
                          plan=None, out=None, lse=None, stream=None):
     """O, LSE of attention over the selected blocks: q [B,H,Sq,D], k and v [B,Hkv,Sk,D] (any
@@ -704,6 +709,20 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
         _expect("lse", lse, (B, H, Sq), torch.float32, q.device)
     if plan is None:
         _expect("idx", idx, (B, Hkv, Sq, idx.shape[-1]), torch.int32, q.device)
+        topk, blocks = idx.shape[-1], _block_count(Sk, block)
+        if Sq <= _TOKEN_RUN and topk <= 1024 and blocks <= 65536:
+            n = _expect_rows("kv_len", kv_len, B, q.device)
+            s = _expect_rows("q_start", q_start, B, q.device)
+            with _Launch(q.device, stream) as st:
+                if out is None:
+                    out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+                if lse is None:
+                    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+                _check(load().dash_attn_sparse_tokens(
+                    q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides(q, k, v), idx.data_ptr(), n,
+                    s, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
+                    int(bool(causal)), float(scale or 0.0), st), "dash_attn_sparse_fwd")
+            return out, lse
         plan = dash_sparse_plan(idx, H, Sk, block, causal, kv_len, q_start, stream)
     _expect_plan(plan, (B, H, Hkv, Sq, Sk), q.device)
     lib = load()

@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libdash_attn.so")
 SOURCES = ["dash_api.cu", "noalloc.cu", "sparse_api.cu", "sched.cpp"]
 DEPS = SOURCES + ["sched.h", "internal.h", "ptx.cuh", "bwd_kernel.cuh", "fwd_kernel.cuh",
                   "aux_kernels.cuh", "block_select.cuh", "ckpt8.cuh", "sparse_plan.cuh",
-                  "sparse_fwd.cuh", "sparse_bwd.cuh"]
+                  "sparse_fwd.cuh", "sparse_bwd.cuh", "sparse_token.cuh"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "dash_attn.h")
 
 NVCC_FLAGS = [

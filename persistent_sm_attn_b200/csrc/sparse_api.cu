@@ -19,6 +19,7 @@
 #include "sparse_bwd.cuh"
 #include "sparse_fwd.cuh"
 #include "sparse_plan.cuh"
+#include "sparse_token.cuh"
 
 namespace {
 
@@ -244,6 +245,38 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
         p.part_o, p.part_l, p.o, p.lse, rows, p.splits);
     DASH_CUDA(cudaGetLastError());
   }
+  return DASH_OK;
+}
+
+// CTAs of a cluster that share a token's picks: enough clusters' CTAs for several on each of
+// 148 SMs, and a chunk at least for each of their warps.
+int token_cluster(long long units, int topk, int block) {
+  const long long most = (long long)topk * (block / dash::kTokenKeys) / dash::kTokenWarps;
+  int cs = 1;
+  while (cs < 8 && units * cs < 148 * 6 && 2 * cs <= most) cs *= 2;
+  return cs;
+}
+
+template <int D>
+int launch_sparse_token(dash::SparseTokenParams& p, long long units, cudaStream_t stream) {
+  using C = dash::SparseTokenCfg<D>;
+  const int cs = token_cluster(units, p.topk, p.block);
+  if (units * cs > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
+  auto kern = dash::dash_sparse_token_kernel<D>;
+  const int smem = C::smem(p.topk, p.nb);
+  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * cs));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cs;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  DASH_CUDA(cudaLaunchKernelEx(&cfg, kern, p));
   return DASH_OK;
 }
 
@@ -597,6 +630,49 @@ int dash_attn_sparse_fwd(const void* q, const void* k, const void* v, const long
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return D == 64 ? launch_sparse_fwd<64>(q, k, v, st, s, plan, o, lse, work, scale, cs)
                    : launch_sparse_fwd<128>(q, k, v, st, s, plan, o, lse, work, scale, cs);
+  }, DASH_ERR_OOM, DASH_ERR_INVALID_ARG);
+}
+
+int dash_attn_sparse_tokens(const void* q, const void* k, const void* v, const long long* strides,
+                            const int* idx, const int* kv_len, const int* q_start, void* o,
+                            float* lse, int B, int H, int Hkv, int Sq, int Sk, int D, int block,
+                            int topk, int causal, float scale, void* stream) {
+  return no_throw([&]() -> int {
+    int rc = check_heads(B, H, Hkv, Sq, Sk);
+    if (rc) return rc;
+    if (block < dash::kUnit || block % dash::kUnit != 0 || topk < 1 ||
+        (causal != 0 && causal != 1) || !(scale >= 0.f) || std::isinf(scale))
+      return DASH_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
+    Strides st[3];
+    if ((rc = take_strides(strides, B, H, Sq, D, &st[0])) ||
+        (rc = take_strides(strides ? strides + 3 : nullptr, B, Hkv, Sk, D, &st[1])) ||
+        (rc = take_strides(strides ? strides + 6 : nullptr, B, Hkv, Sk, D, &st[2])))
+      return rc;
+    if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+        !aligned4(idx) || !aligned4_or_null(kv_len) || !aligned4_or_null(q_start))
+      return DASH_ERR_INVALID_ARG;
+    dash::SparseTokenParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.qb = st[0].b, p.qh = st[0].h, p.qs = st[0].s;
+    p.kb = st[1].b, p.kh = st[1].h, p.ks = st[1].s;
+    p.vb = st[2].b, p.vh = st[2].h, p.vs = st[2].s;
+    p.idx = idx;
+    p.kv_len = kv_len;
+    p.q_start = q_start;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.RG = (p.G + 15) / 16;
+    p.Sq = Sq, p.Sk = Sk, p.block = block, p.topk = topk, p.causal = causal;
+    p.nb = (int)(((long long)Sk + block - 1) / block);
+    if (topk > dash::kTokenTopk || p.nb > dash::kTokenBlocks) return DASH_ERR_UNSUPPORTED;
+    p.scale_log2 = scale_or_default(scale, D) * 1.4426950408889634f;
+    const long long units = (long long)B * Hkv * Sq * p.RG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return D == 64 ? launch_sparse_token<64>(p, units, cs) : launch_sparse_token<128>(p, units, cs);
   }, DASH_ERR_OOM, DASH_ERR_INVALID_ARG);
 }
 

@@ -143,3 +143,32 @@ def test_many_tiles_of_a_cta(shape):
             check_fwd(one, o[b:b + 1, hs], lse[b:b + 1, hs], mm)
             check_bwd(one, o[b:b + 1, hs], lse[b:b + 1, hs],
                       (got["dq"][b:b + 1, hs], got["dk"][b:b + 1, h:h + 1], got["dv"][b:b + 1, h:h + 1]), mm)
+
+
+TOKENS = [
+    # B, H, Hkv, Sq, Sk, D, block, topk, causal, ragged
+    (1, 1, 1, 1, 1, 64, 64, 1, True, False),
+    (1, 32, 8, 1, 4096, 128, 64, 16, True, False),
+    (5, 32, 8, 1, 3000, 128, 64, 16, True, True),
+    (70, 16, 8, 1, 700, 64, 128, 3, True, True),      # a CTA for itself
+    (2, 34, 2, 1, 777, 128, 64, 5, True, True),       # 17 heads: two groups of rows
+    (1, 128, 1, 2, 300, 64, 64, 4, True, False),
+    (3, 6, 2, 4, 1000, 128, 256, 2, False, True),
+    (2, 4, 4, 3, 5000, 64, 64, 90, True, True),       # more picks than lanes, repeats across them
+    (1, 7, 1, 1, 200, 128, 64, 1024, True, False),
+]
+
+
+@pytest.mark.parametrize("shape", TOKENS, ids=str)
+def test_tokens_without_a_plan(shape):
+    c = case(*shape[:9], ragged=shape[9], seed=hash(shape) % 1000)
+    if shape[9]:  # what lies past the sequences may be anything
+        for b in range(shape[0]):
+            c["k"][b, :, int(c["kv_len"][b]):] = float("nan")
+            c["v"][b, :, int(c["kv_len"][b]):] = float("inf")
+    o, lse = run_fwd(c)
+    check_fwd(c, o, lse)
+    with_plan = run_fwd(c, plan=make_plan(c))
+    check_fwd(c, *with_plan)
+    again = run_fwd(c)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
