@@ -530,22 +530,23 @@ def dash_trace_bwd(q, k, v, o, do, lse, causal: bool, schedule="shift", stream=N
 
 class _Launch:
     """The device and stream of one call: tensors made inside belong to that stream."""
+    __slots__ = ("_ctx", "_handle")
 
     def __init__(self, device, stream):
         import torch
         self._ctx = None
         if stream is not None:
-            self._ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(device)
-        self._given, self._device = stream, device
+            self._ctx, self._handle = torch.cuda.stream(stream), stream.cuda_stream
+        else:
+            if device.index != torch.cuda.current_device():
+                self._ctx = torch.cuda.device(device)
+            # torch.cuda.current_stream(device).cuda_stream without the two objects (2 us)
+            self._handle = torch._C._cuda_getCurrentRawStream(device.index)
 
     def __enter__(self):
-        import torch
         if self._ctx is not None:
             self._ctx.__enter__()
-        st = self._given if self._given is not None else torch.cuda.current_stream(self._device)
-        return st.cuda_stream
+        return self._handle
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -554,9 +555,9 @@ class _Launch:
 
 def _expect(name, t, shape, dtype, device=None, contiguous=True):
     """Reject what the C entry point would misread: shape, dtype, device, layout."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a CUDA tensor" + (f" on {device}" if device else ""))
@@ -564,14 +565,16 @@ def _expect(name, t, shape, dtype, device=None, contiguous=True):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return
+    if t.data_ptr() % 16 and t.numel():
+        raise ValueError(f"{name} must be 16-byte aligned")
+    if t.is_contiguous():
+        return
     shape, strides = t.shape, t.stride()
     if t.numel() and strides[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     if t.numel() and any(n > 1 and (st < 8 or st % 8) for n, st in zip(shape[:-1], strides[:-1])):
         raise ValueError(f"{name} has strides {tuple(strides)}: positive multiples of 8 are "
                          "needed (no broadcast dimensions)")
-    if t.numel() and t.data_ptr() % 16:
-        raise ValueError(f"{name} must be 16-byte aligned")
 
 
 def _expect_rows(name, t, B, device):
@@ -582,7 +585,16 @@ def _expect_rows(name, t, B, device):
     return None if t is None else t.data_ptr()
 
 
+def _like(t, dtype=None):
+    """An uninitialised contiguous tensor of t's shape and device."""
+    import torch
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _strides(*tensors):
+    """The strides argument: None where all are contiguous."""
+    if all([t.is_contiguous() for t in tensors]):
+        return None
     flat = [st for t in tensors for st in t.stride()[:3]]
     return (ctypes.c_longlong * len(flat))(*flat)
 
@@ -610,7 +622,7 @@ def dash_block_means(k, block, kv_len=None, start=None, out=None, stream=None):
         _expect("out", out, (B, Hkv, nb, D), torch.float32, k.device)
     with _Launch(k.device, stream) as st:
         if out is None:
-            out = torch.empty((B, Hkv, nb, D), dtype=torch.float32, device=k.device)
+            out = k.new_empty((B, Hkv, nb, D), dtype=torch.float32)
         _check(load().dash_block_means(k.data_ptr(), _strides(k), out.data_ptr(), n, s, B, Hkv, Sk,
                                        D, block, st), "dash_block_means")
     return out
@@ -633,7 +645,7 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
         _expect("out", out, (B, Hkv, Sq, topk), torch.int32, q.device)
     with _Launch(q.device, stream) as st:
         if out is None:
-            out = torch.empty((B, Hkv, Sq, max(int(topk), 0)), dtype=torch.int32, device=q.device)
+            out = q.new_empty((B, Hkv, Sq, max(int(topk), 0)), dtype=torch.int32)
         _check(load().dash_block_select(q.data_ptr(), _strides(q), means.data_ptr(), out.data_ptr(),
                                         n, s, B, H, Hkv, Sq, seq_k, D, block, topk,
                                         int(bool(causal)), sink, local, st), "dash_block_select")
@@ -668,7 +680,7 @@ def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start
     lib = load()
     size = _bytes(lib.dash_sparse_plan_bytes(*shape), "dash_sparse_plan")
     with _Launch(idx.device, stream) as st:
-        buf = torch.empty(max(size, 16), dtype=torch.uint8, device=idx.device)
+        buf = idx.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_sparse_plan(idx.data_ptr(), n, s, buf.data_ptr(), *shape, int(bool(causal)),
                                     st), "dash_sparse_plan")
     return SparsePlan(buf, shape, bool(causal))
@@ -715,9 +727,9 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
             s = _expect_rows("q_start", q_start, B, q.device)
             with _Launch(q.device, stream) as st:
                 if out is None:
-                    out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+                    out = _like(q)
                 if lse is None:
-                    lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+                    lse = q.new_empty((B, H, Sq), dtype=torch.float32)
                 _check(load().dash_attn_sparse_tokens(
                     q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides(q, k, v), idx.data_ptr(), n,
                     s, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
@@ -730,10 +742,10 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
                   "dash_attn_sparse_fwd")
     with _Launch(q.device, stream) as st:
         if out is None:
-            out = torch.empty((B, H, Sq, D), dtype=q.dtype, device=q.device)
+            out = _like(q)
         if lse is None:
-            lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
-        work = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+            lse = q.new_empty((B, H, Sq), dtype=torch.float32)
+        work = q.new_empty((size,), dtype=torch.uint8) if size else None
         _check(lib.dash_attn_sparse_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                         _strides(q, k, v), plan.buf.data_ptr(), out.data_ptr(),
                                         lse.data_ptr(), work.data_ptr() if size else None,
@@ -759,10 +771,10 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
     size = _bytes(lib.dash_attn_sparse_work_bytes(*plan.shape[:5], D, *plan.shape[5:], 1),
                   "dash_attn_sparse_bwd")
     with _Launch(q.device, stream) as st:
-        def like(t, shape):
-            return torch.empty(shape, dtype=q.dtype, device=q.device) if t is None else t
-        dq, dk, dv = like(dq, q.shape), like(dk, k.shape), like(dv, k.shape)
-        work = torch.empty(max(size, 16), dtype=torch.uint8, device=q.device)
+        dq = _like(q) if dq is None else dq
+        dk = _like(k) if dk is None else dk
+        dv = _like(k) if dv is None else dv
+        work = q.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_attn_sparse_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
                                         _strides(q, k, v, do), plan.buf.data_ptr(), o.data_ptr(),
                                         lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
@@ -773,6 +785,10 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
 
 
 # ---------------------------------------------------------------- 8-bit checkpoints
+_POINTERS = [ctypes.c_void_p * n for n in range(5)]  # argument arrays of a launch's tensors
+_LONGS = [ctypes.c_longlong * n for n in range(5)]
+
+
 def dash_ckpt8_pack(*tensors, stream=None):
     """8-bit checkpoints of bf16 tensors (contiguous, last dimension a multiple of 32): for
     each a pair (m, e), int8 of the tensor's shape and int8 [..., D // 32]."""
@@ -788,17 +804,16 @@ def dash_ckpt8_pack(*tensors, stream=None):
     pairs = []
     with _Launch(device, stream) as st:
         for x in tensors:
-            pairs.append((torch.empty(x.shape, dtype=torch.int8, device=device),
-                          torch.empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.int8,
-                                      device=device)))
+            pairs.append((_like(x, torch.int8),
+                          x.new_empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.int8)))
         for a in range(0, len(tensors), 4):
             part = pairs[a:a + 4]
             n = len(part)
-            vp = ctypes.c_void_p * n
+            vp = _POINTERS[n]
             _check(load().dash_ckpt8_pack(vp(*[x.data_ptr() for x in tensors[a:a + 4]]),
                                           vp(*[m.data_ptr() for m, _ in part]),
                                           vp(*[e.data_ptr() for _, e in part]),
-                                          (ctypes.c_longlong * n)(*[m.numel() for m, _ in part]),
+                                          _LONGS[n](*[m.numel() for m, _ in part]),
                                           n, st), "dash_ckpt8_pack")
     return pairs
 
@@ -817,15 +832,15 @@ def dash_ckpt8_unpack(*pairs, stream=None):
         _expect(f"e of checkpoint {j}", e, (*m.shape[:-1], m.shape[-1] // 32), torch.int8, device)
     out = []
     with _Launch(device, stream) as st:
-        out = [torch.empty(m.shape, dtype=torch.bfloat16, device=device) for m, _ in pairs]
+        out = [_like(m, torch.bfloat16) for m, _ in pairs]
         for a in range(0, len(pairs), 4):
             part = pairs[a:a + 4]
             n = len(part)
-            vp = ctypes.c_void_p * n
+            vp = _POINTERS[n]
             _check(load().dash_ckpt8_unpack(vp(*[m.data_ptr() for m, _ in part]),
                                             vp(*[e.data_ptr() for _, e in part]),
                                             vp(*[x.data_ptr() for x in out[a:a + 4]]),
-                                            (ctypes.c_longlong * n)(*[m.numel() for m, _ in part]),
+                                            _LONGS[n](*[m.numel() for m, _ in part]),
                                             n, st), "dash_ckpt8_unpack")
     return out
 

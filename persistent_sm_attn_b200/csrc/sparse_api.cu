@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <map>
@@ -63,6 +64,26 @@ int words_for(int dev, void* stream, bool create, unsigned** out) {
   *out = base.first + 2 * it->second;
   return DASH_OK;
 }
+
+// Shared memory a kernel may use, raised once per kernel and device (the call costs a
+// microsecond).  `tag` is the kernel's own array.
+constexpr int kMaxDevices = 64;
+template <class K>
+int allow_smem(K* kern, int bytes, std::atomic<int> (&tag)[kMaxDevices]) {
+  int dev = 0;
+  DASH_CUDA(cudaGetDevice(&dev));
+  if (dev >= kMaxDevices || tag[dev].load(std::memory_order_relaxed) < bytes) {
+    DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < kMaxDevices) tag[dev].store(bytes, std::memory_order_relaxed);
+  }
+  return DASH_OK;
+}
+#define DASH_ALLOW_SMEM(kern, bytes)                      \
+  do {                                                    \
+    static std::atomic<int> allowed[kMaxDevices];         \
+    const int allow_rc = allow_smem(kern, bytes, allowed); \
+    if (allow_rc) return allow_rc;                        \
+  } while (0)
 
 // ------------------------------------------------------------------ checks
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -237,7 +258,7 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
   const long long grid = (long long)s.B * s.Hkv * s.NT * p.splits;
   if (grid > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
   auto kern = dash::dash_sparse_fwd_kernel<D>;
-  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes));
+  DASH_ALLOW_SMEM(kern, C::kSmemBytes);
   kern<<<(unsigned)grid, C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, p);
   DASH_CUDA(cudaGetLastError());
   if (p.splits > 1) {
@@ -248,12 +269,13 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
   return DASH_OK;
 }
 
-// CTAs of a cluster that share a token's picks: enough clusters' CTAs for several on each of
-// 148 SMs, and a chunk at least for each of their warps.
+// CTAs of a cluster that share a token's picks: more than one while there are fewer clusters
+// than SMs, with a chunk at least for each warp.  (64 tokens of 8 K/V heads, 16 picks of 64:
+// 53 us with one CTA, 68 with two, 89 with four; one token: 8.7 us with eight.)
 int token_cluster(long long units, int topk, int block) {
   const long long most = (long long)topk * (block / dash::kTokenKeys) / dash::kTokenWarps;
   int cs = 1;
-  while (cs < 8 && units * cs < 148 * 6 && 2 * cs <= most) cs *= 2;
+  while (cs < 8 && units * cs < 148 && 2 * cs <= most) cs *= 2;
   return cs;
 }
 
@@ -264,7 +286,7 @@ int launch_sparse_token(dash::SparseTokenParams& p, long long units, cudaStream_
   if (units * cs > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
   auto kern = dash::dash_sparse_token_kernel<D>;
   const int smem = C::smem(p.topk, p.nb);
-  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  DASH_ALLOW_SMEM(kern, smem);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * cs));
   cfg.blockDim = dim3(C::kThreads);
@@ -364,7 +386,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   a.scale_log2 = sc * 1.4426950408889634f;
   a.spin_ns = spin;
   auto kq = dash::dash_sparse_dq_kernel<D>;
-  DASH_CUDA(cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, Cq::kSmemBytes));
+  DASH_ALLOW_SMEM(kq, Cq::kSmemBytes);
   kq<<<std::min(sms, a.tiles), Cq::kThreads, Cq::kSmemBytes, stream>>>(tq, tdo, tk, tv, a);
   DASH_CUDA(cudaGetLastError());
 
@@ -413,7 +435,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   c.scale_log2 = a.scale_log2;
   c.spin_ns = spin;
   auto kk = dash::dash_sparse_dkdv_kernel<D>;
-  DASH_CUDA(cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, Ck::kSmemBytes));
+  DASH_ALLOW_SMEM(kk, Ck::kSmemBytes);
   kk<<<sms, Ck::kThreads, Ck::kSmemBytes, stream>>>(tk, tv, c);
   DASH_CUDA(cudaGetLastError());
 
@@ -456,7 +478,7 @@ int launch_select_tile(const dash::SelectParams& p, int B, cudaStream_t stream) 
   using C = dash::SelectCfg<D, QT>;
   auto kern = dash::dash_block_select_kernel<D, QT, NL>;
   const int smem = C::smem(p.nb);
-  DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  DASH_ALLOW_SMEM(kern, smem);
   kern<<<dim3((p.Sq + QT - 1) / QT, B * p.Hkv), C::kThreads, smem, stream>>>(p);
   DASH_CUDA(cudaGetLastError());
   return DASH_OK;
@@ -588,7 +610,7 @@ int dash_sparse_plan(const int* idx, const int* kv_len, const int* q_start, void
     p.pres = reinterpret_cast<uint32_t*>(at + p.s.off_pres);
     const int smem = p.s.nu * p.s.W * 4;
     auto kern = dash::dash_sparse_plan_kernel;
-    DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024));
+    DASH_ALLOW_SMEM(kern, 200 * 1024);
     kern<<<(unsigned)((long long)B * Hkv * p.s.NT), 128, smem, static_cast<cudaStream_t>(stream)>>>(p);
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
