@@ -468,9 +468,10 @@ int ckpt_params(const void* const* src, void* const* dst, signed char* const* ex
   }
   return DASH_OK;
 }
-// 8 elements a thread; at most 16 CTAs of 256 threads for each of 148 SMs, then a stride
+// 8 elements a piece, four pieces a thread; at most 32 CTAs of 256 threads for each of 148
+// SMs, then a stride
 unsigned ckpt_grid(const dash::CkptParams& p) {
-  return (unsigned)std::min((p.groups[p.n] * 4 + 255) / 256, 148LL * 16);
+  return (unsigned)std::min((p.groups[p.n] * 4 + 1023) / 1024, 148LL * 32);
 }
 
 template <int D, int QT, int NL>
