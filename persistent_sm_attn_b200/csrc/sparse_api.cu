@@ -235,7 +235,7 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
   int rc = words_for(dev, stream, true, &words);
   if (rc) return rc;
   CUtensorMap tq, tk, tv;
-  if ((rc = make_tmap4(&tq, q, s.B, s.H, s.Sq, D, st[0], s.T, s.G)) ||
+  if ((rc = make_tmap4_rows(&tq, q, s.B, s.H, s.Sq, D, st[0], s.T, s.G)) ||
       (rc = make_tmap4(&tk, k, s.B, s.Hkv, s.Sk, D, st[1], dash::kUnit, 1)) ||
       (rc = make_tmap4(&tv, v, s.B, s.Hkv, s.Sk, D, st[2], dash::kUnit, 1)))
     return rc;
