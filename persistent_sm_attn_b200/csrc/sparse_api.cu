@@ -397,8 +397,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   iv.token = reinterpret_cast<int*>(base + w.off_token);
   iv.nu = s.nu, iv.NW = s.NW, iv.NT = s.NT, iv.T = s.T, iv.U = s.U, iv.W = s.W;
   iv.units = w.units;
-  const unsigned inverse_grid = (unsigned)((w.units + 3) / 4);
-  dash::dash_sparse_inverse_kernel<false><<<inverse_grid, 128, 0, stream>>>(iv);
+  dash::dash_sparse_count_kernel<<<(unsigned)((w.units + 3) / 4), 128, 0, stream>>>(iv);
   DASH_CUDA(cudaGetLastError());
 
   dash::ItemParams im{};
@@ -411,7 +410,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   im.units = w.units;
   dash::dash_sparse_items_kernel<<<1, 1024, 0, stream>>>(im);
   DASH_CUDA(cudaGetLastError());
-  dash::dash_sparse_inverse_kernel<true><<<inverse_grid, 128, 0, stream>>>(iv);
+  dash::dash_sparse_fill_kernel<<<(unsigned)w.units, 128, 0, stream>>>(iv);
   DASH_CUDA(cudaGetLastError());
 
   dash::SparseDkvParams c{};

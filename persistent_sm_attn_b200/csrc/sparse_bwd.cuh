@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(384, 1)
 
 // ------------------------------------------------------------------ who reads a unit
 // For every unit the tokens that picked it and see it, ascending: counted, given a place by
-// prefix sums, written.  A warp per unit, a lane per query tile.
+// prefix sums, written.
 struct InverseParams {
   PlanView plan;
   int* count;  // [units] tokens of the unit
@@ -485,60 +485,81 @@ struct InverseParams {
   int nu, NW, NT, T, U, W;
   long long units;  // B*Hkv*nu
 };
-template <bool kFill>
+// The tokens of query tile t that picked unit u, as a mask.
+__device__ __forceinline__ void unit_tokens(const InverseParams& p, long long bh, int u, int t,
+                                            uint32_t (&m)[4]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) m[x] = 0u;  // T <= 128 tokens
+  if (t >= p.NT) return;
+  const long long at = (bh * p.NT + t) * p.NW + (u >> 5);
+  const uint32_t w = p.plan.pres[at];
+  if (!((w >> (u & 31)) & 1u)) return;
+  const int place = p.plan.pre[at] + __popc(w & ((1u << (u & 31)) - 1u));
+  const uint32_t* mask = p.plan.mask + ((bh * p.NT + t) * p.U + place) * p.W;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (x < p.W) m[x] = mask[x];
+}
+// A warp per unit, a lane per query tile.
 __global__ void __launch_bounds__(128)
-    dash_sparse_inverse_kernel(const __grid_constant__ InverseParams p) {
+    dash_sparse_count_kernel(const __grid_constant__ InverseParams p) {
   const long long gu = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (gu >= p.units) return;
   const int lane = threadIdx.x & 31;
-  const long long bh = gu / p.nu;
-  const int u = (int)(gu % p.nu);
-  const uint32_t* pres = p.plan.pres + bh * p.NT * p.NW + (u >> 5);
-  const int* pre = p.plan.pre + bh * p.NT * p.NW + (u >> 5);
-  int* out = kFill ? p.token + p.off[gu] : nullptr;
   int n = 0;
   for (int t0 = 0; t0 < p.NT; t0 += 32) {
-    const int t = t0 + lane;
-    const uint32_t w = t < p.NT ? pres[(long long)t * p.NW] : 0u;
-    const bool on = (w >> (u & 31)) & 1u;
-    uint32_t m[4] = {0u, 0u, 0u, 0u};  // T <= 128 tokens
-    if (on) {
-      const int place = pre[(long long)t * p.NW] + __popc(w & ((1u << (u & 31)) - 1u));
-      const uint32_t* mask = p.plan.mask + ((bh * p.NT + t) * p.U + place) * p.W;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (x < p.W) m[x] = mask[x];
-    }
-    const int mine = __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
-    if constexpr (kFill) {
-      int before = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
-      }
-      const int all = __shfl_sync(0xffffffffu, before, 31);
-      int at = n + before - mine;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        for (uint32_t rest = m[x]; rest; rest &= rest - 1)
-          out[at++] = t * p.T + 32 * x + __ffs(rest) - 1;
-      n += all;
-    } else {
-      n += mine;
-    }
+    uint32_t m[4];
+    unit_tokens(p, gu / p.nu, (int)(gu % p.nu), t0 + lane, m);
+    n += __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
   }
-  if constexpr (!kFill) {
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) p.count[gu] = n;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) p.count[gu] = n;
+}
+// A CTA per unit, 128 tiles at a time: a thread looks its tile up, a warp writes the tokens of
+// its 32 tiles one mask word after the other, a lane per token.
+__global__ void __launch_bounds__(128)
+    dash_sparse_fill_kernel(const __grid_constant__ InverseParams p) {
+  __shared__ int warp_n[4];
+  const long long gu = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int left = p.count[gu];
+  int* out = p.token + p.off[gu];
+  for (int t0 = 0; left > 0 && t0 < p.NT; t0 += 128) {
+    uint32_t m[4];
+    unit_tokens(p, gu / p.nu, (int)(gu % p.nu), t0 + tid, m);
+    const int mine = __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
+    const int all = __reduce_add_sync(0xffffffffu, mine);
+    __syncthreads();
+    if (lane == 0) warp_n[warp] = all;
+    __syncthreads();
+    int at = 0;
+    for (int w = 0; w < warp; ++w) at += warp_n[w];
+    for (unsigned on = __ballot_sync(0xffffffffu, mine > 0); on; on &= on - 1) {
+      const int src = __ffs(on) - 1, token0 = (t0 + warp * 32 + src) * p.T;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x >= p.W) break;
+        const uint32_t word = __shfl_sync(0xffffffffu, m[x], src);
+        if ((word >> lane) & 1u) out[at + __popc(word & ((1u << lane) - 1u))] = token0 + 32 * x + lane;
+        at += __popc(word);
+      }
+    }
+    const int round = warp_n[0] + warp_n[1] + warp_n[2] + warp_n[3];
+    out += round;
+    left -= round;
   }
 }
 
 // Items of the dK/dV pass: every picked unit, its tokens in tiles of T, cut into stretches of
-// at most C tiles with C = max(4, total / kStretches).  Whole stretches come first, so that
-// the CTAs that take items in turn get equally many of them.
-constexpr int kStretches = 148 * 8;
+// at most C tiles with C = max(4, total / kStretches).  The longest come first and the CTAs
+// take them in turns that go to and fro (snake_item), so that all get nearly the same number
+// of tiles.  Fewer and longer stretches would balance less well, more write more partials.
+constexpr int kStretches = 148 * 4;
 constexpr int kMinStretch = 4;
+__device__ __forceinline__ int snake_item(int k) {
+  const int x = (int)blockIdx.x, g = (int)gridDim.x;
+  return k * g + ((k & 1) ? g - 1 - x : x);
+}
 
 struct SparseItem {
   int unit, first, end, slot;   // unit, tiles, partial slot or -1
@@ -553,72 +574,94 @@ struct ItemParams {
   int T, nu, Hkv;
   long long units;
 };
-// One CTA: sums, then exclusive prefix sums of the tokens, items and partial slots per unit.
+// One CTA: sums, a histogram of the stretches' lengths, then exclusive prefix sums of the
+// tokens and partial slots per unit.
 __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParams p) {
+  constexpr int kHeld = 8192, kBuckets = 64;
+  __shared__ int held[kHeld];  // the first units' counts
   __shared__ long long sum[32];
-  __shared__ int pre[4][32];
+  __shared__ int pre[2][32];
+  __shared__ int bucket[kBuckets];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto block_sum = [&](auto&& f) {
-    long long s = 0;
-    for (long long x = tid; x < p.units; x += 1024) s += f((p.count[x] + p.T - 1) / p.T);
+  auto count = [&](long long x) { return x < kHeld ? held[x] : p.count[x]; };
+  long long s = 0;
+  for (long long x = tid; x < p.units; x += 1024) {
+    const int n = p.count[x];
+    if (x < kHeld) held[x] = n;
+    s += (n + p.T - 1) / p.T;
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncthreads();
-    if (lane == 0) sum[warp] = s;
-    __syncthreads();
-    long long t = sum[lane];
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) sum[warp] = s;
+  if (tid < kBuckets) bucket[tid] = 0;
+  __syncthreads();
+  long long total = sum[lane];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
-  };
-  const long long total = block_sum([](int n) { return n; });
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int C = (int)max((long long)kMinStretch, (total + kStretches - 1) / kStretches);
-  const int whole = (int)block_sum([&](int n) { return n / C; });
-  int base[4] = {0, whole, 0, 0};  // whole stretches, rests, slots, tokens
+  // bucket 0 holds whole stretches, bucket 63 the shortest rests
+  auto rest_bucket = [&](int rest) { return kBuckets - 1 - (int)((long long)rest * (kBuckets - 1) / C); };
+  for (long long x = tid; x < p.units; x += 1024) {
+    const int n = (count(x) + p.T - 1) / p.T;
+    if (n / C > 0) atomicAdd(&bucket[0], n / C);
+    if (n % C > 0) atomicAdd(&bucket[rest_bucket(n % C)], 1);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int at = 0;
+    for (int k = 0; k < kBuckets; ++k) {
+      const int n = bucket[k];
+      bucket[k] = at;
+      at += n;
+    }
+    p.head[0] = at;
+    p.head[1] = C;
+  }
+  __syncthreads();
+  int base[2] = {0, 0};  // slots, tokens
   for (long long x0 = 0; x0 < p.units; x0 += 1024) {
     const long long x = x0 + tid;
-    const int tokens = x < p.units ? p.count[x] : 0;
+    const int tokens = x < p.units ? count(x) : 0;
     const int n = (tokens + p.T - 1) / p.T;
     const int full = n / C, rest = n % C > 0, cut = full + rest > 1 ? full + rest : 0;
-    const int own[4] = {full, rest, cut, tokens};
-    int inc[4] = {full, rest, cut, tokens};  // inclusive prefix sums over the warp
+    const int own[2] = {cut, tokens};
+    int inc[2] = {cut, tokens};  // inclusive prefix sums over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const int y = __shfl_up_sync(0xffffffffu, inc[k], o);
         if (lane >= o) inc[k] += y;
       }
     if (lane == 31)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pre[k][warp] = inc[k];
+      for (int k = 0; k < 2; ++k) pre[k][warp] = inc[k];
     __syncthreads();
-    int at[4];
+    int at[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int y = pre[k][lane];
       at[k] = base[k] + __reduce_add_sync(0xffffffffu, lane < warp ? y : 0) + inc[k] - own[k];
       base[k] += __reduce_add_sync(0xffffffffu, y);
     }
     if (x < p.units) {
-      p.off[x] = at[3];
-      p.slot0[x] = n == 0 ? -2 : cut ? at[2] : -1;
+      p.off[x] = at[1];
+      p.slot0[x] = n == 0 ? -2 : cut ? at[0] : -1;
       SparseItem w;
       w.unit = (int)x;
-      w.off = at[3], w.tokens = tokens;
+      w.off = at[1], w.tokens = tokens;
       w.bh = (int)(x / p.nu);
       w.b = w.bh / p.Hkv;
+      // places within a bucket go by whoever asks first: they decide only who computes an item
+      int place = full > 0 ? atomicAdd(&bucket[0], full) : 0;
       for (int k = 0; k < full + rest; ++k) {
+        if (k == full) place = atomicAdd(&bucket[rest_bucket(n % C)], 1);
         w.first = k * C, w.end = min(n, (k + 1) * C);
-        w.slot = cut ? at[2] + k : -1;
-        p.item[k < full ? at[0] + k : at[1]] = w;
+        w.slot = cut ? at[0] + k : -1;
+        p.item[place++] = w;
       }
     }
     __syncthreads();
-  }
-  if (tid == 0) {
-    p.head[0] = base[1];
-    p.head[1] = C;
   }
 }
 
@@ -765,14 +808,14 @@ __global__ void __launch_bounds__(640, 1)
       const int at = e * p.T + t;
       return t < p.T && at < w.tokens ? p.token[w.off + at] : -1;
     };
-    if ((int)blockIdx.x < items) {
-      w = p.item[blockIdx.x];
+    if (snake_item(0) < items) {
+      w = p.item[snake_item(0)];
       token = look(w, w.first);
     }
-    for (int i = blockIdx.x; i < items; i += gridDim.x) {
-      const bool more = i + (int)gridDim.x < items;
+    for (int k = 0; snake_item(k) < items; ++k) {
+      const bool more = snake_item(k + 1) < items;
       SparseItem nw = w;
-      if (more) nw = p.item[i + gridDim.x];
+      if (more) nw = p.item[snake_item(k + 1)];
       const int b = w.b, hk = w.bh - b * p.Hkv;
       const __nv_bfloat16* head = src + b * sB + (long long)hk * p.G * sH;
       for (int e = w.first; e < w.end; ++e, ++it) {
@@ -800,8 +843,8 @@ __global__ void __launch_bounds__(640, 1)
   } else if (warp == 9 && lane == 0) {
     // ---------------------------------------------------------------- K and V
     int k = 0;
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
-      const SparseItem w = p.item[i];
+    for (; snake_item(k) < items; ++k) {
+      const SparseItem w = p.item[snake_item(k)];
       const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
       // K and V of item k - 2 are read to the end; nothing is loaded once a wait has run out
       if (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2))) break;
@@ -824,8 +867,8 @@ __global__ void __launch_bounds__(640, 1)
     int j = 0, k = 0, s = 0;
     uint32_t sph = 0;
 #pragma unroll 1
-    for (int i = blockIdx.x; i < items && ok; i += gridDim.x, ++k) {
-      const int first = p.item[i].first, end = p.item[i].end;
+    for (; snake_item(k) < items && ok; ++k) {
+      const int first = p.item[snake_item(k)].first, end = p.item[snake_item(k)].end;
       if (warp == 8) {
         constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
         const uint32_t kK = sdesc_lo(sK(k), 16), kV = sdesc_lo(sV(k), 16);
@@ -917,14 +960,14 @@ __global__ void __launch_bounds__(640, 1)
     };
     int it = 0, k = 0;
     SparseItem w;
-    if ((int)blockIdx.x < items) {
-      w = p.item[blockIdx.x];
+    if (snake_item(0) < items) {
+      w = p.item[snake_item(0)];
       fetch(w, w.first);
     }
-    for (int i = blockIdx.x; i < items; i += gridDim.x, ++k) {
-      const bool more = i + (int)gridDim.x < items;
+    for (; snake_item(k) < items; ++k) {
+      const bool more = snake_item(k + 1) < items;
       SparseItem nw = w;
-      if (more) nw = p.item[i + gridDim.x];
+      if (more) nw = p.item[snake_item(k + 1)];
       for (int e = w.first; e < w.end; ++e, ++it) {
         const float l2 = lse2, dl = delta;
         const int v = vis - 32 * wg;
