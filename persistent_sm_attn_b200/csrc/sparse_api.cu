@@ -336,6 +336,15 @@ BwdWork bwd_work(const PlanShape& s, int D) {
 template <int D>
 constexpr int kUnitElems = dash::kUnit * D;
 
+// Whether dS keeps a second bf16 part.  Delta comes from the rounded O, and where a query
+// attends to few keys O is large against the terms of dS: the errors of dQ and dK are then
+// 0.0026 of their norms (D = 64, 300 keys) in place of 0.0020 with the second part, the
+// rounding of the result itself being 0.0017.  At 1024 keys and more they are 0.0024, and the
+// second part costs 13 % of a pass of 16k keys, 1024 of them picked.
+bool sparse_low_part(const PlanShape& s) {
+  return std::min((long long)s.Sk, (long long)s.topk * s.block) <= 768;
+}
+
 template <int D>
 int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* dout,
                       const Strides* st, const PlanShape& s, const void* plan, const void* o,
@@ -385,8 +394,10 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   a.scale = sc;
   a.scale_log2 = sc * 1.4426950408889634f;
   a.spin_ns = spin;
-  auto kq = dash::dash_sparse_dq_kernel<D>;
-  DASH_ALLOW_SMEM(kq, Cq::kSmemBytes);
+  const bool low = sparse_low_part(s);
+  auto kq = low ? dash::dash_sparse_dq_kernel<D, true> : dash::dash_sparse_dq_kernel<D, false>;
+  if (low) DASH_ALLOW_SMEM(kq, Cq::kSmemBytes);
+  else DASH_ALLOW_SMEM(kq, Cq::kSmemBytes);
   kq<<<std::min(sms, a.tiles), Cq::kThreads, Cq::kSmemBytes, stream>>>(tq, tdo, tk, tv, a);
   DASH_CUDA(cudaGetLastError());
 
@@ -433,8 +444,10 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   c.scale = sc;
   c.scale_log2 = a.scale_log2;
   c.spin_ns = spin;
-  auto kk = dash::dash_sparse_dkdv_kernel<D>;
-  DASH_ALLOW_SMEM(kk, Ck::kSmemBytes);
+  auto kk = D == 64 && low ? dash::dash_sparse_dkdv_kernel<D, D == 64>
+                           : dash::dash_sparse_dkdv_kernel<D, false>;
+  if (low) DASH_ALLOW_SMEM(kk, Ck::kSmemBytes);
+  else DASH_ALLOW_SMEM(kk, Ck::kSmemBytes);
   kk<<<sms, Ck::kThreads, Ck::kSmemBytes, stream>>>(tk, tv, c);
   DASH_CUDA(cudaGetLastError());
 

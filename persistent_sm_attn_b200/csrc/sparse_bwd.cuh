@@ -103,7 +103,10 @@ struct SparseDqCfg {
 // picks of 64, and 408 us at 8 heads of 16k, D = 64, 8 picks of 128: exponentials and the
 // rest took turns.)  Row t G + g of a tile is token t, head g, so a warp holds few tokens and
 // skips the exponentials of units that none of them picked.
-template <int D>
+//
+// kLow: dS enters its product as the sum of two bf16 values instead of one, whose rounding of
+// up to 2^-8 is otherwise the larger part of the result's error; see sparse_low_part.
+template <int D, bool kLow>
 __global__ void __launch_bounds__(384, 1)
     dash_sparse_dq_kernel(const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmDO,
@@ -140,7 +143,6 @@ __global__ void __launch_bounds__(384, 1)
   auto S_READ = [&](int j) { return bar2 + 16u + 8u * (uint32_t)(j & 1); };
   auto DP_FULL = [&](int j) { return bar2 + 32u + 8u * (uint32_t)(j & 1); };
   auto DP_READ = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j & 1); };
-  // four buffers of dS: unit j + 4 waits for the product of unit j
   auto DS_READY = [&](int j) { return bar2 + 64u + 8u * (uint32_t)(j & 3); };
   const uint32_t FINAL = bar2 + 96;
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
@@ -314,14 +316,14 @@ __global__ void __launch_bounds__(384, 1)
         for (int e = 0; e < n && ok; ++e) {
           const int j = j0 + e;
           const uint32_t mK = sdesc_lo(sK(j), 8192);
-          const uint32_t tDS = tmem + C::TM_DS + 32u * (uint32_t)(j & 3);
+          const uint32_t tDS = tmem + C::TM_DS + (kLow ? 64u * (uint32_t)(j & 1) : 32u * (uint32_t)(j & 3));
           ok = wait(DS_READY(j), (uint32_t)((j >> 2) & 1));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kUnit / 16; ++kk)
-              tc_mma_ts_w(tDQ, tDS + 8 * kk, mK + kk * 128, hi, ID_Q, (uint32_t)(e + kk));
+            for (int kk = 0; kk < (kLow ? 2 : 1) * kUnit / 16; ++kk)  // high, then low parts
+              tc_mma_ts_w(tDQ, tDS + 8 * kk, mK + (kk % 4) * 128, hi, ID_Q, (uint32_t)(e + kk));
             tc_commit(K_EMPTY(j));
             if (e + 1 == n) tc_commit(DONE(k));
           }
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(384, 1)
         const bool clean = __all_sync(0xffffffffu, v >= kUnit || v <= 0);
         const uint32_t keep = v > 0 ? 0xffffffffu : 0u;
         const uint32_t tS = tmem + lane_off + C::TM_S + 128u * h, tDP = tS + 64;
-        const uint32_t tDS = tmem + lane_off + C::TM_DS + 32u * (uint32_t)(j & 3);
+        const uint32_t tDS = tmem + lane_off + C::TM_DS + (kLow ? 64u * h : 32u * (uint32_t)(j & 3));
         float pr[kUnit];
         wait(S_FULL(j), ph2(j));
         tc_fence_after();
@@ -408,13 +410,14 @@ __global__ void __launch_bounds__(384, 1)
           }
           fence_proxy_async_smem();
         }
-        if (j >= 4) wait(K_EMPTY(j - 4), phK(j - 4));  // dS of unit j - 4 has been used
+        constexpr int kBack = kLow ? 2 : 4;  // dS has two buffers of two parts or four of one
+        if (j >= kBack) wait(K_EMPTY(j - kBack), phK(j - kBack));
         wait(DP_FULL(j), ph2(j));
         tc_fence_after();
         if (any) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            uint32_t dp[32], pk[16];
+            uint32_t dp[32], pk[16], low[16];
             tmem_ld32(tDP + 32 * c, dp);
             if (c == 1) {
               tc_fence_before();
@@ -429,15 +432,20 @@ __global__ void __launch_bounds__(384, 1)
                 if (32 * c + 2 * x >= v) d0 = 0.f;
                 if (32 * c + 2 * x + 1 >= v) d1 = 0.f;
               }
-              pk[x] = pack_bf16x2(d0, d1) & keep;
+              const uint32_t high = pack_bf16x2(d0, d1);
+              pk[x] = high & keep;
+              if (kLow)
+                low[x] = pack_bf16x2(d0 - __uint_as_float(high << 16),
+                                     d1 - __uint_as_float(high & 0xffff0000u)) & keep;
             }
             tmem_st16(tDS + 16 * c, pk);
+            if (kLow) tmem_st16(tDS + 32 + 16 * c, low);
           }
         } else {
           warp_arrive(DP_READ(j), lane);
           const uint32_t zero[16] = {};
-          tmem_st16(tDS, zero);
-          tmem_st16(tDS + 16, zero);
+#pragma unroll
+          for (int c = 0; c < (kLow ? 4 : 2); ++c) tmem_st16(tDS + 16 * c, zero);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -693,7 +701,7 @@ struct SparseDkvCfg {
   static constexpr int OFF_QDO = 0;  // per stage dO, then Q: at D = 64 one [dO | Q] operand
   static constexpr int OFF_KV = kStages * 2 * kTile;  // two of K, then V
   static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS
-  static constexpr int OFF_BAR = OFF_P + 2 * kP;
+  static constexpr int OFF_BAR = OFF_P + (D == 64 ? 3 : 2) * kP;  // D = 64: and dS's low part
   static constexpr int kBars = 4 * kStages + 6 + 7;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
@@ -713,8 +721,9 @@ struct SparseDkvCfg {
 // upper half of one product, dK^T the lower of the other.  S and dP of the next tile, K and V
 // and the accumulators of the next item have buffers of their own, so that the products of
 // one tile run under the exponentials of the other, also from item to item.  The two softmax
-// warpgroups take 32 keys of every row each.
-template <int D>
+// warpgroups take 32 keys of every row each.  kLow (D = 64, where shared memory has room): as
+// in the dQ kernel.
+template <int D, bool kLow>
 __global__ void __launch_bounds__(640, 1)
     dash_sparse_dkdv_kernel(const __grid_constant__ CUtensorMap tmK,
                             const __grid_constant__ CUtensorMap tmV,
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(640, 1)
   auto sQ = [&](int s) { return sDO(s) + C::kTile; };
   auto sK = [&](int k) { return sb + C::OFF_KV + (uint32_t)((k & 1) * 2 * C::kKV); };
   auto sV = [&](int k) { return sK(k) + C::kKV; };
-  const uint32_t sP = sb + C::OFF_P, sS = sP + C::kP;
+  const uint32_t sP = sb + C::OFF_P, sS = sP + C::kP, sL = sS + C::kP;
   const uint32_t bar0 = sb + C::OFF_BAR;
   // per stage (Q, dO), per item parity, per tile parity
   auto FULL = [&](int x, int s) { return bar0 + 8u * (uint32_t)(x * ST + s); };
@@ -901,7 +910,7 @@ __global__ void __launch_bounds__(640, 1)
         }
       } else {
         constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
-        const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384);
+        const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384), bL = sdesc_lo(sL, 16384);
         const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
         // the accumulators of item k - 2 must have been read
         if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
@@ -921,6 +930,10 @@ __global__ void __launch_bounds__(640, 1)
             for (int kk = 0; kk < 8; ++kk)
               tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
                           (uint32_t)(e - first + kk));
+            if (kLow)
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ss_w(tA + 64, aK + kk * 128, bL + kk * 128, hi, ID_T, 1u);
             if (D == 64) tc_commit(EMPTY(1, s));
             tc_commit(EMPTY(0, s));
             tc_commit(PDS_FREE);
@@ -938,7 +951,7 @@ __global__ void __launch_bounds__(640, 1)
     const int r = quarter * 32 + lane;
     const int t = (int)((uint32_t)r * inv_g >> 16), g = r - t * p.G;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t rowP = sP + r * 128, rowS = sS + r * 128;
+    const uint32_t rowP = sP + r * 128, rowS = sS + r * 128, rowL = sL + r * 128;
     const float sl2 = p.scale_log2;
     // what this thread's row of a tile needs, fetched one tile ahead
     float lse2 = 0.f, delta = 0.f;
@@ -987,7 +1000,7 @@ __global__ void __launch_bounds__(640, 1)
             tc_fence_before();
             warp_arrive(SDP_READ(it), lane);
           }
-          uint32_t pp[8], ds[8];
+          uint32_t pp[8], ds[8], low[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             float p0, p1, d0, d1;
@@ -1002,6 +1015,9 @@ __global__ void __launch_bounds__(640, 1)
             }
             pp[x] = pack_bf16x2(p0, p1);
             ds[x] = pack_bf16x2(d0, d1);
+            if (kLow)
+              low[x] = pack_bf16x2(d0 - __uint_as_float(ds[x] << 16),
+                                   d1 - __uint_as_float(ds[x] & 0xffff0000u));
           }
           if (h == 0 && it > 0) wait(PDS_FREE, (uint32_t)((it - 1) & 1));
 #pragma unroll
@@ -1009,6 +1025,8 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t off = (uint32_t)(((4 * wg + 2 * h + x) ^ (r & 7)) << 4);
             st_shared_v4(rowP + off, pp[4 * x], pp[4 * x + 1], pp[4 * x + 2], pp[4 * x + 3]);
             st_shared_v4(rowS + off, ds[4 * x], ds[4 * x + 1], ds[4 * x + 2], ds[4 * x + 3]);
+            if (kLow)
+              st_shared_v4(rowL + off, low[4 * x], low[4 * x + 1], low[4 * x + 2], low[4 * x + 3]);
           }
         }
         fence_proxy_async_smem();
