@@ -11,6 +11,9 @@ _BINDING_NAMES = {
     "dash_attn_fwd", "dash_attn_bwd", "dash_attn_sync_status", "dash_status_string",
     "dash_sched_simulate", "dash_sched_table", "dash_dag_longest_path", "dash_set_spin_limit_us",
     "dash_bwd_num_ctas", "dash_release_workspace", "dash_profile_begin", "dash_profile_end", "dash_trace_bwd", "dash_attn_bwd_noalloc", "dash_inject_fault", "SCHEDULES", "DashError", "load",
+    "dash_block_means", "dash_block_select", "SparsePlan", "dash_sparse_plan",
+    "dash_attn_sparse_fwd", "dash_attn_sparse_bwd", "dash_attn_sparse_bwd_ckpt8",
+    "dash_ckpt8_pack", "dash_ckpt8_unpack", "dash_attn_bwd_ckpt8",
 }
 
 

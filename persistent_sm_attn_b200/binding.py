@@ -536,6 +536,8 @@ class _Launch:
         import torch
         self._ctx = None
         if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
             self._ctx, self._handle = torch.cuda.stream(stream), stream.cuda_stream
         else:
             if device.index != torch.cuda.current_device():
@@ -654,10 +656,18 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
 
 class SparsePlan:
     """A selection prepared by dash_sparse_plan for the forward and the backward."""
-    __slots__ = ("buf", "shape", "causal")
+    __slots__ = ("buf", "shape", "causal", "stream")
 
-    def __init__(self, buf, shape, causal):
+    def __init__(self, buf, shape, causal, stream):
         self.buf, self.shape, self.causal = buf, shape, causal  # shape: B,H,Hkv,Sq,Sk,block,topk
+        self.stream = stream  # handle of the stream the plan was made on
+
+    def on(self, stream):
+        """The plan's address for work on `stream` (a handle); the memory outlives that work."""
+        if stream != self.stream:
+            import torch
+            self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
+        return self.buf.data_ptr()
 
 
 def _bytes(n, what):
@@ -683,7 +693,7 @@ def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start
         buf = idx.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_sparse_plan(idx.data_ptr(), n, s, buf.data_ptr(), *shape, int(bool(causal)),
                                     st), "dash_sparse_plan")
-    return SparsePlan(buf, shape, bool(causal))
+    return SparsePlan(buf, shape, bool(causal), st)
 
 
 def _expect_qkv(q, k, v):
@@ -704,7 +714,13 @@ def _expect_plan(plan, shape, device):
         raise ValueError(f"the plan must be on {device}")
 
 
-_TOKEN_RUN = 4  # queries up to which each reads its keys for itself
+def _few_queries(B, H, Hkv, Sq):
+    """Whether each query reads its keys for itself, without a plan: single tokens, and short
+    runs while a token of a K/V head (16 query heads at a time) leaves most SMs free.  With 8
+    K/V heads, 16 picks of 64 keys, D = 128, 16 queries of one sequence take 16 us (21 with a
+    plan), 32 take 24 (24); one token of 64 sequences takes 54 us (53, and two more launches),
+    two take 97 (74)."""
+    return Sq == 1 or B * Hkv * Sq * -(-(H // max(Hkv, 1)) // 16) <= 256
 
 
 def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=None, scale=None,
@@ -722,7 +738,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
     if plan is None:
         _expect("idx", idx, (B, Hkv, Sq, idx.shape[-1]), torch.int32, q.device)
         topk, blocks = idx.shape[-1], _block_count(Sk, block)
-        if Sq <= _TOKEN_RUN and topk <= 1024 and blocks <= 65536:
+        if _few_queries(B, H, Hkv, Sq) and topk <= 1024 and blocks <= 65536:
             n = _expect_rows("kv_len", kv_len, B, q.device)
             s = _expect_rows("q_start", q_start, B, q.device)
             with _Launch(q.device, stream) as st:
@@ -747,7 +763,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
             lse = q.new_empty((B, H, Sq), dtype=torch.float32)
         work = q.new_empty((size,), dtype=torch.uint8) if size else None
         _check(lib.dash_attn_sparse_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                        _strides(q, k, v), plan.buf.data_ptr(), out.data_ptr(),
+                                        _strides(q, k, v), plan.on(st), out.data_ptr(),
                                         lse.data_ptr(), work.data_ptr() if size else None,
                                         *plan.shape[:5], D, *plan.shape[5:], int(plan.causal),
                                         float(scale or 0.0), st), "dash_attn_sparse_fwd")
@@ -776,7 +792,7 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
         dv = _like(k) if dv is None else dv
         work = q.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_attn_sparse_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
-                                        _strides(q, k, v, do), plan.buf.data_ptr(), o.data_ptr(),
+                                        _strides(q, k, v, do), plan.on(st), o.data_ptr(),
                                         lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                         dv.data_ptr(), work.data_ptr(), *plan.shape[:5], D,
                                         *plan.shape[5:], int(plan.causal), float(scale or 0.0), st),

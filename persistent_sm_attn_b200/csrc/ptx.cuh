@@ -225,6 +225,12 @@ __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, u
   }
 }
 
+// Limit of a drain where the waits have a short one: what a CTA waits for before it goes
+// finishes by itself, but not in no time.
+__device__ __forceinline__ uint64_t drain_ns(uint64_t limit_ns) {
+  return limit_ns > 1000000000ull ? limit_ns : 1000000000ull;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
                                             uint32_t bar) {

@@ -545,9 +545,9 @@ int dash_block_means(const void* k, const long long* k_strides, float* means, co
     Strides st;
     int rc = take_strides(k_strides, B, Hkv, Sk, D, &st);
     if (rc) return rc;
+    if (B == 0 || Hkv == 0) return DASH_OK;
     if (!aligned16(k) || !aligned4(means) || !aligned4_or_null(kv_len) || !aligned4_or_null(start))
       return DASH_ERR_INVALID_ARG;
-    if (B == 0 || Hkv == 0) return DASH_OK;
     dash::MeansParams p;
     p.k = static_cast<const __nv_bfloat16*>(k);
     p.sb = st.b, p.sh = st.h, p.ss = st.s;
@@ -575,10 +575,10 @@ int dash_block_select(const void* q, const long long* q_strides, const float* me
     if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
     Strides st;
     if ((rc = take_strides(q_strides, B, H, Sq, D, &st))) return rc;
+    if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
     if (!aligned16(q) || !aligned16(means) || !aligned4(idx) || !aligned4_or_null(kv_len) ||
         !aligned4_or_null(q_start))
       return DASH_ERR_INVALID_ARG;
-    if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
     dash::SelectParams p;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.sb = st.b, p.sh = st.h, p.ss = st.s;
@@ -658,10 +658,10 @@ int dash_attn_sparse_fwd(const void* q, const void* k, const void* v, const long
         (rc = take_strides(strides ? strides + 3 : nullptr, B, Hkv, Sk, D, &st[1])) ||
         (rc = take_strides(strides ? strides + 6 : nullptr, B, Hkv, Sk, D, &st[2])))
       return rc;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse))
-      return DASH_ERR_INVALID_ARG;
     if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
-    if (!aligned16(plan)) return DASH_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+        !aligned16(plan))
+      return DASH_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return D == 64 ? launch_sparse_fwd<64>(q, k, v, st, s, plan, o, lse, work, scale, cs)
                    : launch_sparse_fwd<128>(q, k, v, st, s, plan, o, lse, work, scale, cs);
@@ -728,10 +728,8 @@ int dash_attn_sparse_bwd(const void* q, const void* k, const void* v, const void
         (rc = take_strides(strides ? strides + 6 : nullptr, B, Hkv, Sk, D, &st[2])) ||
         (rc = take_strides(strides ? strides + 9 : nullptr, B, H, Sq, D, &st[3])))
       return rc;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) ||
-        !aligned4(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
-      return DASH_ERR_INVALID_ARG;
     if (B == 0 || H == 0) return DASH_OK;
+    if (!aligned16(dk) || !aligned16(dv)) return DASH_ERR_INVALID_ARG;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (Sq == 0) {  // no query reads a key
       const size_t bytes = (size_t)B * Hkv * Sk * D * 2;
@@ -739,7 +737,9 @@ int dash_attn_sparse_bwd(const void* q, const void* k, const void* v, const void
       DASH_CUDA(cudaMemsetAsync(dv, 0, bytes, cs));
       return DASH_OK;
     }
-    if (!aligned16(plan) || !aligned16(work)) return DASH_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) ||
+        !aligned4(lse) || !aligned16(dq) || !aligned16(plan) || !aligned16(work))
+      return DASH_ERR_INVALID_ARG;
     return D == 64 ? launch_sparse_bwd<64>(q, k, v, dout, st, s, plan, o, lse, dq, dk, dv, work,
                                            scale, cs)
                    : launch_sparse_bwd<128>(q, k, v, dout, st, s, plan, o, lse, dq, dk, dv, work,

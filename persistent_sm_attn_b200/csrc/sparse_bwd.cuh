@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(384, 1)
     }
     // no load may land after the CTA has gone, not even when a wait ran out
     for (int x = max(0, nq - C::kQ); x < nq; ++x)
-      mbar_wait_drain(Q_FULL(x), ph2(x), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(Q_FULL(x), ph2(x), drain_ns(p.spin_ns), p.err, p.err + 1);
     for (int x = max(0, nk - C::kK); x < nk; ++x)
-      mbar_wait_drain(K_FULL(x), phK(x), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(K_FULL(x), phK(x), drain_ns(p.spin_ns), p.err, p.err + 1);
     for (int x = max(0, nv - C::kV); x < nv; ++x)
-      mbar_wait_drain(V_FULL(x), phV(x), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(V_FULL(x), phV(x), drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp >= 1 && warp < 4) {
     // ---------------------------------------------------------------- product issuers
     // Three of them: warps 1 and 2 S and dP of a stream, warp 3 dQ.  One thread's instructions
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(384, 1)
       ++k;
     }
     if (leader) tc_commit(FINAL);  // the CTA does not go before its products
-    mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
+    mbar_wait_drain(FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax gradient
     const int h = (warp - 4) >> 2, quarter = warp & 3;  // warpgroup h takes units j = h mod 2
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(640, 1)
     }
     // no load may land after the CTA has gone, not even when a wait ran out
     for (int j = max(0, k - 2); j < k; ++j)
-      mbar_wait_drain(KV_FULL(j), ph2(j), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(KV_FULL(j), ph2(j), drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp == 8 || warp == 10) {
     // ---------------------------------------------------------------- product issuers
     // Two of them, S and dP and beside them dV and dK (see the dQ kernel)
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(640, 1)
       }
     }
     if (leader) tc_commit(FINAL);  // the CTA does not go before its products
-    mbar_wait_drain(FINAL, 0, p.spin_ns, p.err, p.err + 1);
+    mbar_wait_drain(FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp >= 12) {
     // ---------------------------------------------------------------- softmax gradient
     const int wg = (warp - 12) >> 2, quarter = warp & 3;

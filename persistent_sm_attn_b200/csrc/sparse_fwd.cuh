@@ -153,11 +153,11 @@ __global__ void __launch_bounds__(256, 2)
       u = next;
     }
     // no load may land after the CTA has gone, not even when a wait ran out
-    if (n > 0) mbar_wait_drain(Q_FULL, 0, p.spin_ns, p.err, p.err + 1);
+    if (n > 0) mbar_wait_drain(Q_FULL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
     for (int j = max(0, nk - C::kK); j < nk; ++j)
-      mbar_wait_drain(K_FULL(j), phK(j), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(K_FULL(j), phK(j), drain_ns(p.spin_ns), p.err, p.err + 1);
     for (int j = max(0, nv - C::kV); j < nv; ++j)
-      mbar_wait_drain(V_FULL(j), phV(j), p.spin_ns, p.err, p.err + 1);
+      mbar_wait_drain(V_FULL(j), phV(j), drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S issuer
     constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256, 2)
       }
     }
     if (leader) tc_commit(S_FINAL);  // the CTA does not go before its products
-    mbar_wait_drain(S_FINAL, 0, p.spin_ns, p.err, p.err + 1);
+    mbar_wait_drain(S_FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- P V issuer
     constexpr uint32_t ID_PV = idesc_bf16_f32(128, D, 0, 1);
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256, 2)
       }
     }
     if (leader) tc_commit(O_FINAL);
-    mbar_wait_drain(O_FINAL, 0, p.spin_ns, p.err, p.err + 1);
+    mbar_wait_drain(O_FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
     const int quarter = warp & 3;
