@@ -801,8 +801,30 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
 
 
 # ---------------------------------------------------------------- 8-bit checkpoints
-_POINTERS = [ctypes.c_void_p * n for n in range(5)]  # argument arrays of a launch's tensors
-_LONGS = [ctypes.c_longlong * n for n in range(5)]
+_LONGS = [ctypes.c_longlong * (4 * n) for n in range(5)]  # arguments of a launch of n tensors
+
+
+def _check_ckpt(what, x, dtype, device):
+    """x: contiguous device tensor of dtype in whole groups of 32, 16-byte aligned."""
+    if (x.dtype is dtype and x.is_cuda and x.device == device and x.is_contiguous() and x.dim()
+            and not x.shape[-1] % 32 and not x.data_ptr() % 16):
+        return
+    _expect(what, x, x.shape, dtype, device)
+    raise ValueError(f"{what}: the last dimension must be a multiple of 32, 16-byte aligned")
+
+
+def _ckpt_launch(call, what, inputs, exps, outputs, st):
+    """Launches of up to four tensors: addresses and element counts in one argument array."""
+    for a in range(0, len(inputs), 4):
+        part = inputs[a:a + 4]
+        n = len(part)
+        args = _LONGS[n](*[x.data_ptr() for x in part], *[x.data_ptr() for x in exps[a:a + 4]],
+                         *[x.data_ptr() for x in outputs[a:a + 4]], *[x.numel() for x in part])
+        at = [ctypes.byref(args, 8 * n * k) for k in range(4)]
+        if call == "pack":
+            _check(load().dash_ckpt8_pack(at[0], at[2], at[1], at[3], n, st), what)
+        else:
+            _check(load().dash_ckpt8_unpack(at[0], at[1], at[2], at[3], n, st), what)
 
 
 def dash_ckpt8_pack(*tensors, stream=None):
@@ -812,26 +834,13 @@ def dash_ckpt8_pack(*tensors, stream=None):
     if not tensors:
         return []
     device = tensors[0].device
-    for j, x in enumerate(tensors):
-        _expect(f"tensor {j}", x, x.shape, torch.bfloat16, device)
-        if x.dim() < 1 or x.shape[-1] % 32 or x.data_ptr() % 16:
-            raise ValueError(f"tensor {j}: the last dimension must be a multiple of 32, 16-byte "
-                             "aligned")
-    pairs = []
+    for x in tensors:
+        _check_ckpt("the tensor", x, torch.bfloat16, device)
     with _Launch(device, stream) as st:
-        for x in tensors:
-            pairs.append((_like(x, torch.int8),
-                          x.new_empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.int8)))
-        for a in range(0, len(tensors), 4):
-            part = pairs[a:a + 4]
-            n = len(part)
-            vp = _POINTERS[n]
-            _check(load().dash_ckpt8_pack(vp(*[x.data_ptr() for x in tensors[a:a + 4]]),
-                                          vp(*[m.data_ptr() for m, _ in part]),
-                                          vp(*[e.data_ptr() for _, e in part]),
-                                          _LONGS[n](*[m.numel() for m, _ in part]),
-                                          n, st), "dash_ckpt8_pack")
-    return pairs
+        ms = [torch.empty_like(x, dtype=torch.int8) for x in tensors]
+        es = [x.new_empty((*x.shape[:-1], x.shape[-1] // 32), dtype=torch.int8) for x in tensors]
+        _ckpt_launch("pack", "dash_ckpt8_pack", tensors, es, ms, st)
+    return list(zip(ms, es))
 
 
 def dash_ckpt8_unpack(*pairs, stream=None):
@@ -840,24 +849,13 @@ def dash_ckpt8_unpack(*pairs, stream=None):
     if not pairs:
         return []
     device = pairs[0][0].device
-    for j, (m, e) in enumerate(pairs):
-        _expect(f"m of checkpoint {j}", m, m.shape, torch.int8, device)
-        if m.dim() < 1 or m.shape[-1] % 32 or m.data_ptr() % 16:
-            raise ValueError(f"checkpoint {j}: the last dimension must be a multiple of 32, "
-                             "16-byte aligned")
-        _expect(f"e of checkpoint {j}", e, (*m.shape[:-1], m.shape[-1] // 32), torch.int8, device)
-    out = []
+    for m, e in pairs:
+        _check_ckpt("m of a checkpoint", m, torch.int8, device)
+        _expect("e of a checkpoint", e, (*m.shape[:-1], m.shape[-1] // 32), torch.int8, device)
     with _Launch(device, stream) as st:
-        out = [_like(m, torch.bfloat16) for m, _ in pairs]
-        for a in range(0, len(pairs), 4):
-            part = pairs[a:a + 4]
-            n = len(part)
-            vp = _POINTERS[n]
-            _check(load().dash_ckpt8_unpack(vp(*[m.data_ptr() for m, _ in part]),
-                                            vp(*[e.data_ptr() for _, e in part]),
-                                            vp(*[x.data_ptr() for x in out[a:a + 4]]),
-                                            _LONGS[n](*[m.numel() for m, _ in part]),
-                                            n, st), "dash_ckpt8_unpack")
+        ms = [m for m, _ in pairs]
+        out = [torch.empty_like(m, dtype=torch.bfloat16) for m in ms]
+        _ckpt_launch("unpack", "dash_ckpt8_unpack", ms, [e for _, e in pairs], out, st)
     return out
 
 
