@@ -107,107 +107,346 @@ __device__ __forceinline__ double exact_score(const double (&qd)[D / 32], const 
   return s;
 }
 
-// Few queries (serving): a CTA per query reads the K/V head's means once, a warp per row
-// with 16 (D = 64: 8) bytes a lane, four rows in flight.  The r-th largest key is found by
-// halving the key range, usually in under 20 counts.  Bound by reading the means.
-template <int D>
+// What a warp knows of its query's picks: of the visible blocks j0 <= j < j1 are contested, r
+// places of them are to be given.  Bit x of take and open: block 32 x + lane is taken; is to be
+// decided in fp64.  NL: 32-block words that a lane's share of a row has room for.
+template <int NL>
+struct Picks {
+  static constexpr int W = (NL + 31) / 32;
+  uint32_t take[W], open[W];
+  int nvis, j0, j1, nl, r;
+  __device__ Picks(const SelectParams& p, int visible)
+      : nvis(visible), j0(p.sink), j1(visible - p.local), nl((visible + 31) / 32),
+        r(p.topk - p.sink - p.local) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
+  }
+};
+
+// Picks by approximate scores `row` that are off by at most eps2 / 2 and within +-most_score.
+// A cut with exactly r scores above it is found by counting; where the lowest score above and
+// the highest below are more than eps2 apart, the picks are those of the exact scores.
+// Otherwise the scores within eps2 of the cut stay open; returned is how many of them to take.
+// guess: in, where the first counts are taken; out, the cut (both of most_score).
+template <int NL>
+__device__ __forceinline__ int pick_approx(Picks<NL>& k, const float* row, float most_score,
+                                           float eps2, float& guess, int lane) {
+  constexpr int W = Picks<NL>::W;
+  const int j0 = k.j0, j1 = k.j1, nl = k.nl, r = k.r;
+  if (!(eps2 < 1e30f)) {  // a partial sum might have overflowed, or an operand is not finite
+    for (int x = 0; x < nl; ++x) {
+      const int j = 32 * x + lane;
+      if (j >= j0 && j < j1) k.open[W == 1 ? 0 : x >> 5] |= 1u << (x & 31);
+    }
+    return r;
+  }
+  // this lane's scores, -inf where not contested: in registers for up to 512 blocks
+  constexpr bool kHeld = NL <= 16;
+  float held[kHeld ? NL : 1] = {};
+  if constexpr (kHeld)
+#pragma unroll
+    for (int x = 0; x < NL; ++x) {
+      if (x % 2 == 0 && x >= nl) break;
+      const int j = 32 * x + lane;
+      held[x] = j >= j0 && j < j1 ? row[j] : -INFINITY;
+    }
+  auto each = [&](auto&& f) {
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int x = 0; x < NL; ++x) {
+        if (x > 0 && x % 2 == 0 && x >= nl) break;
+        f(x, held[x]);
+      }
+    } else {
+#pragma unroll 4
+      for (int x = 0; x < nl; ++x) {
+        const int j = 32 * x + lane;
+        f(x, j >= j0 && j < j1 ? row[j] : -INFINITY);
+      }
+    }
+  };
+  // the r-th and the next largest lie in (lo, hi]: no score is beyond |q| max|m|
+  float lo = -1.01f * most_score - 1e-30f, hi = -lo, cut = 0.f;
+  bool found = false;
+  // the range falls to a quarter (a third) with each count: up to 512 blocks leave
+  // room for three counts in a word
+  constexpr int kBits = kHeld ? 10 : 16;
+  // and the first counts are taken around where the last query's cut was
+  float near = guess * most_score;
+  while (!found && hi - lo > eps2) {
+    float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
+    float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
+    if (near != 0.f) {
+      d = 0.1f * fabsf(near);
+      m1 = near - d, m2 = kHeld ? near : near + d, m3 = near + d;
+      near = 0.f;
+    }
+    if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
+    unsigned c = 0;
+    each([&](int, float v) {
+      c += (v > m1 ? 1u : 0u) + (v > m2 ? 1u << kBits : 0u);
+      if constexpr (kHeld) c += v > m3 ? 1u << (2 * kBits) : 0u;
+    });
+    c = __reduce_add_sync(0xffffffffu, c);
+    const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
+    int c3 = 0;
+    if constexpr (kHeld) c3 = (int)(c >> (2 * kBits));
+    if (c1 == r) cut = m1, found = true;
+    else if (c2 == r) cut = m2, found = true;
+    else if (kHeld && c3 == r) cut = m3, found = true;
+    else if (c1 < r) hi = m1;
+    else if (c2 < r) lo = m1, hi = m2;
+    else if (!kHeld) lo = m2;
+    else if (c3 < r) lo = m2, hi = m3;
+    else lo = m3;
+  }
+  if (found && most_score > 1e-20f) guess = cut / most_score;
+  float a = lo, z = hi;
+  if (found) {  // lowest above the cut, highest below
+    int ka = 0x7f800000, kz = (int)0x807fffff;  // as integers that order like the floats
+    each([&](int, float v) {
+      const int k = ordered_int(v);
+      if (v > cut) ka = min(ka, k);
+      else kz = max(kz, k);
+    });
+    a = __int_as_float(ordered_int_inverse(__reduce_min_sync(0xffffffffu, ka)));
+    z = __int_as_float(ordered_int_inverse(__reduce_max_sync(0xffffffffu, kz)));
+  }
+  const bool clear = found && a - z > eps2;
+  const float in_at = clear ? cut : z + eps2, open_at = clear ? INFINITY : a - eps2;
+  int in = 0;
+  each([&](int x, float v) {
+    if (v > in_at) k.take[W == 1 ? 0 : x >> 5] |= 1u << (x & 31), ++in;
+    else if (v >= open_at) k.open[W == 1 ? 0 : x >> 5] |= 1u << (x & 31);
+  });
+  return clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
+}
+
+// Decides the open blocks, `need` of which are to be taken, by their fp64 scores.  key: a word
+// a block of shared memory.
+template <int D, int NL>
+__device__ __forceinline__ void pick_exact(Picks<NL>& k, int need, const SelectParams& p, int b,
+                                           int hk, int i, const float* means, uint32_t* key,
+                                           int lane) {
+  constexpr int W = Picks<NL>::W;
+  const int j0 = k.j0, j1 = k.j1, nl = k.nl;
+  uint32_t(&take)[W] = k.take;
+  uint32_t(&open)[W] = k.open;
+  int undecided = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) undecided += __popc(open[w]);
+  undecided = __reduce_add_sync(0xffffffffu, undecided);
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int x = 0; x < nl; ++x) {
+      const int j = 32 * x + lane;
+      if (j >= j0 && j < j1) f(x, j);
+    }
+  };
+  double qd[D / 32] = {};
+  const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+#pragma unroll 4
+  for (int g = 0; g < p.G; ++g)
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
+  if (undecided <= 32) {
+    // the usual case: one open block a lane (ascending), its place among them by 64-bit keys
+    int mine = -1, n = 0;
+#pragma unroll 1
+    for (int x = 0; x < nl; ++x) {
+      unsigned m = __ballot_sync(0xffffffffu, (open[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u);
+      for (; m; m &= m - 1, ++n)
+        if (lane == n) mine = 32 * x + __ffs(m) - 1;
+    }
+    unsigned long long key64 = 0;
+#pragma unroll 2
+    for (int t = 0; t < n; ++t) {
+      const int j = __shfl_sync(0xffffffffu, mine, t);
+      const unsigned long long k = order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+      if (lane == t) key64 = k;
+    }
+    int place = 0;
+#pragma unroll 2
+    for (int t = 0; t < n; ++t) {
+      const unsigned long long k = __shfl_sync(0xffffffffu, key64, t);
+      place += k > key64 || (k == key64 && t < lane);
+    }
+    const bool in = lane < n && place < need;
+#pragma unroll 2
+    for (int t = 0; t < n; ++t) {
+      const int j = __shfl_sync(0xffffffffu, in ? mine : -1, t);
+      if (j >= 0 && (j & 31) == lane)
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (w == j >> 10) take[w] |= 1u << ((j >> 5) & 31);
+    }
+    need = 0;
+  }
+  if (need > 0) {  // many open blocks (equal ones, operands that are not finite)
+    // exact scores of the open blocks, their keys' upper words in place of the scores;
+    // then, among those that tie in it, by the lower words; then by number
+#pragma unroll 1
+    for (int word = 0; word < 2; ++word) {
+#pragma unroll 1
+      for (int x = 0; x < nl; ++x) {
+        unsigned m = __ballot_sync(0xffffffffu, (open[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u);
+        while (m) {
+          const int src = __ffs(m) - 1;
+          m &= m - 1;
+          const int j = 32 * x + src;
+          const unsigned long long k =
+              order_key(exact_score<D>(qd, means + (long long)j * D, lane));
+          if (lane == src) key[j] = word == 0 ? (uint32_t)(k >> 32) : (uint32_t)k;
+        }
+      }
+      uint32_t t = 0;  // the need-th largest word, bit by bit
+#pragma unroll 1
+      for (uint32_t bitv = 0x80000000u; bitv; bitv >>= 1) {
+        int c = 0;
+        each([&](int x, int j) {
+          if ((open[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u) c += key[j] >= (t | bitv);
+        });
+        if ((int)__reduce_add_sync(0xffffffffu, c) >= need) t |= bitv;
+      }
+      int in = 0, same = 0;
+      each([&](int x, int j) {
+        const uint32_t bx = 1u << (x & 31);
+        if (!(open[W == 1 ? 0 : x >> 5] & bx)) return;
+        if (key[j] > t) take[W == 1 ? 0 : x >> 5] |= bx, open[W == 1 ? 0 : x >> 5] &= ~bx, ++in;
+        else if (key[j] < t) open[W == 1 ? 0 : x >> 5] &= ~bx;
+        else ++same;
+      });
+      need -= __reduce_add_sync(0xffffffffu, in);
+      same = __reduce_add_sync(0xffffffffu, same);
+      if (same == need) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) take[w] |= open[w], open[w] = 0u;
+        need = 0;
+        break;
+      }
+    }
+    // exact ties: the lowest numbers
+#pragma unroll 1
+    for (int x = 0; x < nl && need > 0; ++x) {
+      const bool tie = (open[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u;
+      const unsigned m = __ballot_sync(0xffffffffu, tie);
+      if (tie && __popc(m & ((1u << lane) - 1u)) < need) take[W == 1 ? 0 : x >> 5] |= 1u << (x & 31);
+      need -= __popc(m);
+    }
+  }
+}
+
+// Writes the picks ascending, then -1.
+template <int NL>
+__device__ __forceinline__ void put_out(const Picks<NL>& k, int topk, int* out, int lane) {
+  constexpr int W = Picks<NL>::W;
+  const bool all = k.nvis <= topk;
+  int done = 0;
+#pragma unroll (NL <= 16 ? NL : 4)
+  for (int x = 0; x < NL; ++x) {
+    if (x >= k.nl) break;
+    const int j = 32 * x + lane;
+    const bool on =
+        j < k.nvis && (all || j < k.j0 || j >= k.j1 || ((k.take[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u));
+    const unsigned m = __ballot_sync(0xffffffffu, on);
+    if (on) out[done + __popc(m & ((1u << lane) - 1u))] = j;
+    done += __popc(m);
+  }
+  for (int x = done + lane; x < topk; x += 32) out[x] = -1;
+}
+
+// Few queries (serving): a CTA per query reads the K/V head's means once, a warp per row with
+// 16 (D = 64: 8) bytes a lane, eight rows in flight.  A score is a sum of D products in fp32
+// with D/32 + 5 roundings on the way of each, so it is off by less than 2^-20 |q||m|, and by
+// what the heads' sum was rounded by (see dash_block_select_kernel); |m| is at most sqrt(D)
+// times the largest element.  Bound by reading the means.
+template <int D, int NL>
 __global__ void __launch_bounds__(256) dash_block_select_token_kernel(const SelectParams p) {
   extern __shared__ __align__(16) unsigned char select_smem[];
-  unsigned long long* keys = reinterpret_cast<unsigned long long*>(select_smem);  // [nb]
-  constexpr int V = D / 32;
+  float* sc = reinterpret_cast<float*>(select_smem);  // [nb]
+  __shared__ int top_bits;
+  constexpr int V = D / 32, kRows = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y, b = bh / p.Hkv, hk = bh % p.Hkv, i = blockIdx.x;
   const int nvis = visible_blocks(p, b, i);
-  int* out = p.idx + ((long long)bh * p.Sq + i) * p.topk;
-  double qd[V] = {};
-  if (nvis > p.topk) {
-    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
+  const float* means = p.means + (long long)bh * p.nb * D;
+  Picks<NL> k(p, nvis);
+  const bool contest = nvis > p.topk && k.r > 0;
+  if (threadIdx.x == 0) top_bits = 0;
+  __syncthreads();
+  float n2 = 0.f, a2 = 0.f;  // this lane's share of |q|^2 and of |sum of |heads||^2
+  if (contest) {
+    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss + lane * V;
+    float qs[V] = {}, qa[V] = {};
+#pragma unroll 4
     for (int g = 0; g < p.G; ++g)
 #pragma unroll
-      for (int x = 0; x < V; ++x)
-        qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + lane * V + x]);
-    const float* means = p.means + (long long)bh * p.nb * D + lane * V;
-    const int j1 = nvis - p.local;
-    for (int j0 = p.sink + warp * 4; j0 < j1; j0 += 32) {
-      float m[4][V];
+      for (int x = 0; x < V; ++x) {
+        const float y = __bfloat162float(q[(long long)g * p.sh + x]);
+        qs[x] += y, qa[x] += fabsf(y);
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float* src = means + (long long)min(j0 + r, j1 - 1) * D;
+    for (int x = 0; x < V; ++x) n2 += qs[x] * qs[x], a2 += qa[x] * qa[x];
+    int top = 0;  // largest |element| as bits, so that an infinity or NaN stays the largest
+    for (int base = k.j0 + warp * kRows; base < k.j1; base += 8 * kRows) {
+      float m[kRows][V], s[kRows];
+#pragma unroll
+      for (int y = 0; y < kRows; ++y) {
+        const float* src = means + (long long)min(base + y, k.j1 - 1) * D + lane * V;
         if constexpr (V == 4) {
           const float4 w = *reinterpret_cast<const float4*>(src);
-          m[r][0] = w.x, m[r][1] = w.y, m[r][2] = w.z, m[r][3] = w.w;
+          m[y][0] = w.x, m[y][1] = w.y, m[y][2] = w.z, m[y][3] = w.w;
         } else {
           const float2 w = *reinterpret_cast<const float2*>(src);
-          m[r][0] = w.x, m[r][1] = w.y;
+          m[y][0] = w.x, m[y][1] = w.y;
         }
       }
-      double s[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s[r] = 0.0;
+      for (int y = 0; y < kRows; ++y) {
+        s[y] = 0.f;
 #pragma unroll
-        for (int x = 0; x < V; ++x) s[r] += qd[x] * (double)m[r][x];
+        for (int x = 0; x < V; ++x) {
+          s[y] = fmaf(qs[x], m[y][x], s[y]);
+          top = max(top, __float_as_int(m[y][x]) & 0x7fffffff);
+        }
       }
+      // eight sums over the warp: halves swap what the other sums on
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
+      for (int h = 4; h > 0; h >>= 1) {
+        const bool up = lane & (h * 4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-      if (lane < 4 && j0 + lane < j1)
-        keys[j0 + lane] = order_key(lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3]);
+        for (int y = 0; y < h; ++y) {
+          const float give = up ? s[y] : s[y + h], keep = up ? s[y + h] : s[y];
+          s[y] = keep + __shfl_xor_sync(0xffffffffu, give, h * 4);
+        }
+      }
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+      const int row = base + (lane >> 2);  // bits 4, 3, 2 of the lane chose the row's
+      if ((lane & 3) == 0 && row < k.j1) sc[row] = s[0];
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) atomicMax(&top_bits, top);
   }
   __syncthreads();
   if (warp > 0) return;
-  const int j0 = p.sink, j1 = nvis - p.local;  // the contested blocks, where nvis > topk
-  unsigned long long cut = 0;                  // taken: key > cut, and `ties` of key == cut
-  int ties = 0;
-  const int r = p.topk - p.sink - p.local;
-  if (nvis > p.topk && r > 0) {
-    // lo < the r-th largest key <= hi
-    unsigned long long lo = ~0ull, hi = 0;
-    for (int j = j0 + lane; j < j1; j += 32) lo = min(lo, keys[j]), hi = max(hi, keys[j]);
+  if (contest) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      a2 += __shfl_xor_sync(0xffffffffu, a2, o);
     }
-    bool found = false, bottom = lo == 0;  // a key 0 cannot be undercut: it stands for itself
-    if (!bottom) --lo;
-    while (!found && hi - lo > 1) {
-      const unsigned long long mid = lo + (hi - lo) / 2;
-      int c = 0;
-      for (int j = j0 + lane; j < j1; j += 32) c += keys[j] > mid;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c == r) cut = mid, found = true;
-      else if (c > r) lo = mid, bottom = false;
-      else hi = mid;
-    }
-    if (!found) {
-      cut = hi;
-      int c = 0, e = 0;
-      for (int j = j0 + lane; j < j1; j += 32) c += keys[j] > hi, e += keys[j] >= hi;
-      c = __reduce_add_sync(0xffffffffu, c);
-      e = __reduce_add_sync(0xffffffffu, e);
-      if (bottom && e < r) cut = 0, c = e;  // keys of 1 and more do not suffice
-      ties = r - c;
-    }
+    const float mnorm = sqrtf((float)D) * __int_as_float(top_bits);
+    const float qn = sqrtf(n2), most = (qn + 0x1p-10f * sqrtf(a2)) * mnorm;
+    const float eps2 = 2.f * ((0x1p-20f * qn + 0x1p-24f * p.G * sqrtf(a2)) * mnorm + 1e-35f);
+    float guess = 0.f;
+    const int need = pick_approx<NL>(k, sc, most, eps2, guess, lane);
+    __syncwarp();
+    if (need > 0)
+      pick_exact<D, NL>(k, need, p, b, hk, i, means, reinterpret_cast<uint32_t*>(sc), lane);
   }
-  int done = 0;
-  for (int x0 = 0; x0 < nvis; x0 += 32) {
-    const int j = x0 + lane;
-    bool take = j < nvis, tie = false;
-    if (take && nvis > p.topk && j >= j0 && j < j1) {
-      take = r > 0 && keys[j] > cut;
-      tie = r > 0 && !take && keys[j] == cut;
-    }
-    const unsigned mt = __ballot_sync(0xffffffffu, tie);
-    if (tie) take = __popc(mt & ((1u << lane) - 1u)) < ties;
-    ties = max(0, ties - __popc(mt));
-    const unsigned m = __ballot_sync(0xffffffffu, take);
-    if (take) out[done + __popc(m & ((1u << lane) - 1u))] = j;
-    done += __popc(m);
-  }
-  for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
+  put_out(k, p.topk, p.idx + ((long long)bh * p.Sq + i) * p.topk, lane);
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -242,15 +481,12 @@ struct SelectCfg {
 // Many queries: QT of one K/V head, all visible blocks, 64 at a time.
 //
 // Scores: q = q_h + q_l, m = m_h + m_l in bf16, score ~ q_h m_h + q_h m_l + q_l m_h, fp32
-// accumulators.  What is left out and rounded is at most 3 * 2^-16 sum|q||m|, the sums of
-// the heads and of 3 D products in fp32 at most (G + 3 D + 3) 2^-23 of the same; with
-// G <= 128, D <= 128 and sum|q||m| <= |q| |m| (Euclidean norms) the error is below
-//     eps = 2^-13 |q| max_j |m_j|.
-// Picks: a cut T with exactly r scores above it, by halving the range of the scores.  Where
-// the lowest score above T and the highest below are more than 2 eps apart, the picks are
-// those of the exact scores.  Otherwise the scores within 2 eps of the cut are computed in
-// fp64 and decided by those.  An eps that is not
-// finite (an infinity or NaN among the operands) leaves everything to fp64.
+// accumulators.  What is left out and rounded is at most 3 * 2^-16 sum|q||m|, the sum of 3 D
+// products in fp32 at most (3 D + 3) 2^-23 of the same: below 2^-13 |q| max_j |m_j| (Euclidean
+// norms).  The heads' sum q itself is rounded, by at most G 2^-24 sum_g |q_g|, which their
+// cancelling may make large against q.  Together the error is below
+//     eps = 2^-13 (|q| + G 2^-11 |sum_g |q_g||) max_j |m_j|.
+// An eps that is not finite (an infinity or NaN among the operands) leaves everything to fp64.
 //
 // NL: 32-block words that a lane's share of a row has room for.
 template <int D, int QT, int NL>
@@ -281,7 +517,7 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
     const bool on = row < QT && i0 + row < p.Sq;
     const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh +
                              (long long)(on ? i0 + row : 0) * p.ss + c * 8;
-    float v[8] = {};
+    float v[8] = {}, va[8] = {};
     if (on) {
 #pragma unroll 4
       for (int g = 0; g < p.G; ++g) {
@@ -289,24 +525,29 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          v[2 * k] += __uint_as_float(u[k] << 16);
-          v[2 * k + 1] += __uint_as_float(u[k] & 0xffff0000u);
+          const float x0 = __uint_as_float(u[k] << 16), x1 = __uint_as_float(u[k] & 0xffff0000u);
+          v[2 * k] += x0, va[2 * k] += fabsf(x0);
+          v[2 * k + 1] += x1, va[2 * k + 1] += fabsf(x1);
         }
       }
     }
-    float n2 = 0.f;
+    float n2 = 0.f, a2 = 0.f;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       n2 += v[2 * k] * v[2 * k] + v[2 * k + 1] * v[2 * k + 1];
+      a2 += va[2 * k] * va[2 * k] + va[2 * k + 1] * va[2 * k + 1];
       split_bf16(v[2 * k], v[2 * k + 1], hi[k], lo[k]);
     }
     unsigned char* at = select_smem + row * C::kLd + c * 16;
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + C::kRows * C::kLd) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 #pragma unroll
-    for (int o = CH / 2; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-    if (c == 0) qnorm[row] = sqrtf(n2);
+    for (int o = CH / 2; o > 0; o >>= 1) {
+      n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      a2 += __shfl_xor_sync(0xffffffffu, a2, o);
+    }
+    if (c == 0) qnorm[row] = sqrtf(n2) + 0x1p-11f * p.G * sqrtf(a2);
   }
 
   // ---- scores; the next 64 means are on their way while these are multiplied
@@ -375,254 +616,43 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
   // ---- picks, a warp per query.  Queries whose picks the bound leaves open are put off, so
   // that the warps share them (one in fifteen on normal data, two blocks each)
   const float mnorm = sqrtf(__int_as_float(mnorm_bits));
-  const int r = p.topk - p.sink - p.local;
   uint32_t* saved = reinterpret_cast<uint32_t*>(mstage);  // [QT][2 W][32], over the means
-  auto put_out = [&](int rr, int nvis, const uint32_t(&take)[W]) {
-    const bool all = nvis <= p.topk;
-    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
-    int* out = p.idx + ((long long)bh * p.Sq + i0 + rr) * p.topk;
-    int done = 0;
-#pragma unroll (NL <= 16 ? NL : 4)
-    for (int x = 0; x < NL; ++x) {
-      if (x >= nl) break;
-      const int j = 32 * x + lane;
-      const bool on = j < nvis && (all || j < j0 || j >= j1 || ((take[x >> 5] >> (x & 31)) & 1u));
-      const unsigned m = __ballot_sync(0xffffffffu, on);
-      if (on) out[done + __popc(m & ((1u << lane) - 1u))] = j;
-      done += __popc(m);
-    }
-    for (int x = done + lane; x < p.topk; x += 32) out[x] = -1;
-  };
+  auto out = [&](int rr) { return p.idx + ((long long)bh * p.Sq + i0 + rr) * p.topk; };
   float guess = 0.f;  // the last cut, of the largest score that could be
   for (int rr = warp; rr < QT && i0 + rr < p.Sq; rr += C::kThreads / 32) {
-    const int nvis = nv[rr];
-    const float* row = sc + rr * ld;
-    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
-    uint32_t take[W], open[W];  // bit x: block 32 x + lane is taken; is to be decided in fp64
-#pragma unroll
-    for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
+    Picks<NL> k(p, nv[rr]);
     int need = 0;
-    if (nvis > p.topk && r > 0) {
-      // this lane's scores, -inf where not contested: in registers for up to 512 blocks
-      constexpr bool kHeld = NL <= 16;
-      float held[kHeld ? NL : 1] = {};
-      if constexpr (kHeld)
-#pragma unroll
-        for (int x = 0; x < NL; ++x) {
-          if (x % 2 == 0 && x >= nl) break;
-          const int j = 32 * x + lane;
-          held[x] = j >= j0 && j < j1 ? row[j] : -INFINITY;
-        }
-      auto each = [&](auto&& f) {
-        if constexpr (kHeld) {
-#pragma unroll
-          for (int x = 0; x < NL; ++x) {
-            if (x > 0 && x % 2 == 0 && x >= nl) break;
-            f(x, held[x]);
-          }
-        } else {
-#pragma unroll 4
-          for (int x = 0; x < nl; ++x) {
-            const int j = 32 * x + lane;
-            f(x, j >= j0 && j < j1 ? row[j] : -INFINITY);
-          }
-        }
-      };
+    if (k.nvis > p.topk && k.r > 0) {
       const float most_score = qnorm[rr] * mnorm;
-      const float eps2 = 2.f * (0x1p-13f * most_score + 1e-35f);
-      need = r;
-      if (eps2 < 1e30f) {  // beyond, a partial sum might overflow
-        // the r-th and the next largest lie in (lo, hi]: no score is beyond |q| max|m|
-        float lo = -1.01f * most_score - 1e-30f, hi = -lo, cut = 0.f;
-        bool found = false;
-        // the range falls to a quarter (a third) with each count: up to 512 blocks leave
-        // room for three counts in a word
-        constexpr int kBits = kHeld ? 10 : 16;
-        // and the first counts are taken around where the last query's cut was
-        float near = guess * most_score;
-        while (!found && hi - lo > eps2) {
-          float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
-          float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
-          if (near != 0.f) {
-            d = 0.1f * fabsf(near);
-            m1 = near - d, m2 = kHeld ? near : near + d, m3 = near + d;
-            near = 0.f;
-          }
-          if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
-          unsigned c = 0;
-          each([&](int, float v) {
-            c += (v > m1 ? 1u : 0u) + (v > m2 ? 1u << kBits : 0u);
-            if constexpr (kHeld) c += v > m3 ? 1u << (2 * kBits) : 0u;
-          });
-          c = __reduce_add_sync(0xffffffffu, c);
-          const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
-          int c3 = 0;
-          if constexpr (kHeld) c3 = (int)(c >> (2 * kBits));
-          if (c1 == r) cut = m1, found = true;
-          else if (c2 == r) cut = m2, found = true;
-          else if (kHeld && c3 == r) cut = m3, found = true;
-          else if (c1 < r) hi = m1;
-          else if (c2 < r) lo = m1, hi = m2;
-          else if (!kHeld) lo = m2;
-          else if (c3 < r) lo = m2, hi = m3;
-          else lo = m3;
-        }
-        if (found && most_score > 1e-20f) guess = cut / most_score;
-        float a = lo, z = hi;
-        if (found) {  // lowest above the cut, highest below
-          int ka = 0x7f800000, kz = (int)0x807fffff;  // as integers that order like the floats
-          each([&](int, float v) {
-            const int k = ordered_int(v);
-            if (v > cut) ka = min(ka, k);
-            else kz = max(kz, k);
-          });
-          a = __int_as_float(ordered_int_inverse(__reduce_min_sync(0xffffffffu, ka)));
-          z = __int_as_float(ordered_int_inverse(__reduce_max_sync(0xffffffffu, kz)));
-        }
-        const bool clear = found && a - z > eps2;
-        const float in_at = clear ? cut : z + eps2, open_at = clear ? INFINITY : a - eps2;
-        int in = 0;
-        each([&](int x, float v) {
-          if (v > in_at) take[x >> 5] |= 1u << (x & 31), ++in;
-          else if (v >= open_at) open[x >> 5] |= 1u << (x & 31);
-        });
-        need = clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
-      } else {
-        for (int x = 0; x < nl; ++x) {
-          const int j = 32 * x + lane;
-          if (j >= j0 && j < j1) open[x >> 5] |= 1u << (x & 31);
-        }
-      }
+      need = pick_approx<NL>(k, sc + rr * ld, most_score, 2.f * (0x1p-13f * most_score + 1e-35f),
+                             guess, lane);
     }
     if (need > 0) {
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        saved[(rr * 2 * W + w) * 32 + lane] = take[w];
-        saved[(rr * 2 * W + W + w) * 32 + lane] = open[w];
+        saved[(rr * 2 * W + w) * 32 + lane] = k.take[w];
+        saved[(rr * 2 * W + W + w) * 32 + lane] = k.open[w];
       }
       if (lane == 0) {
         const int t = atomicAdd(&todo_n, 1);
         todo[t] = make_int2(rr, need);
       }
     } else {
-      put_out(rr, nvis, take);
+      put_out(k, p.topk, out(rr), lane);
     }
   }
   __syncthreads();
-  for (int t0 = warp; t0 < todo_n; t0 += C::kThreads / 32) {
-    const int rr = todo[t0].x, i = i0 + rr, nvis = nv[rr];
-    int need = todo[t0].y;
-    uint32_t* key = reinterpret_cast<uint32_t*>(sc + rr * ld);
-    const int j0 = p.sink, j1 = nvis - p.local, nl = (nvis + 31) / 32;
-    uint32_t take[W], open[W];
-    int undecided = 0;
+  for (int t = warp; t < todo_n; t += C::kThreads / 32) {
+    const int rr = todo[t].x;
+    Picks<NL> k(p, nv[rr]);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      take[w] = saved[(rr * 2 * W + w) * 32 + lane];
-      open[w] = saved[(rr * 2 * W + W + w) * 32 + lane];
-      undecided += __popc(open[w]);
+      k.take[w] = saved[(rr * 2 * W + w) * 32 + lane];
+      k.open[w] = saved[(rr * 2 * W + W + w) * 32 + lane];
     }
-    undecided = __reduce_add_sync(0xffffffffu, undecided);
-    auto each = [&](auto&& f) {
-#pragma unroll 1
-      for (int x = 0; x < nl; ++x) {
-        const int j = 32 * x + lane;
-        if (j >= j0 && j < j1) f(x, j);
-      }
-    };
-    double qd[D / 32] = {};
-    const __nv_bfloat16* q = p.q + b * p.sb + (long long)hk * p.G * p.sh + (long long)i * p.ss;
-#pragma unroll 4
-    for (int g = 0; g < p.G; ++g)
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x)
-        qd[x] += (double)__bfloat162float(q[(long long)g * p.sh + 32 * x + lane]);
-    if (undecided <= 32) {
-      // the usual case: one open block a lane (ascending), its place among them by 64-bit keys
-      int mine = -1, n = 0;
-#pragma unroll 1
-      for (int x = 0; x < nl; ++x) {
-        unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
-        for (; m; m &= m - 1, ++n)
-          if (lane == n) mine = 32 * x + __ffs(m) - 1;
-      }
-      unsigned long long key64 = 0;
-#pragma unroll 2
-      for (int t = 0; t < n; ++t) {
-        const int j = __shfl_sync(0xffffffffu, mine, t);
-        const unsigned long long k = order_key(exact_score<D>(qd, means + (long long)j * D, lane));
-        if (lane == t) key64 = k;
-      }
-      int place = 0;
-#pragma unroll 2
-      for (int t = 0; t < n; ++t) {
-        const unsigned long long k = __shfl_sync(0xffffffffu, key64, t);
-        place += k > key64 || (k == key64 && t < lane);
-      }
-      const bool in = lane < n && place < need;
-#pragma unroll 2
-      for (int t = 0; t < n; ++t) {
-        const int j = __shfl_sync(0xffffffffu, in ? mine : -1, t);
-        if (j >= 0 && (j & 31) == lane)
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-            if (w == j >> 10) take[w] |= 1u << ((j >> 5) & 31);
-      }
-      need = 0;
-    }
-    if (need > 0) {  // many open blocks (equal ones, operands that are not finite)
-      // exact scores of the open blocks, their keys' upper words in place of the scores;
-      // then, among those that tie in it, by the lower words; then by number
-#pragma unroll 1
-      for (int word = 0; word < 2; ++word) {
-#pragma unroll 1
-        for (int x = 0; x < nl; ++x) {
-          unsigned m = __ballot_sync(0xffffffffu, (open[x >> 5] >> (x & 31)) & 1u);
-          while (m) {
-            const int src = __ffs(m) - 1;
-            m &= m - 1;
-            const int j = 32 * x + src;
-            const unsigned long long k =
-                order_key(exact_score<D>(qd, means + (long long)j * D, lane));
-            if (lane == src) key[j] = word == 0 ? (uint32_t)(k >> 32) : (uint32_t)k;
-          }
-        }
-        uint32_t t = 0;  // the need-th largest word, bit by bit
-#pragma unroll 1
-        for (uint32_t bitv = 0x80000000u; bitv; bitv >>= 1) {
-          int c = 0;
-          each([&](int x, int j) {
-            if ((open[x >> 5] >> (x & 31)) & 1u) c += key[j] >= (t | bitv);
-          });
-          if ((int)__reduce_add_sync(0xffffffffu, c) >= need) t |= bitv;
-        }
-        int in = 0, same = 0;
-        each([&](int x, int j) {
-          const uint32_t bx = 1u << (x & 31);
-          if (!(open[x >> 5] & bx)) return;
-          if (key[j] > t) take[x >> 5] |= bx, open[x >> 5] &= ~bx, ++in;
-          else if (key[j] < t) open[x >> 5] &= ~bx;
-          else ++same;
-        });
-        need -= __reduce_add_sync(0xffffffffu, in);
-        same = __reduce_add_sync(0xffffffffu, same);
-        if (same == need) {
-#pragma unroll
-          for (int w = 0; w < W; ++w) take[w] |= open[w], open[w] = 0u;
-          need = 0;
-          break;
-        }
-      }
-      // exact ties: the lowest numbers
-#pragma unroll 1
-      for (int x = 0; x < nl && need > 0; ++x) {
-        const bool tie = (open[x >> 5] >> (x & 31)) & 1u;
-        const unsigned m = __ballot_sync(0xffffffffu, tie);
-        if (tie && __popc(m & ((1u << lane) - 1u)) < need) take[x >> 5] |= 1u << (x & 31);
-        need -= __popc(m);
-      }
-    }
-    put_out(rr, nvis, take);
+    pick_exact<D, NL>(k, todo[t].y, p, b, hk, i0 + rr, means,
+                      reinterpret_cast<uint32_t*>(sc + rr * ld), lane);
+    put_out(k, p.topk, out(rr), lane);
   }
 }
 

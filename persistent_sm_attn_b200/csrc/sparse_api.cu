@@ -503,8 +503,9 @@ int launch_select_tile(const dash::SelectParams& p, int B, cudaStream_t stream) 
 template <int D>
 int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
   if (p.Sq < 16) {
-    dash::dash_block_select_token_kernel<D>
-        <<<dim3(p.Sq, B * p.Hkv), 256, (size_t)p.nb * 8, stream>>>(p);
+    auto kern = p.nb <= 256 ? dash::dash_block_select_token_kernel<D, 8>
+                            : dash::dash_block_select_token_kernel<D, 128>;
+    kern<<<dim3(p.Sq, B * p.Hkv), 256, (size_t)p.nb * 4, stream>>>(p);
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
   }

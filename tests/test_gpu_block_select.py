@@ -140,3 +140,16 @@ def test_select_takes_strided_queries():
     assert not view.is_contiguous()
     assert torch.equal(dash.dash_block_select(view, means, 900, 64, 4),
                        dash.dash_block_select(q, means, 900, 64, 4))
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+@pytest.mark.parametrize("far", [1e3, 1e6])
+def test_heads_that_cancel(Sq, far):
+    # the heads' sum in fp32 would lose what decides: 1000 + x - 1000 keeps few bits of x
+    q, k, _, _ = inputs(1, 4, 1, Sq, 3000, 64, False, 7)
+    q[:, 0], q[:, 2] = far, -far
+    q[:, 1] *= 1e-3
+    q[:, 3] *= 1e-3
+    means = dash.dash_block_means(k, 64)
+    got = dash.dash_block_select(q, means, 3000, 64, 9, False, 1, 1)
+    assert torch.equal(got.cpu(), R.select(q, means, 3000, 64, 9, False, 1, 1))
