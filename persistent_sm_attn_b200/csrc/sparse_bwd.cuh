@@ -702,7 +702,7 @@ struct SparseDkvCfg {
   static constexpr int OFF_KV = kStages * 2 * kTile;  // two of K, then V
   static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS
   static constexpr int OFF_BAR = OFF_P + (D == 64 ? 3 : 2) * kP;  // D = 64: and dS's low part
-  static constexpr int kBars = 4 * kStages + 6 + 7;
+  static constexpr int kBars = 4 * kStages + 12 + 5;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
@@ -750,9 +750,12 @@ __global__ void __launch_bounds__(640, 1)
   auto KV_FULL = [&](int k) { return bar1 + 8u * (uint32_t)(k & 1); };
   auto ITEM_DONE = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
-  auto SDP_FULL = [&](int j) { return bar1 + 48u + 8u * (uint32_t)(j & 1); };
-  const uint32_t PDS_READY = bar1 + 64, PDS_FREE = bar1 + 72, FINAL = bar1 + 96;
+  // per tile parity; P and dS have one buffer each
+  auto S_FULL = [&](int j) { return bar1 + 48u + 8u * (uint32_t)(j & 1); };
+  auto DP_FULL = [&](int j) { return bar1 + 64u + 8u * (uint32_t)(j & 1); };
   auto SDP_READ = [&](int j) { return bar1 + 80u + 8u * (uint32_t)(j & 1); };
+  const uint32_t P_READY = bar1 + 96, P_FREE = bar1 + 104, DS_READY = bar1 + 112;
+  const uint32_t DS_FREE = bar1 + 120, FINAL = bar1 + 128;
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phS = [](int j) { return (uint32_t)((j / ST) & 1); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_SLOT);
@@ -774,11 +777,14 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(KV_FULL(k), 1);
       mbar_init(ITEM_DONE(k), 1);
       mbar_init(ACC_FREE(k), 8);
-      mbar_init(SDP_FULL(k), 1);
+      mbar_init(S_FULL(k), 1);
+      mbar_init(DP_FULL(k), 1);
       mbar_init(SDP_READ(k), 8);
     }
-    mbar_init(PDS_READY, 8);
-    mbar_init(PDS_FREE, 1);
+    mbar_init(P_READY, 8);
+    mbar_init(P_FREE, 1);
+    mbar_init(DS_READY, 8);
+    mbar_init(DS_FREE, 1);
     mbar_init(FINAL, 2);
     fence_mbar_init();
   }
@@ -849,103 +855,113 @@ __global__ void __launch_bounds__(640, 1)
       }
       w = nw;
     }
-  } else if (warp == 9 && lane == 0) {
-    // ---------------------------------------------------------------- K and V
-    int k = 0;
-    for (; snake_item(k) < items; ++k) {
-      const SparseItem w = p.item[snake_item(k)];
-      const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
-      // K and V of item k - 2 are read to the end; nothing is loaded once a wait has run out
-      if (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2))) break;
-      mbar_expect_tx(KV_FULL(k), 2 * C::kKV);
+  } else if (warp < 12) {
+    if (warp == 9 && lane == 0) {
+      // ---------------------------------------------------------------- K and V
+      int k = 0;
+      for (; snake_item(k) < items; ++k) {
+        const SparseItem w = p.item[snake_item(k)];
+        const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
+        // K and V of item k - 2 are read to the end; nothing is loaded once a wait has run out
+        if (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2))) break;
+        mbar_expect_tx(KV_FULL(k), 2 * C::kKV);
 #pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb) {
-        tma_load_4d(sK(k) + cb * 8192, &tmK, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
-        tma_load_4d(sV(k) + cb * 8192, &tmV, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
-      }
-    }
-    // no load may land after the CTA has gone, not even when a wait ran out
-    for (int j = max(0, k - 2); j < k; ++j)
-      mbar_wait_drain(KV_FULL(j), ph2(j), drain_ns(p.spin_ns), p.err, p.err + 1);
-  } else if (warp == 8 || warp == 10) {
-    // ---------------------------------------------------------------- product issuers
-    // Two of them, S and dP and beside them dV and dK (see the dQ kernel)
-    const bool leader = elect_one();
-    const uint32_t hi = sdesc_hi(1024);
-    bool ok = true;  // no wait has run out: else no more products
-    int j = 0, k = 0, s = 0;
-    uint32_t sph = 0;
-#pragma unroll 1
-    for (; snake_item(k) < items && ok; ++k) {
-      const int first = p.item[snake_item(k)].first, end = p.item[snake_item(k)].end;
-      if (warp == 8) {
-        constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
-        const uint32_t kK = sdesc_lo(sK(k), 16), kV = sdesc_lo(sV(k), 16);
-        ok = wait(KV_FULL(k), ph2(k));
-#pragma unroll 1
-        for (int e = first; e < end && ok; ++e, ++j) {
-          const uint32_t kQ = sdesc_lo(sQ(s), 16), kDO = sdesc_lo(sDO(s), 16);
-          const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(j & 1);
-          ok = wait(FULL(0, s), sph) && (j < 2 || wait(SDP_READ(j), ph2(j - 2)));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                          kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                          kk > 0 ? 1u : 0u);
-          ok = wait(FULL(1, s), sph);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                          kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
-                          kk > 0 ? 1u : 0u);
-            tc_commit(SDP_FULL(j));
-          }
-          if (++s == ST) s = 0, sph ^= 1u;
+        for (int cb = 0; cb < D / 64; ++cb) {
+          tma_load_4d(sK(k) + cb * 8192, &tmK, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
+          tma_load_4d(sV(k) + cb * 8192, &tmV, cb * 64, u * kUnit, hk, w.b, KV_FULL(k));
         }
-      } else {
-        constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
-        const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384), bL = sdesc_lo(sL, 16384);
-        const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
-        // the accumulators of item k - 2 must have been read
-        if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
+      }
+      // no load may land after the CTA has gone, not even when a wait ran out
+      for (int j = max(0, k - 2); j < k; ++j)
+        mbar_wait_drain(KV_FULL(j), ph2(j), drain_ns(p.spin_ns), p.err, p.err + 1);
+    } else if (warp == 8 || warp == 10) {
+      // ---------------------------------------------------------------- product issuers
+      // Two of them, S and dP and beside them dV and dK (see the dQ kernel)
+      const bool leader = elect_one();
+      const uint32_t hi = sdesc_hi(1024);
+      bool ok = true;  // no wait has run out: else no more products
+      int j = 0, k = 0, s = 0;
+      uint32_t sph = 0;
 #pragma unroll 1
-        for (int e = first; e < end && ok; ++e, ++j) {
-          const uint32_t aV = sdesc_lo(sDO(s), 16384);
-          const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
-          ok = wait(PDS_READY, (uint32_t)(j & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
+      for (; snake_item(k) < items && ok; ++k) {
+        const int first = p.item[snake_item(k)].first, end = p.item[snake_item(k)].end;
+        if (warp == 8) {
+          constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
+          const uint32_t kK = sdesc_lo(sK(k), 16), kV = sdesc_lo(sV(k), 16);
+          ok = wait(KV_FULL(k), ph2(k));
+#pragma unroll 1
+          for (int e = first; e < end && ok; ++e, ++j) {
+            const uint32_t kQ = sdesc_lo(sQ(s), 16), kDO = sdesc_lo(sDO(s), 16);
+            const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(j & 1);
+            ok = wait(FULL(0, s), sph) && (j < 2 || wait(SDP_READ(j), ph2(j - 2)));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (uint32_t)(e - first + kk));
-            if (D == 128) tc_commit(EMPTY(1, s));
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_ss_w(tS, kQ + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            kK + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                            kk > 0 ? 1u : 0u);
+              tc_commit(S_FULL(j));
+            }
+            ok = wait(FULL(1, s), sph);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
-                          (uint32_t)(e - first + kk));
-            if (kLow)
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_ss_w(tS + 64, kDO + (uint32_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                            kV + (uint32_t)(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), hi, ID_S,
+                            kk > 0 ? 1u : 0u);
+              tc_commit(DP_FULL(j));
+            }
+            if (++s == ST) s = 0, sph ^= 1u;
+          }
+        } else {
+          constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
+          const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384), bL = sdesc_lo(sL, 16384);
+          const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
+          // the accumulators of item k - 2 must have been read
+          if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
+#pragma unroll 1
+          for (int e = first; e < end && ok; ++e, ++j) {
+            const uint32_t aV = sdesc_lo(sDO(s), 16384);
+            const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
+            ok = wait(P_READY, (uint32_t)(j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ss_w(tA + 64, aK + kk * 128, bL + kk * 128, hi, ID_T, 1u);
-            if (D == 64) tc_commit(EMPTY(1, s));
-            tc_commit(EMPTY(0, s));
-            tc_commit(PDS_FREE);
-            if (e + 1 == end) tc_commit(ITEM_DONE(k));
+                tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (uint32_t)(e - first + kk));
+              tc_commit(P_FREE);
+              if (D == 128) tc_commit(EMPTY(1, s));
+            }
+            ok = wait(DS_READY, (uint32_t)(j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ss_w(tA + 64, aK + kk * 128, bS + kk * 128, hi, ID_T,
+                            (uint32_t)(e - first + kk));
+              if (kLow)
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  tc_mma_ss_w(tA + 64, aK + kk * 128, bL + kk * 128, hi, ID_T, 1u);
+              if (D == 64) tc_commit(EMPTY(1, s));
+              tc_commit(EMPTY(0, s));
+              tc_commit(DS_FREE);
+              if (e + 1 == end) tc_commit(ITEM_DONE(k));
+            }
+            if (++s == ST) s = 0;
           }
-          if (++s == ST) s = 0;
         }
       }
+      if (leader) tc_commit(FINAL);  // the CTA does not go before its products
+      mbar_wait_drain(FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
     }
-    if (leader) tc_commit(FINAL);  // the CTA does not go before its products
-    mbar_wait_drain(FINAL, 0, drain_ns(p.spin_ns), p.err, p.err + 1);
-  } else if (warp >= 12) {
+  } else {
     // ---------------------------------------------------------------- softmax gradient
     const int wg = (warp - 12) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
@@ -988,50 +1004,73 @@ __global__ void __launch_bounds__(640, 1)
         else if (more) fetch(nw, nw.first);
         const bool whole = __all_sync(0xffffffffu, v >= 32);
         const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(it & 1) + 32u * wg;
-        wait(SDP_FULL(it), ph2(it));
+        wait(S_FULL(it), ph2(it));
         tc_fence_after();
+        // P, of which the dV product can be issued while dS is computed
+        float pr[32];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t sv[16], dp[16];
-          tmem_ld16_async(tS + 16 * h, sv);
-          tmem_ld16_async(tS + 64 + 16 * h, dp);
-          tmem_wait_ld();
-          if (h == 1) {
+        for (int c = 0; c < 32; c += 16) {
+          uint32_t sv[16];
+          tmem_ld16(tS + c, sv);
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            fma_f32x2(pr[c + x], pr[c + x + 1], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]),
+                      sl2, -l2);
+            pr[c + x] = ex2_approx(pr[c + x]);
+            pr[c + x + 1] = ex2_approx(pr[c + x + 1]);
+          }
+        }
+        if (!whole)  // selected, not multiplied: S and dP of a masked key may be anything
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (x >= v) pr[x] = 0.f;
+        if (it > 0) wait(P_FREE, (uint32_t)((it - 1) & 1));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t off = (uint32_t)(((4 * wg + x) ^ (r & 7)) << 4);
+          st_shared_v4(rowP + off, pack_bf16x2(pr[8 * x], pr[8 * x + 1]),
+                       pack_bf16x2(pr[8 * x + 2], pr[8 * x + 3]),
+                       pack_bf16x2(pr[8 * x + 4], pr[8 * x + 5]),
+                       pack_bf16x2(pr[8 * x + 6], pr[8 * x + 7]));
+        }
+        fence_proxy_async_smem();
+        warp_arrive(P_READY, lane);
+        wait(DP_FULL(it), ph2(it));
+        tc_fence_after();
+        if (it > 0) wait(DS_FREE, (uint32_t)((it - 1) & 1));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t dp[16];
+          tmem_ld16(tS + 64 + 16 * c, dp);
+          if (c == 1) {
             tc_fence_before();
             warp_arrive(SDP_READ(it), lane);
           }
-          uint32_t pp[8], ds[8], low[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            float p0, p1, d0, d1;
-            fma_f32x2(p0, p1, __uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]), sl2, -l2);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            add_f32x2(d0, d1, __uint_as_float(dp[2 * x]), __uint_as_float(dp[2 * x + 1]), -dl);
-            mul_f32x2(d0, d1, p0, p1, d0, d1);
-            if (!whole) {  // selected, not multiplied: S and dP of a masked key may be anything
-              if (16 * h + 2 * x >= v) p0 = d0 = 0.f;
-              if (16 * h + 2 * x + 1 >= v) p1 = d1 = 0.f;
-            }
-            pp[x] = pack_bf16x2(p0, p1);
-            ds[x] = pack_bf16x2(d0, d1);
-            if (kLow)
-              low[x] = pack_bf16x2(d0 - __uint_as_float(ds[x] << 16),
-                                   d1 - __uint_as_float(ds[x] & 0xffff0000u));
-          }
-          if (h == 0 && it > 0) wait(PDS_FREE, (uint32_t)((it - 1) & 1));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t off = (uint32_t)(((4 * wg + 2 * h + x) ^ (r & 7)) << 4);
-            st_shared_v4(rowP + off, pp[4 * x], pp[4 * x + 1], pp[4 * x + 2], pp[4 * x + 3]);
-            st_shared_v4(rowS + off, ds[4 * x], ds[4 * x + 1], ds[4 * x + 2], ds[4 * x + 3]);
-            if (kLow)
-              st_shared_v4(rowL + off, low[4 * x], low[4 * x + 1], low[4 * x + 2], low[4 * x + 3]);
+            uint32_t ds[4], low[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int z = 8 * x + 2 * y, q = 16 * c + z;
+              float d0, d1;
+              add_f32x2(d0, d1, __uint_as_float(dp[z]), __uint_as_float(dp[z + 1]), -dl);
+              mul_f32x2(d0, d1, pr[q], pr[q + 1], d0, d1);
+              if (!whole) {
+                if (q >= v) d0 = 0.f;
+                if (q + 1 >= v) d1 = 0.f;
+              }
+              ds[y] = pack_bf16x2(d0, d1);
+              if (kLow)
+                low[y] = pack_bf16x2(d0 - __uint_as_float(ds[y] << 16),
+                                     d1 - __uint_as_float(ds[y] & 0xffff0000u));
+            }
+            const uint32_t off = (uint32_t)(((4 * wg + 2 * c + x) ^ (r & 7)) << 4);
+            st_shared_v4(rowS + off, ds[0], ds[1], ds[2], ds[3]);
+            if (kLow) st_shared_v4(rowL + off, low[0], low[1], low[2], low[3]);
           }
         }
         fence_proxy_async_smem();
-        tc_fence_before();
-        warp_arrive(PDS_READY, lane);
+        warp_arrive(DS_READY, lane);
       }
       // epilogue: warpgroup 0 writes dV, warpgroup 1 dK; lane = head dimension, column = key
       wait(ITEM_DONE(k), ph2(k));
