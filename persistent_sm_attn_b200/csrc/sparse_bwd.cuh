@@ -697,12 +697,15 @@ struct SparseDkvCfg {
   static constexpr int kTile = kTileRows * D * 2;
   static constexpr int kKV = kUnit * D * 2;
   static constexpr int kP = kTileRows * kUnit * 2;  // [128][64] bf16
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  // D = 64 has room for P and dS of two tiles: the warpgroups take tiles in turn
+  static constexpr bool kTurns = D == 64;
   static constexpr int OFF_QDO = 0;  // per stage dO, then Q: at D = 64 one [dO | Q] operand
   static constexpr int OFF_KV = kStages * 2 * kTile;  // two of K, then V
-  static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS
-  static constexpr int OFF_BAR = OFF_P + (D == 64 ? 3 : 2) * kP;  // D = 64: and dS's low part
-  static constexpr int kBars = 4 * kStages + 12 + 5;
+  static constexpr int OFF_P = OFF_KV + 4 * kKV;      // P, then dS, then (D = 64) its low part
+  static constexpr int kPDS = (D == 64 ? 3 : 2) * kP;
+  static constexpr int OFF_BAR = OFF_P + (kTurns ? 2 : 1) * kPDS;
+  static constexpr int kBars = 4 * kStages + 12 + 9;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(640, 1)
   auto sQ = [&](int s) { return sDO(s) + C::kTile; };
   auto sK = [&](int k) { return sb + C::OFF_KV + (uint32_t)((k & 1) * 2 * C::kKV); };
   auto sV = [&](int k) { return sK(k) + C::kKV; };
-  const uint32_t sP = sb + C::OFF_P, sS = sP + C::kP, sL = sS + C::kP;
+  auto sP = [&](int j) { return sb + C::OFF_P + (C::kTurns ? (uint32_t)((j & 1) * C::kPDS) : 0u); };
   const uint32_t bar0 = sb + C::OFF_BAR;
   // per stage (Q, dO), per item parity, per tile parity
   auto FULL = [&](int x, int s) { return bar0 + 8u * (uint32_t)(x * ST + s); };
@@ -750,12 +753,15 @@ __global__ void __launch_bounds__(640, 1)
   auto KV_FULL = [&](int k) { return bar1 + 8u * (uint32_t)(k & 1); };
   auto ITEM_DONE = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
-  // per tile parity; P and dS have one buffer each
+  // per tile parity
   auto S_FULL = [&](int j) { return bar1 + 48u + 8u * (uint32_t)(j & 1); };
   auto DP_FULL = [&](int j) { return bar1 + 64u + 8u * (uint32_t)(j & 1); };
   auto SDP_READ = [&](int j) { return bar1 + 80u + 8u * (uint32_t)(j & 1); };
-  const uint32_t P_READY = bar1 + 96, P_FREE = bar1 + 104, DS_READY = bar1 + 112;
-  const uint32_t DS_FREE = bar1 + 120, FINAL = bar1 + 128;
+  auto P_READY = [&](int j) { return bar1 + 96u + 8u * (uint32_t)(j & 1); };
+  auto P_FREE = [&](int j) { return bar1 + 112u + 8u * (uint32_t)(j & 1); };
+  auto DS_READY = [&](int j) { return bar1 + 128u + 8u * (uint32_t)(j & 1); };
+  auto DS_FREE = [&](int j) { return bar1 + 144u + 8u * (uint32_t)(j & 1); };
+  const uint32_t FINAL = bar1 + 160;
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phS = [](int j) { return (uint32_t)((j / ST) & 1); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + C::OFF_SLOT);
@@ -779,12 +785,12 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(ACC_FREE(k), 8);
       mbar_init(S_FULL(k), 1);
       mbar_init(DP_FULL(k), 1);
-      mbar_init(SDP_READ(k), 8);
+      mbar_init(SDP_READ(k), C::kTurns ? 4 : 8);
+      mbar_init(P_READY(k), 8);
+      mbar_init(P_FREE(k), 1);
+      mbar_init(DS_READY(k), C::kTurns ? 4 : 8);
+      mbar_init(DS_FREE(k), 1);
     }
-    mbar_init(P_READY, 8);
-    mbar_init(P_FREE, 1);
-    mbar_init(DS_READY, 8);
-    mbar_init(DS_FREE, 1);
     mbar_init(FINAL, 2);
     fence_mbar_init();
   }
@@ -919,25 +925,26 @@ __global__ void __launch_bounds__(640, 1)
           }
         } else {
           constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
-          const uint32_t bP = sdesc_lo(sP, 16384), bS = sdesc_lo(sS, 16384), bL = sdesc_lo(sL, 16384);
-          const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
+            const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
           // the accumulators of item k - 2 must have been read
           if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
 #pragma unroll 1
           for (int e = first; e < end && ok; ++e, ++j) {
             const uint32_t aV = sdesc_lo(sDO(s), 16384);
             const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
-            ok = wait(P_READY, (uint32_t)(j & 1));
+          const uint32_t bP = sdesc_lo(sP(j), 16384), bS = sdesc_lo(sP(j) + C::kP, 16384);
+          const uint32_t bL = sdesc_lo(sP(j) + 2 * C::kP, 16384);
+            ok = wait(C::kTurns ? DS_READY(j) : P_READY(j), ph2(j));
             if (!ok) break;
             tc_fence_after();
             if (leader) {
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (uint32_t)(e - first + kk));
-              tc_commit(P_FREE);
+              tc_commit(P_FREE(j));
               if (D == 128) tc_commit(EMPTY(1, s));
             }
-            ok = wait(DS_READY, (uint32_t)(j & 1));
+            ok = C::kTurns || wait(DS_READY(j), ph2(j));
             if (!ok) break;
             tc_fence_after();
             if (leader) {
@@ -951,7 +958,7 @@ __global__ void __launch_bounds__(640, 1)
                   tc_mma_ss_w(tA + 64, aK + kk * 128, bL + kk * 128, hi, ID_T, 1u);
               if (D == 64) tc_commit(EMPTY(1, s));
               tc_commit(EMPTY(0, s));
-              tc_commit(DS_FREE);
+              tc_commit(DS_FREE(j));
               if (e + 1 == end) tc_commit(ITEM_DONE(k));
             }
             if (++s == ST) s = 0;
@@ -967,7 +974,6 @@ __global__ void __launch_bounds__(640, 1)
     const int r = quarter * 32 + lane;
     const int t = (int)((uint32_t)r * inv_g >> 16), g = r - t * p.G;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t rowP = sP + r * 128, rowS = sS + r * 128, rowL = sL + r * 128;
     const float sl2 = p.scale_log2;
     // what this thread's row of a tile needs, fetched one tile ahead
     float lse2 = 0.f, delta = 0.f;
@@ -987,23 +993,93 @@ __global__ void __launch_bounds__(640, 1)
       delta = p.delta[row];
       if (p.causal) vis = (int)min((long long)kvlen, (long long)p.plan.start[w.b] + token + 1) - base;
     };
-    int it = 0, k = 0;
+    // the tiles e that this warpgroup takes: all, or with kTurns those of its parity
+    constexpr int kStep = C::kTurns ? 2 : 1;
+    int it0 = 0, k = 0;  // the item's first tile number, the item's number
     SparseItem w;
-    if (snake_item(0) < items) {
-      w = p.item[snake_item(0)];
-      fetch(w, w.first);
-    }
+    if (snake_item(0) < items) w = p.item[snake_item(0)];
+    bool have = false;  // lse2, delta and vis are those of the next tile taken
     for (; snake_item(k) < items; ++k) {
       const bool more = snake_item(k + 1) < items;
       SparseItem nw = w;
       if (more) nw = p.item[snake_item(k + 1)];
-      for (int e = w.first; e < w.end; ++e, ++it) {
+      auto first_own = [&](const SparseItem& x, int at) {
+        return x.first + (C::kTurns ? ((at ^ wg) & 1) : 0);
+      };
+      const int it1 = it0 + w.end - w.first, own = first_own(w, it0);
+      if (!have && own < w.end) fetch(w, own);
+      have = false;
+      for (int e = own; e < w.end; e += kStep) {
+        const int it = it0 + e - w.first;
         const float l2 = lse2, dl = delta;
-        const int v = vis - 32 * wg;
-        if (e + 1 < w.end) fetch(w, e + 1);
-        else if (more) fetch(nw, nw.first);
-        const bool whole = __all_sync(0xffffffffu, v >= 32);
-        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(it & 1) + 32u * wg;
+        const int v = C::kTurns ? vis : vis - 32 * wg;
+        if (e + kStep < w.end) {
+          fetch(w, e + kStep);
+        } else if (more && first_own(nw, it1) < nw.end) {
+          fetch(nw, first_own(nw, it1));
+          have = true;
+        }
+        const bool whole = __all_sync(0xffffffffu, v >= (C::kTurns ? kUnit : 32));
+        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(it & 1) +
+                            (C::kTurns ? 0u : 32u * wg);
+        const uint32_t rowP = sP(it) + r * 128, rowS = rowP + C::kP, rowL = rowS + C::kP;
+        // two keys of a row from S and dP: dS and P as bf16 pairs
+        auto to_ds = [&](int key, float p0, float p1, uint32_t dp0, uint32_t dp1, uint32_t& ds,
+                         uint32_t& low) {
+          float d0, d1;
+          add_f32x2(d0, d1, __uint_as_float(dp0), __uint_as_float(dp1), -dl);
+          mul_f32x2(d0, d1, p0, p1, d0, d1);
+          if (!whole) {  // selected, not multiplied: S and dP of a masked key may be anything
+            if (key >= v) d0 = 0.f;
+            if (key + 1 >= v) d1 = 0.f;
+          }
+          ds = pack_bf16x2(d0, d1);
+          if (kLow)
+            low = pack_bf16x2(d0 - __uint_as_float(ds << 16), d1 - __uint_as_float(ds & 0xffff0000u));
+        };
+        if constexpr (C::kTurns) {
+          wait(S_FULL(it), ph2(it));
+          wait(DP_FULL(it), ph2(it));
+          tc_fence_after();
+          if (it >= 2) wait(DS_FREE(it), ph2(it - 2));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t sv[16], dp[16];
+            tmem_ld16_async(tS + 16 * c, sv);
+            tmem_ld16_async(tS + 64 + 16 * c, dp);
+            tmem_wait_ld();
+            if (c == 3) {
+              tc_fence_before();
+              warp_arrive(SDP_READ(it), lane);
+            }
+            uint32_t pp[8], ds[8], low[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int key = 16 * c + 2 * x;
+              float p0, p1;
+              fma_f32x2(p0, p1, __uint_as_float(sv[2 * x]), __uint_as_float(sv[2 * x + 1]), sl2, -l2);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              if (!whole) {
+                if (key >= v) p0 = 0.f;
+                if (key + 1 >= v) p1 = 0.f;
+              }
+              pp[x] = pack_bf16x2(p0, p1);
+              to_ds(key, p0, p1, dp[2 * x], dp[2 * x + 1], ds[x], low[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t off = (uint32_t)(((2 * c + x) ^ (r & 7)) << 4);
+              st_shared_v4(rowP + off, pp[4 * x], pp[4 * x + 1], pp[4 * x + 2], pp[4 * x + 3]);
+              st_shared_v4(rowS + off, ds[4 * x], ds[4 * x + 1], ds[4 * x + 2], ds[4 * x + 3]);
+              if (kLow)
+                st_shared_v4(rowL + off, low[4 * x], low[4 * x + 1], low[4 * x + 2], low[4 * x + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+          warp_arrive(DS_READY(it), lane);
+          continue;
+        }
         wait(S_FULL(it), ph2(it));
         tc_fence_after();
         // P, of which the dV product can be issued while dS is computed
@@ -1024,7 +1100,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (x >= v) pr[x] = 0.f;
-        if (it > 0) wait(P_FREE, (uint32_t)((it - 1) & 1));
+        if (it > 0) wait(P_FREE(it - 1), ph2(it - 1));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const uint32_t off = (uint32_t)(((4 * wg + x) ^ (r & 7)) << 4);
@@ -1034,10 +1110,10 @@ __global__ void __launch_bounds__(640, 1)
                        pack_bf16x2(pr[8 * x + 6], pr[8 * x + 7]));
         }
         fence_proxy_async_smem();
-        warp_arrive(P_READY, lane);
+        warp_arrive(P_READY(it), lane);
         wait(DP_FULL(it), ph2(it));
         tc_fence_after();
-        if (it > 0) wait(DS_FREE, (uint32_t)((it - 1) & 1));
+        if (it > 0) wait(DS_FREE(it - 1), ph2(it - 1));
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t dp[16];
@@ -1052,17 +1128,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const int z = 8 * x + 2 * y, q = 16 * c + z;
-              float d0, d1;
-              add_f32x2(d0, d1, __uint_as_float(dp[z]), __uint_as_float(dp[z + 1]), -dl);
-              mul_f32x2(d0, d1, pr[q], pr[q + 1], d0, d1);
-              if (!whole) {
-                if (q >= v) d0 = 0.f;
-                if (q + 1 >= v) d1 = 0.f;
-              }
-              ds[y] = pack_bf16x2(d0, d1);
-              if (kLow)
-                low[y] = pack_bf16x2(d0 - __uint_as_float(ds[y] << 16),
-                                     d1 - __uint_as_float(ds[y] & 0xffff0000u));
+              to_ds(q, pr[q], pr[q + 1], dp[z], dp[z + 1], ds[y], low[y]);
             }
             const uint32_t off = (uint32_t)(((4 * wg + 2 * c + x) ^ (r & 7)) << 4);
             st_shared_v4(rowS + off, ds[0], ds[1], ds[2], ds[3]);
@@ -1070,7 +1136,7 @@ __global__ void __launch_bounds__(640, 1)
           }
         }
         fence_proxy_async_smem();
-        warp_arrive(DS_READY, lane);
+        warp_arrive(DS_READY(it), lane);
       }
       // epilogue: warpgroup 0 writes dV, warpgroup 1 dK; lane = head dimension, column = key
       wait(ITEM_DONE(k), ph2(k));
@@ -1104,6 +1170,7 @@ __global__ void __launch_bounds__(640, 1)
         }
       }
       w = nw;
+      it0 = it1;
     }
   }
   tc_fence_before();
