@@ -85,24 +85,25 @@ struct SparseDqCfg {
   static constexpr int OFF_K = kQ * 2 * kTile;
   static constexpr int OFF_V = OFF_K + kK * kKV;
   static constexpr int OFF_BAR = OFF_V + kV * kKV;
-  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 2 * 4 + 4 + 1;
+  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 3 * 3 + 1;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
   static_assert(kSmemBytes > 116 * 1024, "one CTA per SM: its 512 TMEM columns are free");
   static constexpr int kAcc = D == 128 ? 1 : 2;  // accumulators
-  static constexpr uint32_t TM_S = 0, TM_DS = 256, TM_DQ = 384, kTmemCols = 512;
+  static constexpr uint32_t TM_S = 0, TM_DQ = 384, kTmemCols = 512;
 };
 
 // A persistent CTA per SM takes query tiles, those with the longest lists (the last, under a
 // causal mask) first.  Per listed unit j: S = Q K^T, dP = dO V^T (128 x 64, TMEM), dS in bf16
-// to TMEM, dQ += dS K.  Even and odd units are two streams, each with its buffers, its issuer
-// of S and dP and its softmax warpgroup, so that one stream's exponentials run beside the
-// other's dS; S and dP are free again as soon as they are read.  (One stream of 128-key
-// products, both warpgroups on the same pair, measured 231 us at 16 heads of 8k, D = 128, 16
-// picks of 64, and 408 us at 8 heads of 16k, D = 64, 8 picks of 128: exponentials and the
-// rest took turns.)  Row t G + g of a tile is token t, head g, so a warp holds few tokens and
-// skips the exponentials of units that none of them picked.
+// over S, dQ += dS K.  Even and odd units have an issuer of S and dP and a softmax warpgroup
+// each, so that one unit's exponentials run beside the other's dS; three buffers of S and dP
+// turn, and a unit's products wait only for the dQ product three units back.  (Two buffers,
+// free again as they were read: 226 us at 16 heads of 8k, D = 128, 16 picks of 64, 351 us at 8
+// heads of 16k, D = 64, 8 picks of 128.  One stream of 128-key products, both warpgroups on
+// the same pair: 231 and 408, exponentials and the rest took turns.)  Row t G + g of a tile is
+// token t, head g, so a warp holds few tokens and skips the exponentials of units that none
+// of them picked.
 //
 // kLow: dS enters its product as the sum of two bf16 values instead of one, whose rounding of
 // up to 2^-8 is otherwise the larger part of the result's error; see sparse_low_part.
@@ -137,14 +138,13 @@ __global__ void __launch_bounds__(384, 1)
   auto Q_EMPTY = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto DONE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 48u + 8u * (uint32_t)(k & 1); };
-  // per stream
+  // per buffer of S and dP
   const uint32_t bar2 = bar1 + 64u;
-  auto S_FULL = [&](int j) { return bar2 + 8u * (uint32_t)(j & 1); };
-  auto S_READ = [&](int j) { return bar2 + 16u + 8u * (uint32_t)(j & 1); };
-  auto DP_FULL = [&](int j) { return bar2 + 32u + 8u * (uint32_t)(j & 1); };
-  auto DP_READ = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j & 1); };
-  auto DS_READY = [&](int j) { return bar2 + 64u + 8u * (uint32_t)(j & 3); };
-  const uint32_t FINAL = bar2 + 96;
+  auto S_FULL = [&](int j) { return bar2 + 8u * (uint32_t)(j % 3); };
+  auto DP_FULL = [&](int j) { return bar2 + 24u + 8u * (uint32_t)(j % 3); };
+  auto DS_READY = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j % 3); };
+  const uint32_t FINAL = bar2 + 72;
+  auto ph3 = [](int j) { return (uint32_t)((j / 3) & 1); };
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phK = [](int j) { return (uint32_t)((j / C::kK) & 1); };
   auto phV = [](int j) { return (uint32_t)((j / C::kV) & 1); };
@@ -178,13 +178,11 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(DONE(k), 1);
       mbar_init(ACC_FREE(k), 8);
     }
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 3; ++j) {
       mbar_init(S_FULL(j), 1);
-      mbar_init(S_READ(j), 4);
       mbar_init(DP_FULL(j), 1);
-      mbar_init(DP_READ(j), 4);
+      mbar_init(DS_READY(j), 4);
     }
-    for (int j = 0; j < 4; ++j) mbar_init(DS_READY(j), 4);
     mbar_init(FINAL, 3);
     fence_mbar_init();
   }
@@ -276,13 +274,14 @@ __global__ void __launch_bounds__(384, 1)
       if (warp < 3) {
         constexpr uint32_t ID_S = idesc_bf16_f32(128, kUnit, 0, 0);
         const uint32_t kQ = sdesc_lo(sQ(k), 16), kDO = sdesc_lo(sDO(k), 16);
-        const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(warp - 1);
         ok = wait(Q_FULL(k), ph2(k));
 #pragma unroll 1
         for (int e = (j0 ^ (warp - 1)) & 1; e < n && ok; e += 2) {
           const int j = j0 + e;
           const uint32_t kK = sdesc_lo(sK(j), 16), kV = sdesc_lo(sV(j), 16);
-          ok = wait(K_FULL(j), phK(j)) && (j < 2 || wait(S_READ(j), ph2(j - 2)));
+          const uint32_t tS = tmem + C::TM_S + 128u * (uint32_t)(j % 3);
+          // dS of unit j - 3 lay in S's columns
+          ok = wait(K_FULL(j), phK(j)) && (j < 3 || wait(K_EMPTY(j - 3), phK(j - 3)));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(384, 1)
                           kk > 0 ? 1u : 0u);
             tc_commit(S_FULL(j));
           }
-          ok = wait(V_FULL(j), phV(j)) && (j < 2 || wait(DP_READ(j), ph2(j - 2)));
+          ok = wait(V_FULL(j), phV(j));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -316,8 +315,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int e = 0; e < n && ok; ++e) {
           const int j = j0 + e;
           const uint32_t mK = sdesc_lo(sK(j), 8192);
-          const uint32_t tDS = tmem + C::TM_DS + (kLow ? 64u * (uint32_t)(j & 1) : 32u * (uint32_t)(j & 3));
-          ok = wait(DS_READY(j), (uint32_t)((j >> 2) & 1));
+          const uint32_t tDS = tmem + C::TM_S + 128u * (uint32_t)(j % 3);
+          ok = wait(DS_READY(j), ph3(j));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -381,16 +380,13 @@ __global__ void __launch_bounds__(384, 1)
         const bool any = __any_sync(0xffffffffu, v > 0);
         const bool clean = __all_sync(0xffffffffu, v >= kUnit || v <= 0);
         const uint32_t keep = v > 0 ? 0xffffffffu : 0u;
-        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * h, tDP = tS + 64;
-        const uint32_t tDS = tmem + lane_off + C::TM_DS + (kLow ? 64u * h : 32u * (uint32_t)(j & 3));
+        const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(j % 3), tDP = tS + 64;
         float pr[kUnit];
-        wait(S_FULL(j), ph2(j));
+        wait(S_FULL(j), ph3(j));
         tc_fence_after();
         if (any) {
           uint32_t sv[2][32];
           tmem_ld32x2(tS, tS + 32, sv[0], sv[1]);
-          tc_fence_before();
-          warp_arrive(S_READ(j), lane);
 #pragma unroll
           for (int x = 0; x < kUnit; x += 2) {
             fma_f32x2(pr[x], pr[x + 1], __uint_as_float(sv[x >> 5][x & 31]),
@@ -398,8 +394,6 @@ __global__ void __launch_bounds__(384, 1)
             pr[x] = ex2_approx(pr[x]);
             pr[x + 1] = ex2_approx(pr[x + 1]);
           }
-        } else {
-          warp_arrive(S_READ(j), lane);
         }
         if (partial) {
           // K rows past the sequence hold whatever the cache holds: 0 * NaN would reach dQ
@@ -410,19 +404,13 @@ __global__ void __launch_bounds__(384, 1)
           }
           fence_proxy_async_smem();
         }
-        constexpr int kBack = kLow ? 2 : 4;  // dS has two buffers of two parts or four of one
-        if (j >= kBack) wait(K_EMPTY(j - kBack), phK(j - kBack));
-        wait(DP_FULL(j), ph2(j));
+        wait(DP_FULL(j), ph3(j));
         tc_fence_after();
         if (any) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t dp[32], pk[16], low[16];
             tmem_ld32(tDP + 32 * c, dp);
-            if (c == 1) {
-              tc_fence_before();
-              warp_arrive(DP_READ(j), lane);
-            }
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               float d0, d1;
@@ -438,14 +426,13 @@ __global__ void __launch_bounds__(384, 1)
                 low[x] = pack_bf16x2(d0 - __uint_as_float(high << 16),
                                      d1 - __uint_as_float(high & 0xffff0000u)) & keep;
             }
-            tmem_st16(tDS + 16 * c, pk);
-            if (kLow) tmem_st16(tDS + 32 + 16 * c, low);
+            tmem_st16(tS + 16 * c, pk);
+            if (kLow) tmem_st16(tS + 32 + 16 * c, low);
           }
         } else {
-          warp_arrive(DP_READ(j), lane);
           const uint32_t zero[16] = {};
 #pragma unroll
-          for (int c = 0; c < (kLow ? 4 : 2); ++c) tmem_st16(tDS + 16 * c, zero);
+          for (int c = 0; c < (kLow ? 4 : 2); ++c) tmem_st16(tS + 16 * c, zero);
         }
         tmem_wait_st();
         tc_fence_before();
