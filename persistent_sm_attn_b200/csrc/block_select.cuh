@@ -475,6 +475,7 @@ struct SelectCfg {
   static constexpr int kLd = D * 2 + 16;           // bytes of a staged row: no bank conflicts
   static constexpr int kQ = 2 * kRows * kLd;       // queries, high and low parts
   static constexpr int kStage = kQ + 2 * 64 * kLd; // and 64 means
+  static constexpr float kError = 1.001f * (3 * 0x1p-16f + (3 * D + 3) * 0x1p-23f);
   static int smem(int nb) { return kStage + QT * ((nb + 63) / 64 * 64 + 8) * 4; }
 };
 
@@ -482,10 +483,11 @@ struct SelectCfg {
 //
 // Scores: q = q_h + q_l, m = m_h + m_l in bf16, score ~ q_h m_h + q_h m_l + q_l m_h, fp32
 // accumulators.  What is left out and rounded is at most 3 * 2^-16 sum|q||m|, the sum of 3 D
-// products in fp32 at most (3 D + 3) 2^-23 of the same: below 2^-13 |q| max_j |m_j| (Euclidean
-// norms).  The heads' sum q itself is rounded, by at most G 2^-24 sum_g |q_g|, which their
-// cancelling may make large against q.  Together the error is below
-//     eps = 2^-13 (|q| + G 2^-11 |sum_g |q_g||) max_j |m_j|.
+// products in fp32 at most (3 D + 3) 2^-23 of the same, and that at most |q| max_j |m_j|
+// (Euclidean norms).  The heads' sum q itself is rounded, by at most G 2^-24 sum_g |q_g|, which
+// their cancelling may make large against q.  Together, with u = 3 * 2^-16 + (3 D + 3) 2^-23
+// and a thousandth for the norms' own rounding, the error is below
+//     eps = 1.001 u (|q| + G 2^-24 / u |sum_g |q_g||) max_j |m_j|.
 // An eps that is not finite (an infinity or NaN among the operands) leaves everything to fp64.
 //
 // NL: 32-block words that a lane's share of a row has room for.
@@ -509,6 +511,19 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
   const int most = visible_blocks(p, b, last);  // of the CTA's queries (they see ever more)
   if (tid == 0) mnorm_bits = todo_n = 0;
   if (tid < QT) nv[tid] = visible_blocks(p, b, i0 + tid);
+
+  // ---- means: 64 are on their way while the last 64 (first, the queries) are worked on
+  const float* means = p.means + (long long)bh * p.nb * D;
+  unsigned char* const mstage = select_smem + C::kQ;
+  float4 next[D / 32];
+  const int mrow = tid >> 3, part = tid & 7;
+  auto fetch = [&](int j0) {
+    const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + mrow) * D) + part;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      next[x] = j0 + mrow < most ? src[8 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(0);
 
   // ---- the group's queries, summed, split and staged
   constexpr int CH = D / 8;  // 16-byte pieces of a row, in consecutive lanes
@@ -547,21 +562,10 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
       n2 += __shfl_xor_sync(0xffffffffu, n2, o);
       a2 += __shfl_xor_sync(0xffffffffu, a2, o);
     }
-    if (c == 0) qnorm[row] = sqrtf(n2) + 0x1p-11f * p.G * sqrtf(a2);
+    if (c == 0) qnorm[row] = sqrtf(n2) + 0x1p-24f / C::kError * p.G * sqrtf(a2);
   }
 
-  // ---- scores; the next 64 means are on their way while these are multiplied
-  const float* means = p.means + (long long)bh * p.nb * D;
-  unsigned char* const mstage = select_smem + C::kQ;
-  float4 next[D / 32];
-  const int mrow = tid >> 3, part = tid & 7;
-  auto fetch = [&](int j0) {
-    const float4* src = reinterpret_cast<const float4*>(means + (long long)(j0 + mrow) * D) + part;
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x)
-      next[x] = j0 + mrow < most ? src[8 * x] : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  fetch(0);
+  // ---- scores
   for (int j0 = 0; j0 < most; j0 += 64) {
     __syncthreads();
     {
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
     __syncthreads();
     if (j0 + 64 < most) fetch(j0 + 64);
     if (rg < C::RG) {
-      float acc[4] = {};
+      float acc[3][4] = {};  // high x high, high x low, low x high: three chains of products
       // queries: rows 0-7, rows 8-15, rows 0-7 of the next 8 columns, rows 8-15
       const uint32_t qat = stage + (uint32_t)(rg * 16 + (lane & 15)) * C::kLd + (lane >> 4) * 16;
       // means: high k 0-7, high k 8-15, low k 0-7, low k 8-15
@@ -598,16 +602,18 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
         ldmatrix_x4(qat + kk * 32, qh);
         ldmatrix_x4(qat + C::kRows * C::kLd + kk * 32, ql);
         ldmatrix_x4(mat + kk * 32, m);
-        mma_bf16(acc, qh, m[0], m[1]);
-        mma_bf16(acc, qh, m[2], m[3]);
-        mma_bf16(acc, ql, m[0], m[1]);
+        mma_bf16(acc[0], qh, m[0], m[1]);
+        mma_bf16(acc[1], qh, m[2], m[3]);
+        mma_bf16(acc[2], ql, m[0], m[1]);
       }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[0][x] += acc[1][x] + acc[2][x];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int row = rg * 16 + half * 8 + (lane >> 2);
         if (row < QT)
           *reinterpret_cast<float2*>(sc + row * ld + j0 + cg * 8 + (lane & 3) * 2) =
-              make_float2(acc[2 * half], acc[2 * half + 1]);
+              make_float2(acc[0][2 * half], acc[0][2 * half + 1]);
       }
     }
   }
@@ -624,8 +630,8 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
     int need = 0;
     if (k.nvis > p.topk && k.r > 0) {
       const float most_score = qnorm[rr] * mnorm;
-      need = pick_approx<NL>(k, sc + rr * ld, most_score, 2.f * (0x1p-13f * most_score + 1e-35f),
-                             guess, lane);
+      need = pick_approx<NL>(k, sc + rr * ld, most_score,
+                             2.f * (C::kError * most_score + 1e-35f), guess, lane);
     }
     if (need > 0) {
 #pragma unroll

@@ -595,7 +595,9 @@ __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParam
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int C = (int)max((long long)kMinStretch, (total + kStretches - 1) / kStretches);
   // bucket 0 holds whole stretches, bucket 63 the shortest rests
-  auto rest_bucket = [&](int rest) { return kBuckets - 1 - (int)((long long)rest * (kBuckets - 1) / C); };
+  auto rest_bucket = [&](int rest) {
+    return kBuckets - 1 - (int)((float)rest / (float)C * (kBuckets - 1));
+  };
   for (long long x = tid; x < p.units; x += 1024) {
     const int n = (count(x) + p.T - 1) / p.T;
     if (n / C > 0) atomicAdd(&bucket[0], n / C);
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParam
       SparseItem w;
       w.unit = (int)x;
       w.off = at[1], w.tokens = tokens;
-      w.bh = (int)(x / p.nu);
+      w.bh = (int)x / p.nu;
       w.b = w.bh / p.Hkv;
       // places within a bucket go by whoever asks first: they decide only who computes an item
       int place = full > 0 ? atomicAdd(&bucket[0], full) : 0;
