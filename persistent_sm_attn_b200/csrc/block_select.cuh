@@ -121,18 +121,36 @@ struct Picks {
 #pragma unroll
     for (int w = 0; w < W; ++w) take[w] = open[w] = 0u;
   }
+  // Every visible block, or the first `sink` and the last `local` of them, is taken.
+  __device__ __forceinline__ void take_all(int lane) { take_where(lane, nvis, nvis); }
+  __device__ __forceinline__ void take_forced(int lane) { take_where(lane, j0, j1); }
+  __device__ __forceinline__ void take_where(int lane, int below, int from) {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      // bits x of word w with 32 (32 w + x) + lane < n
+      auto bits = [&](int n) {
+        const int k = (n - lane + 31) / 32 - 32 * w;
+        return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+      };
+      const uint32_t seen = bits(nvis);
+      take[w] |= seen & (bits(max(below, 0)) | ~bits(max(from, 0)));
+    }
+  }
 };
 
 // Picks by approximate scores `row` that are off by at most eps2 / 2 and within +-most_score.
 // A cut with exactly r scores above it is found by counting; where the lowest score above and
 // the highest below are more than eps2 apart, the picks are those of the exact scores.
 // Otherwise the scores within eps2 of the cut stay open; returned is how many of them to take.
-// guess: in, where the first counts are taken; out, the cut (both of most_score).
+// guess: in, where the first counts are taken; out, the cut (both of most_score).  Without one
+// (0) they are taken where the cut of normally distributed scores of deviation spread most_score
+// would be (Abramowitz and Stegun 26.2.22).  Both only decide how many counts it takes.
 template <int NL>
 __device__ __forceinline__ int pick_approx(Picks<NL>& k, const float* row, float most_score,
-                                           float eps2, float& guess, int lane) {
+                                           float eps2, float& guess, float spread, int lane) {
   constexpr int W = Picks<NL>::W;
   const int j0 = k.j0, j1 = k.j1, nl = k.nl, r = k.r;
+  k.take_forced(lane);
   if (!(eps2 < 1e30f)) {  // a partial sum might have overflowed, or an operand is not finite
     for (int x = 0; x < nl; ++x) {
       const int j = 32 * x + lane;
@@ -171,23 +189,28 @@ __device__ __forceinline__ int pick_approx(Picks<NL>& k, const float* row, float
   // the range falls to a quarter (a third) with each count: up to 512 blocks leave
   // room for three counts in a word
   constexpr int kBits = kHeld ? 10 : 16;
-  // and the first counts are taken around where the last query's cut was
+  if (guess == 0.f) {
+    const float t = sqrtf(1.3862944f * __log2f((float)(j1 - j0) / (float)r));  // sqrt(-2 ln p)
+    guess = spread * (t - (2.30753f + 0.27061f * t) / (1.f + t * (0.99229f + 0.04481f * t)));
+  }
   float near = guess * most_score;
   while (!found && hi - lo > eps2) {
-    float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
+    const float d = kHeld ? 0.25f * hi - 0.25f * lo : (hi - lo) * (1.f / 3.f);
     float m1 = lo + d, m2 = kHeld ? 0.5f * lo + 0.5f * hi : hi - d, m3 = hi - d;
-    if (near != 0.f) {
-      d = 0.1f * fabsf(near);
-      m1 = near - d, m2 = kHeld ? near : near + d, m3 = near + d;
-      near = 0.f;
-    }
+    const float off = 0.2f * fabsf(near);
+    if (off > 0.f && near - off > lo && near + off < hi)
+      m1 = near - off, m2 = kHeld ? near : near + off, m3 = near + off;
+    near = 0.f;
     if (!(m1 > lo && m2 > lo && m1 < hi && m2 < hi)) break;
-    unsigned c = 0;
+    // a score above m makes m - score negative: its sign bit is added
+    unsigned n1 = 0, n2 = 0, n3 = 0;
     each([&](int, float v) {
-      c += (v > m1 ? 1u : 0u) + (v > m2 ? 1u << kBits : 0u);
-      if constexpr (kHeld) c += v > m3 ? 1u << (2 * kBits) : 0u;
+      n1 += __float_as_uint(m1 - v) >> 31;
+      n2 += __float_as_uint(m2 - v) >> 31;
+      if constexpr (kHeld) n3 += __float_as_uint(m3 - v) >> 31;
     });
-    c = __reduce_add_sync(0xffffffffu, c);
+    const unsigned c =
+        __reduce_add_sync(0xffffffffu, n1 + (n2 << kBits) + (kHeld ? n3 << (2 * kBits % 32) : 0u));
     const int c1 = (int)(c & ((1u << kBits) - 1)), c2 = (int)((c >> kBits) & ((1u << kBits) - 1));
     int c3 = 0;
     if constexpr (kHeld) c3 = (int)(c >> (2 * kBits));
@@ -202,24 +225,31 @@ __device__ __forceinline__ int pick_approx(Picks<NL>& k, const float* row, float
   }
   if (found && most_score > 1e-20f) guess = cut / most_score;
   float a = lo, z = hi;
+  uint32_t above[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) above[w] = 0u;
   if (found) {  // lowest above the cut, highest below
     int ka = 0x7f800000, kz = (int)0x807fffff;  // as integers that order like the floats
-    each([&](int, float v) {
-      const int k = ordered_int(v);
-      if (v > cut) ka = min(ka, k);
-      else kz = max(kz, k);
+    each([&](int x, float v) {
+      const int o = ordered_int(v);
+      if (v > cut) ka = min(ka, o), above[W == 1 ? 0 : x >> 5] |= 1u << (x & 31);
+      else kz = max(kz, o);
     });
     a = __int_as_float(ordered_int_inverse(__reduce_min_sync(0xffffffffu, ka)));
     z = __int_as_float(ordered_int_inverse(__reduce_max_sync(0xffffffffu, kz)));
+    if (a - z > eps2) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) k.take[w] |= above[w];
+      return 0;
+    }
   }
-  const bool clear = found && a - z > eps2;
-  const float in_at = clear ? cut : z + eps2, open_at = clear ? INFINITY : a - eps2;
+  const float in_at = z + eps2, open_at = a - eps2;
   int in = 0;
   each([&](int x, float v) {
     if (v > in_at) k.take[W == 1 ? 0 : x >> 5] |= 1u << (x & 31), ++in;
     else if (v >= open_at) k.open[W == 1 ? 0 : x >> 5] |= 1u << (x & 31);
   });
-  return clear ? 0 : r - __reduce_add_sync(0xffffffffu, in);
+  return r - __reduce_add_sync(0xffffffffu, in);
 }
 
 // Decides the open blocks, `need` of which are to be taken, by their fp64 scores.  key: a word
@@ -341,16 +371,14 @@ __device__ __forceinline__ void pick_exact(Picks<NL>& k, int need, const SelectP
 template <int NL>
 __device__ __forceinline__ void put_out(const Picks<NL>& k, int topk, int* out, int lane) {
   constexpr int W = Picks<NL>::W;
-  const bool all = k.nvis <= topk;
+  const unsigned below = (1u << lane) - 1u;
   int done = 0;
 #pragma unroll (NL <= 16 ? NL : 4)
   for (int x = 0; x < NL; ++x) {
     if (x >= k.nl) break;
-    const int j = 32 * x + lane;
-    const bool on =
-        j < k.nvis && (all || j < k.j0 || j >= k.j1 || ((k.take[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u));
+    const bool on = (k.take[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u;
     const unsigned m = __ballot_sync(0xffffffffu, on);
-    if (on) out[done + __popc(m & ((1u << lane) - 1u))] = j;
+    if (on) out[done + __popc(m & below)] = 32 * x + lane;
     done += __popc(m);
   }
   for (int x = done + lane; x < topk; x += 32) out[x] = -1;
@@ -441,10 +469,15 @@ __global__ void __launch_bounds__(256) dash_block_select_token_kernel(const Sele
     const float qn = sqrtf(n2), most = (qn + 0x1p-10f * sqrtf(a2)) * mnorm;
     const float eps2 = 2.f * ((0x1p-20f * qn + 0x1p-24f * p.G * sqrtf(a2)) * mnorm + 1e-35f);
     float guess = 0.f;
-    const int need = pick_approx<NL>(k, sc, most, eps2, guess, lane);
+    const int need = pick_approx<NL>(k, sc, most, eps2, guess, qn / (most + 1e-30f) *
+                                     __int_as_float(top_bits) * 0.25f, lane);
     __syncwarp();
     if (need > 0)
       pick_exact<D, NL>(k, need, p, b, hk, i, means, reinterpret_cast<uint32_t*>(sc), lane);
+  } else if (nvis > p.topk) {
+    k.take_forced(lane);
+  } else {
+    k.take_all(lane);
   }
   put_out(k, p.topk, p.idx + ((long long)bh * p.Sq + i) * p.topk, lane);
 }
@@ -631,7 +664,12 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
     if (k.nvis > p.topk && k.r > 0) {
       const float most_score = qnorm[rr] * mnorm;
       need = pick_approx<NL>(k, sc + rr * ld, most_score,
-                             2.f * (C::kError * most_score + 1e-35f), guess, lane);
+                             2.f * (C::kError * most_score + 1e-35f), guess, rsqrtf((float)D),
+                             lane);
+    } else if (k.nvis > p.topk) {
+      k.take_forced(lane);
+    } else {
+      k.take_all(lane);
     }
     if (need > 0) {
 #pragma unroll
