@@ -8,8 +8,7 @@
 // a step, max|x| 2^-7 (one step, where an element above 127 steps is clamped to 127).  A
 // group that holds an infinity or a NaN gets e = -128 and reads back as NaN.
 #pragma once
-#include <cuda_bf16.h>
-#include <cstdint>
+#include "ptx.cuh"
 
 namespace dash {
 
@@ -41,35 +40,50 @@ __device__ __forceinline__ uint32_t ckpt_scale(uint32_t x, uint32_t s) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// A thread takes pieces of 8 consecutive elements, four threads a group, several pieces in
-// flight: neighbouring threads read neighbouring pieces.  Bound by HBM: 2 bytes read and 33/32
-// written an element.
-//
-// Packing, a warp takes 64 pieces, a thread pieces `lane` and `32 + lane`; lane pairs swap, so
-// that the even lane stores 16 bytes of the first half and the odd lane of the second.  (Stores
-// of 8 bytes: 4.1 TB/s; 16 elements a thread, its two loads beside each other: 5.1.)
+// Pieces of 8 consecutive elements, four to a group; a warp takes 64 at a time, a thread pieces
+// `lane` and `32 + lane`, so that neighbouring threads read and write neighbouring pieces.
+// Where piece `x` of a round that starts at piece `c` lies: its tensor and first element there.
+struct CkptPlace {
+  int t;
+  long long at;
+};
+__device__ __forceinline__ CkptPlace ckpt_place(const CkptParams& p, long long c, int x, int lane) {
+  int t = ckpt_tensor(p, c >> 2);  // c is the same in the whole warp
+  const long long end = p.groups[t + 1] * 4;
+  if (c + 64 <= end) return {t, (c - p.groups[t] * 4) * 8 + x * 256 + lane * 8};
+  // the round reaches into the next tensor or past the last piece
+  const long long i = min(c + 32 * x + lane, p.groups[p.n] * 4 - 4 + (lane & 3));
+  t = ckpt_tensor(p, i >> 2);
+  return {t, (i - p.groups[t] * 4) * 8};
+}
+constexpr int kCkptAhead = 2;  // rounds of 64 pieces a warp has in flight
+
+// Lane pairs swap, so that the even lane stores 16 bytes of the round's first half and the odd
+// lane of its second.  Bound by HBM: 2 bytes read and 33/32 written an element, 268 million in
+// 167 us, 4.9 TB/s.  (Stores of 8 bytes and fp32 arithmetic: 4.1.  Twice the loads in flight,
+// fewer or more CTAs, no exponents stored: no faster.)
 __global__ void __launch_bounds__(256) dash_ckpt8_pack_kernel(const __grid_constant__ CkptParams p) {
   const long long pieces = p.groups[p.n] * 4, stride = (long long)gridDim.x * 8 * 64;
   const int lane = threadIdx.x & 31;
-  constexpr int kAhead = 2;  // rounds of 64 pieces in flight
-  for (long long c0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 64; c0 < pieces;
-       c0 += stride * kAhead) {
-    uint4 w[kAhead][2];
-    long long at[kAhead][2];
-    int tensor[kAhead][2];
+  const bool odd = lane & 1;
+  for (long long c0 = ((long long)blockIdx.x * 8 + dev::warp_uniform()) * 64; c0 < pieces;
+       c0 += stride * kCkptAhead) {
+    uint4 w[kCkptAhead][2];
+    CkptPlace at[kCkptAhead][2];
 #pragma unroll
-    for (int y = 0; y < kAhead; ++y)
+    for (int y = 0; y < kCkptAhead; ++y) {
+      const long long c = min(c0 + y * stride, pieces - 1);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const long long i = min(c0 + y * stride + 32 * x + lane, pieces - 4 + (lane & 3)), g = i >> 2;
-        const int t = ckpt_tensor(p, g);
-        tensor[y][x] = t;
-        at[y][x] = (g - p.groups[t]) * 32 + (i & 3) * 8;
-        w[y][x] = __ldcs(
-            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.src[t]) + at[y][x]));
+        at[y][x] = ckpt_place(p, c, x, lane);
+        w[y][x] = __ldcs(reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.src[at[y][x].t]) + at[y][x].at));
       }
+    }
 #pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
+    for (int y = 0; y < kCkptAhead; ++y) {
+      const long long c = c0 + y * stride;
+      if (c >= pieces) break;
       uint2 pk[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -103,59 +117,63 @@ __global__ void __launch_bounds__(256) dash_ckpt8_pack_kernel(const __grid_const
           q[h] = bad ? 0u : bytes;
         }
         pk[x] = make_uint2(q[0], q[1]);
-        if ((lane & 3) == 0 && c0 + y * stride + 32 * x + lane < pieces)
-          p.exps[tensor[y][x]][at[y][x] >> 5] = (int8_t)(bad ? kCkptBad : e);
+        if ((lane & 3) == 0 && c + 32 * x + lane < pieces)
+          p.exps[at[y][x].t][at[y][x].at >> 5] = (int8_t)(bad ? kCkptBad : e);
       }
-      const bool odd = lane & 1;
       const uint2 give = odd ? pk[0] : pk[1], keep = odd ? pk[1] : pk[0];
       const uint2 got = make_uint2(__shfl_xor_sync(0xffffffffu, give.x, 1),
                                    __shfl_xor_sync(0xffffffffu, give.y, 1));
-      const long long i = c0 + y * stride + (odd ? 31 + lane : lane);  // the pair's first piece
-      const int t = odd ? tensor[y][1] : tensor[y][0];
-      int8_t* dst = static_cast<int8_t*>(p.dst[t]) + (odd ? at[y][1] - 8 : at[y][0]);
-      if (i < pieces)
+      const int t = odd ? at[y][1].t : at[y][0].t;
+      int8_t* dst = static_cast<int8_t*>(p.dst[t]) + (odd ? at[y][1].at - 8 : at[y][0].at);
+      if (c + (odd ? 31 + lane : lane) < pieces)  // the pair's first piece
         *reinterpret_cast<uint4*>(dst) = odd ? make_uint4(got.x, got.y, keep.x, keep.y)
                                              : make_uint4(keep.x, keep.y, got.x, got.y);
     }
   }
 }
 
-// (One piece of a thread in flight: 5.4 TB/s; four: 5.9.)
-constexpr int kCkptAhead = 4;
+// Bound by HBM: 268 million elements in 135 us, 6.0 TB/s.
 __global__ void __launch_bounds__(256) dash_ckpt8_unpack_kernel(const __grid_constant__ CkptParams p) {
-  const long long pieces = p.groups[p.n] * 4;
-  const long long stride = (long long)gridDim.x * blockDim.x;
-  for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < pieces;
-       i0 += stride * kCkptAhead) {
-    uint2 w[kCkptAhead];
-    int e[kCkptAhead], tensor[kCkptAhead];
-    long long at[kCkptAhead];
+  const long long pieces = p.groups[p.n] * 4, stride = (long long)gridDim.x * 8 * 64;
+  const int lane = threadIdx.x & 31;
+  for (long long c0 = ((long long)blockIdx.x * 8 + dev::warp_uniform()) * 64; c0 < pieces;
+       c0 += stride * kCkptAhead) {
+    uint2 w[kCkptAhead][2];
+    int e[kCkptAhead][2];
+    CkptPlace at[kCkptAhead][2];
 #pragma unroll
     for (int y = 0; y < kCkptAhead; ++y) {
-      const long long i = min(i0 + y * stride, pieces - 1), g = i >> 2;
-      const int t = ckpt_tensor(p, g);
-      tensor[y] = t;
-      at[y] = (g - p.groups[t]) * 32 + (i & 3) * 8;
-      w[y] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.src[t]) + at[y]));
-      e[y] = p.exps[t][at[y] >> 5];
+      const long long c = min(c0 + y * stride, pieces - 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        at[y][x] = ckpt_place(p, c, x, lane);
+        w[y][x] = __ldcs(reinterpret_cast<const uint2*>(
+            static_cast<const int8_t*>(p.src[at[y][x].t]) + at[y][x].at));
+        e[y][x] = p.exps[at[y][x].t][at[y][x].at >> 5];
+      }
     }
 #pragma unroll
     for (int y = 0; y < kCkptAhead; ++y) {
-      if (i0 + y * stride >= pieces) break;
-      // a foreign exponent below the stored range reads as the smallest one
-      const float f = e[y] == kCkptBad ? __int_as_float(0x7fc00000) : exp2_int(max(e[y], -126));
-      uint32_t out[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t word = k < 2 ? w[y].x : w[y].y;
-        const float lo = (float)(int8_t)(word >> (16 * (k & 1))) * f;
-        const float hi = (float)(int8_t)(word >> (16 * (k & 1) + 8)) * f;
-        // exact: at most 7 significant bits
-        __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-        out[k] = *reinterpret_cast<uint32_t*>(&b);
+      for (int x = 0; x < 2; ++x) {
+        if (c0 + y * stride + 32 * x + lane >= pieces) continue;
+        // a foreign exponent below the stored range reads as the smallest one
+        const float f = e[y][x] == kCkptBad ? __int_as_float(0x7fc00000) : exp2_int(max(e[y][x], -126));
+        // a byte b + 128 as the low mantissa bits of 2^23: minus 2^23 + 128 it is b exactly
+        const uint32_t words[2] = {w[y][x].x ^ 0x80808080u, w[y][x].y ^ 0x80808080u};
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t word = words[k >> 1];
+          float lo = __uint_as_float(__byte_perm(word, 0x4b000000u, 0x7540 + 2 * (k & 1)));
+          float hi = __uint_as_float(__byte_perm(word, 0x4b000000u, 0x7541 + 2 * (k & 1)));
+          lo = (lo - 8388736.f) * f;
+          hi = (hi - 8388736.f) * f;
+          out[k] = dev::pack_bf16x2(lo, hi);  // exact: at most 7 significant bits
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dst[at[y][x].t]) + at[y][x].at) =
+            make_uint4(out[0], out[1], out[2], out[3]);
       }
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dst[tensor[y]]) + at[y]) =
-          make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }

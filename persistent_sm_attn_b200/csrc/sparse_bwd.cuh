@@ -6,8 +6,7 @@
 //
 // Two passes recompute S and dP, each with its result resident in TMEM, so that every sum
 // has one owner and a fixed order and no partial of dQ goes through memory:
-//   dash_sparse_dq_kernel   a CTA per query tile walks the tile's listed units (as the
-//                           forward does) and also writes delta;
+//   dash_sparse_dq_kernel   walks the listed units of a query tile, as the forward does;
 //   dash_sparse_dkdv_kernel a persistent CTA per SM takes items: a unit of 64 keys and a
 //                           stretch of the tokens that picked it.
 // A unit that many tokens picked (the first block of a causal sequence) is cut into stretches;
@@ -22,7 +21,8 @@ namespace dash {
 
 // ------------------------------------------------------------------ delta
 // delta = rowsum(dO o O) of every row, D / 8 lanes a row, four rows in flight a lane.  Bound
-// by reading O and dO.
+// by reading O and dO: 67 MB in 13.6 us.  (Taken by two warps of the dQ kernel a tile ahead it
+// kept the softmax waiting, 276 us for 232 + 13.)
 struct SparseDeltaParams {
   const __nv_bfloat16 *o, *dout;
   long long ob, oh, os;  // strides of dout in elements
@@ -104,6 +104,10 @@ struct SparseDqCfg {
 // the same pair: 231 and 408, exponentials and the rest took turns.)  Row t G + g of a tile is
 // token t, head g, so a warp holds few tokens and skips the exponentials of units that none
 // of them picked.
+//
+// Measured: 214 us and 329 us in these two cases, 1400 and 1100 cycles a unit where the products
+// alone take 1160 and 730 (a 128 x 64 x 16 product 48, which is what reading its operands from
+// shared memory takes, a commit 35); the busiest CTA has 11 % more units than the mean.
 //
 // kLow: dS enters its product as the sum of two bf16 values instead of one, whose rounding of
 // up to 2^-8 is otherwise the larger part of the result's error; see sparse_low_part.
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(384, 1)
 
 // ------------------------------------------------------------------ who reads a unit
 // For every unit the tokens that picked it and see it, ascending: counted, given a place by
-// prefix sums, written.
+// prefix sums, written.  8 and 9 us for 35 thousand (tile, unit) pairs.
 struct InverseParams {
   PlanView plan;
   int* count;  // [units] tokens of the unit
@@ -570,7 +574,7 @@ struct ItemParams {
   long long units;
 };
 // One CTA: sums, a histogram of the stretches' lengths, then exclusive prefix sums of the
-// tokens and partial slots per unit.
+// tokens and partial slots per unit.  8 us for 512 units, 15 for 2048.
 __global__ void __launch_bounds__(1024) dash_sparse_items_kernel(const ItemParams p) {
   constexpr int kHeld = 8192, kBuckets = 64;
   __shared__ int held[kHeld];  // the first units' counts
@@ -712,9 +716,15 @@ struct SparseDkvCfg {
 // would halve the rate).  At D = 64 the stacked operand [dO | Q] serves both: dV^T is the
 // upper half of one product, dK^T the lower of the other.  S and dP of the next tile, K and V
 // and the accumulators of the next item have buffers of their own, so that the products of
-// one tile run under the exponentials of the other, also from item to item.  The two softmax
-// warpgroups take 32 keys of every row each.  kLow (D = 64, where shared memory has room): as
-// in the dQ kernel.
+// one tile run under the exponentials of the other, also from item to item.  D = 128: the two
+// softmax warpgroups take 32 keys of every row each, and the dV product is issued before dS
+// is computed.  D = 64: they take tiles in turn.  kLow (D = 64, where shared memory has room):
+// as in the dQ kernel.
+//
+// Measured: 16 heads of 8k, 4 K/V heads, D = 128, 16 picks of 64: 181 us, 3000 cycles a tile;
+// 8 heads of 16k, D = 64, 8 picks of 128: 147 us, 2400.  The products take 2000 and 1280.  At
+// D = 128 two stages are all that fits, and a stage's way from load to last product bounds it.
+// Tiles of neighbouring tokens: 544 and 1159 us; dV and dK issued together: 201 and 170.
 template <int D, bool kLow>
 __global__ void __launch_bounds__(640, 1)
     dash_sparse_dkdv_kernel(const __grid_constant__ CUtensorMap tmK,

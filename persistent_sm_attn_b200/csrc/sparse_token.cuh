@@ -10,6 +10,10 @@
 // the cluster through each other's: O = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w, in the
 // order of w.  Bound by reading the picked K and V once: the products (mma.sync, 16 rows) run
 // under the loads, three chunks of which each warp keeps in flight (16-byte cp.async).
+//
+// Measured, 16 picks of 64 keys, 32 heads, 8 K/V heads, D = 128: one token 8.7 us (latency: the
+// picks, the keys, the joins), 64 tokens 53 us, 268 MB at 5.1 TB/s.  Two stages took 65, four
+// (one CTA an SM) 75.
 #pragma once
 #include "block_select.cuh"
 
