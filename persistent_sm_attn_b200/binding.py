@@ -590,6 +590,8 @@ def _expect_rows(name, t, B, device):
 def _like(t, dtype=None):
     """An uninitialised contiguous tensor of t's shape and device."""
     import torch
+    if t.is_contiguous():
+        return torch.empty_like(t, dtype=dtype)
     return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
@@ -697,14 +699,23 @@ def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start
 
 
 def _expect_qkv(q, k, v):
+    """B, H, Hkv, Sq, Sk, D and the strides argument of q, k, v."""
     import torch
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,H,Sq,D] and k [B,Hkv,Sk,D]")
     B, H, Sq, D = q.shape
-    _expect("q", q, q.shape, torch.bfloat16, contiguous=False)
-    _expect("k", k, (B, k.shape[1], k.shape[2], D), torch.bfloat16, q.device, contiguous=False)
-    _expect("v", v, k.shape, torch.bfloat16, q.device, contiguous=False)
-    return B, H, k.shape[1], Sq, k.shape[2], D
+    Bk, Hkv, Sk, Dk = k.shape
+    bf, device = torch.bfloat16, q.device
+    # the usual case at once: what is wrong is looked for only where something is
+    if (Bk == B and Dk == D and v.shape == k.shape and q.dtype is bf and k.dtype is bf
+            and v.dtype is bf and q.is_cuda and k.device == device and v.device == device
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and not (q.data_ptr() | k.data_ptr() | v.data_ptr()) & 15):
+        return B, H, Hkv, Sq, Sk, D, None
+    _expect("q", q, q.shape, bf, contiguous=False)
+    _expect("k", k, (B, Hkv, Sk, D), bf, device, contiguous=False)
+    _expect("v", v, k.shape, bf, device, contiguous=False)
+    return B, H, Hkv, Sq, Sk, D, _strides(q, k, v)
 
 
 def _expect_plan(plan, shape, device):
@@ -730,7 +741,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
     nothing gets O = 0 and LSE = -inf.  Give the `plan` of idx where the backward follows;
     idx, block, causal, kv_len and q_start are then those it was made with."""
     import torch
-    B, H, Hkv, Sq, Sk, D = _expect_qkv(q, k, v)
+    B, H, Hkv, Sq, Sk, D, strides = _expect_qkv(q, k, v)
     if out is not None:
         _expect("out", out, (B, H, Sq, D), torch.bfloat16, q.device)
     if lse is not None:
@@ -739,16 +750,19 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
         _expect("idx", idx, (B, Hkv, Sq, idx.shape[-1]), torch.int32, q.device)
         topk, blocks = idx.shape[-1], _block_count(Sk, block)
         if _few_queries(B, H, Hkv, Sq) and topk <= 1024 and blocks <= 65536:
-            n = _expect_rows("kv_len", kv_len, B, q.device)
-            s = _expect_rows("q_start", q_start, B, q.device)
+            n = s = None
+            if kv_len is not None:
+                n = _expect_rows("kv_len", kv_len, B, q.device)
+            if q_start is not None:
+                s = _expect_rows("q_start", q_start, B, q.device)
             with _Launch(q.device, stream) as st:
                 if out is None:
                     out = _like(q)
                 if lse is None:
                     lse = q.new_empty((B, H, Sq), dtype=torch.float32)
                 _check(load().dash_attn_sparse_tokens(
-                    q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides(q, k, v), idx.data_ptr(), n,
-                    s, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
+                    q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, idx.data_ptr(), n, s,
+                    out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
                     int(bool(causal)), float(scale or 0.0), st), "dash_attn_sparse_fwd")
             return out, lse
         plan = dash_sparse_plan(idx, H, Sk, block, causal, kv_len, q_start, stream)
@@ -763,7 +777,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
             lse = q.new_empty((B, H, Sq), dtype=torch.float32)
         work = q.new_empty((size,), dtype=torch.uint8) if size else None
         _check(lib.dash_attn_sparse_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                        _strides(q, k, v), plan.on(st), out.data_ptr(),
+                                        strides, plan.on(st), out.data_ptr(),
                                         lse.data_ptr(), work.data_ptr() if size else None,
                                         *plan.shape[:5], D, *plan.shape[5:], int(plan.causal),
                                         float(scale or 0.0), st), "dash_attn_sparse_fwd")
@@ -775,7 +789,7 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
     """dQ [B,H,Sq,D], dK and dV [B,Hkv,Sk,D] of dash_attn_sparse_fwd with the same plan, from
     its O and LSE; bitwise reproducible."""
     import torch
-    B, H, Hkv, Sq, Sk, D = _expect_qkv(q, k, v)
+    B, H, Hkv, Sq, Sk, D, _ = _expect_qkv(q, k, v)
     _expect("o", o, q.shape, torch.bfloat16, q.device)
     _expect("do", do, q.shape, torch.bfloat16, q.device, contiguous=False)
     _expect("lse", lse, (B, H, Sq), torch.float32, q.device)
