@@ -448,3 +448,41 @@ def test_gradients_against_differences():
         got = (grads[i].double() * d).sum()
         bound = ((bounds[i] + extra[i]) * d.abs()).sum()
         assert (got - diff).abs() <= bound + 1e-6 * diff.abs() + 1e-6
+
+
+FIRST_USE = """
+import torch
+from persistent_sm_attn_b200 import binding as dash
+g = torch.Generator(device="cuda").manual_seed(1)
+mk = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+q, k, v, do = mk(1, 4, 300, 64), mk(1, 2, 300, 64), mk(1, 2, 300, 64), mk(1, 4, 300, 64)
+torch.cuda.synchronize()
+
+def step():
+    means = dash.dash_block_means(k, 64)
+    idx = dash.dash_block_select(q, means, 300, 64, 3)
+    plan = dash.dash_sparse_plan(idx, 4, 300, 64)
+    o, lse = dash.dash_attn_sparse_fwd(q, k, v, idx, 64, plan=plan)
+    packed = dash.dash_ckpt8_pack(q, k, v, o)
+    grads = dash.dash_attn_sparse_bwd_ckpt8(*packed, do, lse, plan)
+    one = q[:, :, -1:].contiguous()
+    last = dash.dash_block_select(one, means, 300, 64, 3)
+    return (o, lse, *grads, *dash.dash_attn_sparse_fwd(one, k, v, last, 64))
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = step()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(held, step()):
+    assert torch.equal(a, b)
+assert dash.dash_attn_sync_status() == 0
+print("same")
+"""
+
+
+def test_the_first_use_may_be_captured():
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", FIRST_USE], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "same" in out.stdout, out.stderr[-2000:]
