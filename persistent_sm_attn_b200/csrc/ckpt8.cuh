@@ -31,15 +31,6 @@ __device__ __forceinline__ int ckpt_tensor(const CkptParams& p, long long g) {
 // 2^e as a float, -126 <= e <= 127
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
-// clamp(x s, -127, 127) of two bf16 values and two powers of two
-__device__ __forceinline__ uint32_t ckpt_scale(uint32_t x, uint32_t s) {
-  const __nv_bfloat162 a = *reinterpret_cast<__nv_bfloat162*>(&x);
-  const __nv_bfloat162 b = *reinterpret_cast<__nv_bfloat162*>(&s);
-  const __nv_bfloat162 top = __float2bfloat162_rn(127.f), low = __float2bfloat162_rn(-127.f);
-  const __nv_bfloat162 m = __hmax2(__hmin2(__hmul2(a, b), top), low);
-  return *reinterpret_cast<const uint32_t*>(&m);
-}
-
 // Pieces of 8 consecutive elements, four to a group; a warp takes 64 at a time, a thread pieces
 // `lane` and `32 + lane`, so that neighbouring threads read and write neighbouring pieces.
 // Where piece `x` of a round that starts at piece `c` lies: its tensor and first element there.
@@ -60,8 +51,9 @@ constexpr int kCkptAhead = 2;  // rounds of 64 pieces a warp has in flight
 
 // Lane pairs swap, so that the even lane stores 16 bytes of the round's first half and the odd
 // lane of its second.  Bound by HBM: 2 bytes read and 33/32 written an element, 268 million in
-// 167 us, 4.9 TB/s.  (Stores of 8 bytes and fp32 arithmetic: 4.1.  Twice the loads in flight,
-// fewer or more CTAs, no exponents stored: no faster.)
+// 158 us, 5.1 TB/s; the same loads and stores with next to no arithmetic take 136.  (Products and
+// clamps in bf16 pairs: 167 us.  Stores of 8 bytes and fp32 arithmetic: 198.  Twice the loads in
+// flight, fewer or more CTAs, no exponents stored: no faster.)
 __global__ void __launch_bounds__(256) dash_ckpt8_pack_kernel(const __grid_constant__ CkptParams p) {
   const long long pieces = p.groups[p.n] * 4, stride = (long long)gridDim.x * 8 * 64;
   const int lane = threadIdx.x & 31;
@@ -98,24 +90,27 @@ __global__ void __launch_bounds__(256) dash_ckpt8_pack_kernel(const __grid_const
         const bool bad = top >= 0x7f80u;
         // the biased exponent of a normal maximum is floor(log2) + 127; below that, clamped
         const int e = max((int)(top >> 7) - 127 - 6, -126);
-        // 2^-e, -121 <= -e <= 126, in bf16: x 2^-e is exact there (or rounds to 0 below), and
-        // clamping before the rounding gives what clamping after it would
-        const uint32_t inv = (uint32_t)(127 - e) << 7;
+        // x 2^-e + 1.5 2^10, exact in fp32 (below 2^-6 it rounds, but far from a half), as fp16,
+        // whose steps are 1 there: the rounding half to even, and the integer in the low byte
+        const float inv = exp2_int(-e);  // -122 <= -e <= 126
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float lo, hi;
+          dev::fma_f32x2(lo, hi, __uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u),
+                         inv, 1536.f);
+          const __half2 m = __floats2half2_rn(lo, hi);
+          r[k] = *reinterpret_cast<const uint32_t*>(&m);
+        }
+        // +-127.5 steps, the largest there is, rounds to 128: clamped where a group holds it
+        if (__any_sync(0xffffffffu, (top & 0x7fu) == 0x7fu)) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = __vmaxs2(__vmins2(r[k], 0x667f667fu), 0x65816581u);
+        }
         uint32_t q[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t m = ckpt_scale(u[2 * h + k], inv | inv << 16);
-            // the sum with 1.5 2^23 has the integer, rounded half to even, in its low byte
-            r[2 * k] = __float_as_uint(__uint_as_float(m << 16) + 12582912.f);
-            r[2 * k + 1] = __float_as_uint(__uint_as_float(m & 0xffff0000u) + 12582912.f);
-          }
-          const uint32_t bytes =
-              __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
-          q[h] = bad ? 0u : bytes;
-        }
+        for (int h = 0; h < 2; ++h)
+          q[h] = bad ? 0u : __byte_perm(r[2 * h], r[2 * h + 1], 0x6420);
         pk[x] = make_uint2(q[0], q[1]);
         if ((lane & 3) == 0 && c + 32 * x + lane < pieces)
           p.exps[at[y][x].t][at[y][x].at >> 5] = (int8_t)(bad ? kCkptBad : e);
