@@ -60,6 +60,27 @@ def test_empty_and_several_tensors():
     assert dash.dash_ckpt8_pack() == [] and dash.dash_ckpt8_unpack() == []
 
 
+def test_halves_and_clamps():
+    # groups with a maximum of 64 to 127.5 steps beside every half step below it, either sign
+    top = torch.arange(128, 256, device="cuda") / 2
+    half = torch.arange(128, device="cuda").view(1, -1) + 0.5
+    vals = torch.minimum(half.expand(128, 128), top.view(-1, 1))
+    g = torch.stack([top.view(-1, 1).expand(128, 128), vals, -vals, -top.view(-1, 1).expand(128, 128)], -1)
+    x = torch.zeros(128 * 128, 32, device="cuda")
+    x[:, [0, 13, 22, 31]] = g.reshape(-1, 4).float()
+    for e in (-126, -20, 0, 60):
+        check((x * 2.0 ** e).to(torch.bfloat16))
+
+
+def test_tensors_that_end_inside_a_chunk():
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    xs = [torch.randn(s, 32, generator=gen, device="cuda").to(torch.bfloat16)
+          for s in (129, 5, 515, 32, 64, 1, 31)]
+    for x, (m, e), y in zip(xs, pairs := dash.dash_ckpt8_pack(*xs), dash.dash_ckpt8_unpack(*pairs)):
+        assert torch.equal(m, R.ckpt_pack(x)[0]) and torch.equal(e, R.ckpt_pack(x)[1])
+        assert torch.equal(y.double(), R.ckpt_values(m, e))
+
+
 @pytest.mark.parametrize("H,Hkv,S,D,causal,schedule", [
     (2, 2, 256, 64, True, "sym_shift"), (2, 2, 256, 128, False, "shift"), (4, 1, 384, 64, False, "shift"),
     (2, 2, 256, 64, False, "shift_pairs")])
