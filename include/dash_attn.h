@@ -481,7 +481,7 @@ int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* d
  * backward is made for.  Conventions that differ from the calls above:
  *   - q, o, dout, dq: [B, H, Sq, D]; k, v, dk, dv: [B, Hkv, Sk, D], bf16, D in {64, 128},
  *     H any multiple of Hkv up to 128 query heads per K/V head.  Sq >= 0 and Sk >= 1 are
- *     free (no multiple of 128).  Query head h reads K/V head h / (H / Hkv).
+ *     free (no multiple of 128), Sk at most 2^30.  Query head h reads K/V head h / (H / Hkv).
  *   - Inputs may be strided: `strides` holds (batch, head, row) strides in elements for
  *     each strided input in the order of the arguments, positive multiples of 8 (the last
  *     dimension is contiguous; the stride of an extent of 1 is not looked at); NULL means
@@ -491,8 +491,8 @@ int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* d
  *     q_start: device int [B], the position of query 0 (NULL: Sk - Sq, the queries are the
  *     last Sq positions of Sk).  Query i sees keys j < limit_i = min(kv_len, q_start + i + 1)
  *     with causal = 1, j < kv_len with causal = 0.
- *   - block: keys per block, a positive multiple of 64.  Block numbers run from 0 to
- *     ceil(Sk / block) - 1.
+ *   - block: keys per block, a positive multiple of 64 up to 2^30.  Block numbers run from 0
+ *     to ceil(Sk / block) - 1.  topk: picks per query, 1 to 2^20.
  *   - Nothing is allocated and no answer is kept: plans and workspaces are the caller's,
  *     16-byte aligned, of the sizes the *_bytes calls give (a negative value is a negated
  *     status), and a workspace is free again when the call's work on `stream` is done.  All

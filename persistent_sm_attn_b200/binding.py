@@ -606,6 +606,8 @@ def _strides(*tensors):
 def _block_count(Sk, block):
     if block < 64 or block % 64:
         raise ValueError(f"block must be a positive multiple of 64, not {block}")
+    if block > 1 << 30 or Sk > 1 << 30:  # more would not pass the C entry points' int whole
+        raise ValueError(f"{Sk} keys in blocks of {block}: more than 2^30")
     return -(-Sk // block)
 
 
@@ -642,6 +644,9 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
         raise ValueError("q must be [B,H,Sq,D] and means [B,Hkv,nb,D]")
     B, H, Sq, D = q.shape
     Hkv = means.shape[1]
+    if not (0 < topk <= 1 << 20 and 0 <= sink <= topk and 0 <= local <= topk - sink):
+        raise ValueError(f"topk = {topk}, sink = {sink}, local = {local}: sink + local <= topk, "
+                         "1 <= topk <= 2^20 are needed")
     _expect("q", q, q.shape, torch.bfloat16, contiguous=False)
     _expect("means", means, (B, Hkv, _block_count(seq_k, block), D), torch.float32, q.device)
     n, s = _expect_rows("kv_len", kv_len, B, q.device), _expect_rows("q_start", q_start, B, q.device)
@@ -649,7 +654,7 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
         _expect("out", out, (B, Hkv, Sq, topk), torch.int32, q.device)
     with _Launch(q.device, stream) as st:
         if out is None:
-            out = q.new_empty((B, Hkv, Sq, max(int(topk), 0)), dtype=torch.int32)
+            out = q.new_empty((B, Hkv, Sq, topk), dtype=torch.int32)
         _check(load().dash_block_select(q.data_ptr(), _strides(q), means.data_ptr(), out.data_ptr(),
                                         n, s, B, H, Hkv, Sq, seq_k, D, block, topk,
                                         int(bool(causal)), sink, local, st), "dash_block_select")
@@ -689,6 +694,9 @@ def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start
     n = _expect_rows("kv_len", kv_len, B, idx.device)
     s = _expect_rows("q_start", q_start, B, idx.device)
     shape = (B, int(heads), Hkv, Sq, int(seq_k), int(block), topk)
+    _block_count(*shape[4:6])
+    if not 0 <= shape[1] < 1 << 31:
+        raise ValueError(f"heads must be a number of query heads, not {heads}")
     lib = load()
     size = _bytes(lib.dash_sparse_plan_bytes(*shape), "dash_sparse_plan")
     with _Launch(idx.device, stream) as st:

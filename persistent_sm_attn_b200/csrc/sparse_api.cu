@@ -66,22 +66,23 @@ int words_for(int dev, void* stream, bool create, unsigned** out) {
 }
 
 // Shared memory a kernel may use, raised once per kernel and device (the call costs a
-// microsecond).  `tag` is the kernel's own array.
+// microsecond) to the most that any launch of it takes: launches of two threads cannot lower
+// it for each other.  `done` is the kernel's own array.
 constexpr int kMaxDevices = 64;
 template <class K>
-int allow_smem(K* kern, int bytes, std::atomic<int> (&tag)[kMaxDevices]) {
+int allow_smem(K* kern, int most, std::atomic<bool> (&done)[kMaxDevices]) {
   int dev = 0;
   DASH_CUDA(cudaGetDevice(&dev));
-  if (dev >= kMaxDevices || tag[dev].load(std::memory_order_relaxed) < bytes) {
-    DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-    if (dev < kMaxDevices) tag[dev].store(bytes, std::memory_order_relaxed);
+  if (dev >= kMaxDevices || !done[dev].load(std::memory_order_acquire)) {
+    DASH_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    if (dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
   }
   return DASH_OK;
 }
-#define DASH_ALLOW_SMEM(kern, bytes)                      \
+#define DASH_ALLOW_SMEM(kern, most)                       \
   do {                                                    \
-    static std::atomic<int> allowed[kMaxDevices];         \
-    const int allow_rc = allow_smem(kern, bytes, allowed); \
+    static std::atomic<bool> allowed[kMaxDevices];        \
+    const int allow_rc = allow_smem(kern, most, allowed); \
     if (allow_rc) return allow_rc;                        \
   } while (0)
 
@@ -107,8 +108,16 @@ int take_strides(const long long* in, int B, int H, int S, int D, Strides* out) 
   return DASH_OK;
 }
 
+// What keeps ceil(Sk / block), the places of a tile's picks and the like within 32 bits
+constexpr int kMostKeys = 1 << 30, kMostPicks = 1 << 20;
+int check_block(int block, int topk) {
+  if (block < dash::kUnit || block % dash::kUnit != 0 || topk < 1) return DASH_ERR_INVALID_ARG;
+  return block > kMostKeys || topk > kMostPicks ? DASH_ERR_UNSUPPORTED : DASH_OK;
+}
+
 int check_heads(int B, int H, int Hkv, int Sq, int Sk) {
   if (B < 0 || H < 0 || Sq < 0 || Sk < 1) return DASH_ERR_INVALID_ARG;
+  if (Sk > kMostKeys) return DASH_ERR_UNSUPPORTED;
   if (B == 0 || H == 0) return DASH_OK;
   if (Hkv < 1 || H % Hkv != 0) return DASH_ERR_INVALID_ARG;
   if (H / Hkv > dash::kTileRows) return DASH_ERR_UNSUPPORTED;
@@ -123,8 +132,8 @@ int plan_shape(int B, int H, int Hkv, int Sq, int Sk, int block, int topk, int c
                PlanShape* s) {
   int rc = check_heads(B, H, Hkv, Sq, Sk);
   if (rc) return rc;
-  if (block < dash::kUnit || block % dash::kUnit != 0 || topk < 1 || (causal != 0 && causal != 1))
-    return DASH_ERR_INVALID_ARG;
+  if ((rc = check_block(block, topk))) return rc;
+  if (causal != 0 && causal != 1) return DASH_ERR_INVALID_ARG;
   *s = PlanShape{};
   s->B = B, s->H = H, s->Hkv = Hkv, s->Sq = Sq, s->Sk = Sk;
   s->block = block, s->topk = topk, s->causal = causal;
@@ -286,7 +295,7 @@ int launch_sparse_token(dash::SparseTokenParams& p, long long units, cudaStream_
   if (units * cs > 0x7fffffffLL) return DASH_ERR_UNSUPPORTED;
   auto kern = dash::dash_sparse_token_kernel<D>;
   const int smem = C::smem(p.topk, p.nb);
-  DASH_ALLOW_SMEM(kern, smem);
+  DASH_ALLOW_SMEM(kern, C::smem(dash::kTokenTopk, dash::kTokenBlocks));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(units * cs));
   cfg.blockDim = dim3(C::kThreads);
@@ -491,7 +500,7 @@ int launch_select_tile(const dash::SelectParams& p, int B, cudaStream_t stream) 
   using C = dash::SelectCfg<D, QT>;
   auto kern = dash::dash_block_select_kernel<D, QT, NL>;
   const int smem = C::smem(p.nb);
-  DASH_ALLOW_SMEM(kern, smem);
+  DASH_ALLOW_SMEM(kern, C::smem(NL * 32));  // NL blocks a lane
   kern<<<dim3((p.Sq + QT - 1) / QT, B * p.Hkv), C::kThreads, smem, stream>>>(p);
   DASH_CUDA(cudaGetLastError());
   return DASH_OK;
@@ -539,12 +548,13 @@ extern "C" {
 int dash_block_means(const void* k, const long long* k_strides, float* means, const int* kv_len,
                      const int* start, int B, int Hkv, int Sk, int D, int block, void* stream) {
   return no_throw([&]() -> int {
-    if (B < 0 || Hkv < 0 || Sk < 1 || block < dash::kUnit || block % dash::kUnit != 0)
-      return DASH_ERR_INVALID_ARG;
+    if (B < 0 || Hkv < 0 || Sk < 1) return DASH_ERR_INVALID_ARG;
+    int rc = check_block(block, 1);
+    if (rc) return rc;
     if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
-    if ((long long)B * Hkv > 65535) return DASH_ERR_UNSUPPORTED;
+    if (Sk > kMostKeys || (long long)B * Hkv > 65535) return DASH_ERR_UNSUPPORTED;
     Strides st;
-    int rc = take_strides(k_strides, B, Hkv, Sk, D, &st);
+    rc = take_strides(k_strides, B, Hkv, Sk, D, &st);
     if (rc) return rc;
     if (B == 0 || Hkv == 0) return DASH_OK;
     if (!aligned16(k) || !aligned4(means) || !aligned4_or_null(kv_len) || !aligned4_or_null(start))
@@ -570,8 +580,8 @@ int dash_block_select(const void* q, const long long* q_strides, const float* me
   return no_throw([&]() -> int {
     int rc = check_heads(B, H, Hkv, Sq, Sk);
     if (rc) return rc;
-    if (block < dash::kUnit || block % dash::kUnit != 0 || topk < 1 || sink < 0 || local < 0 ||
-        (long long)sink + local > topk || (causal != 0 && causal != 1))
+    if ((rc = check_block(block, topk))) return rc;
+    if (sink < 0 || local < 0 || (long long)sink + local > topk || (causal != 0 && causal != 1))
       return DASH_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
     Strides st;
@@ -676,8 +686,8 @@ int dash_attn_sparse_tokens(const void* q, const void* k, const void* v, const l
   return no_throw([&]() -> int {
     int rc = check_heads(B, H, Hkv, Sq, Sk);
     if (rc) return rc;
-    if (block < dash::kUnit || block % dash::kUnit != 0 || topk < 1 ||
-        (causal != 0 && causal != 1) || !(scale >= 0.f) || std::isinf(scale))
+    if ((rc = check_block(block, topk))) return rc;
+    if ((causal != 0 && causal != 1) || !(scale >= 0.f) || std::isinf(scale))
       return DASH_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
     Strides st[3];

@@ -112,6 +112,30 @@ def test_selection_refuses(lib, al):
     assert select(q=0, Sq=0) == OK
 
 
+def test_sizes_that_pass_32_bits(lib, al):
+    for call in (fwd, tokens, bwd):
+        assert call(lib, al, Sk=(1 << 30) + 64, block=1 << 30) == UNSUPPORTED
+        assert call(lib, al, block=2 ** 31 - 64) == UNSUPPORTED
+        assert call(lib, al, topk=(1 << 20) + 1) == UNSUPPORTED
+    assert lib.dash_sparse_plan_bytes(1, 4, 2, 8, 256, 2 ** 31 - 64, 2) == -UNSUPPORTED
+    assert lib.dash_block_means(al, None, al, None, None, 1, 2, 256, 64, 2 ** 31 - 64, None) == UNSUPPORTED
+    assert lib.dash_block_select(al, None, al, al, None, None, 1, 4, 2, 8, 256, 64, 2 ** 31 - 64, 4, 1, 1,
+                                 1, None) == UNSUPPORTED
+    # a Python integer past the entry points' int does not arrive as another one
+    q, k = host(1, 4, 8, 64), host(1, 2, 256, 64)
+    means, idx = host(1, 2, 1, 64, dtype=torch.float32), host(1, 2, 8, 2, dtype=torch.int32)
+    for block in (2 ** 31, 2 ** 32 + 64):
+        with pytest.raises(ValueError):
+            dash._block_count(256, block)
+    with pytest.raises(ValueError):
+        dash._block_count(2 ** 32 + 256, 64)
+    for bad in (dict(topk=2 ** 32 + 1), dict(sink=2 ** 32), dict(local=2 ** 32 + 1), dict(topk=0)):
+        with pytest.raises(ValueError, match="topk"):
+            dash.dash_block_select(q, means, 256, 256, **dict(dict(topk=2), **bad))
+    with pytest.raises(ValueError):
+        dash.dash_sparse_plan(idx, 2 ** 32 + 4, 256, 64)
+
+
 def test_checkpoints_refuse(lib, al):
     vp, ll = ctypes.c_void_p * 1, ctypes.c_longlong * 1
     for call in (lib.dash_ckpt8_pack, lib.dash_ckpt8_unpack):
