@@ -581,10 +581,23 @@ def _expect(name, t, shape, dtype, device=None, contiguous=True):
 
 def _expect_rows(name, t, B, device):
     """An optional int32 [B] tensor of the batch (kv_len, q_start, start)."""
+    if t is None:
+        return None
     import torch
-    if t is not None:
+    if not (t.dtype is torch.int32 and t.is_cuda and t.device == device and t.shape == (B,)
+            and t.is_contiguous()):
         _expect(name, t, (B,), torch.int32, device)
-    return None if t is None else t.data_ptr()
+    return t.data_ptr()
+
+
+def _expect_input(name, t):
+    """A bf16 input of any strides, of which only shape and device are its own; the strides
+    argument.  The usual case at once (1 us in place of 3)."""
+    import torch
+    if t.dtype is torch.bfloat16 and t.is_cuda and t.is_contiguous() and not t.data_ptr() & 15:
+        return None
+    _expect(name, t, t.shape, torch.bfloat16, contiguous=False)
+    return _strides(t)
 
 
 def _like(t, dtype=None):
@@ -619,17 +632,17 @@ def dash_block_means(k, block, kv_len=None, start=None, out=None, stream=None):
     if k.dim() != 4:
         raise ValueError("k must be [B,Hkv,Sk,D]")
     B, Hkv, Sk, D = k.shape
-    _expect("k", k, k.shape, torch.bfloat16, contiguous=False)
+    strides, device = _expect_input("k", k), k.device
     nb = _block_count(Sk, block)
     if start is not None and out is None:
         raise ValueError("start updates means in place: give them as out")
-    n, s = _expect_rows("kv_len", kv_len, B, k.device), _expect_rows("start", start, B, k.device)
+    n, s = _expect_rows("kv_len", kv_len, B, device), _expect_rows("start", start, B, device)
     if out is not None:
-        _expect("out", out, (B, Hkv, nb, D), torch.float32, k.device)
-    with _Launch(k.device, stream) as st:
+        _expect("out", out, (B, Hkv, nb, D), torch.float32, device)
+    with _Launch(device, stream) as st:
         if out is None:
             out = k.new_empty((B, Hkv, nb, D), dtype=torch.float32)
-        _check(load().dash_block_means(k.data_ptr(), _strides(k), out.data_ptr(), n, s, B, Hkv, Sk,
+        _check(load().dash_block_means(k.data_ptr(), strides, out.data_ptr(), n, s, B, Hkv, Sk,
                                        D, block, st), "dash_block_means")
     return out
 
@@ -647,15 +660,15 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
     if not (0 < topk <= 1 << 20 and 0 <= sink <= topk and 0 <= local <= topk - sink):
         raise ValueError(f"topk = {topk}, sink = {sink}, local = {local}: sink + local <= topk, "
                          "1 <= topk <= 2^20 are needed")
-    _expect("q", q, q.shape, torch.bfloat16, contiguous=False)
-    _expect("means", means, (B, Hkv, _block_count(seq_k, block), D), torch.float32, q.device)
-    n, s = _expect_rows("kv_len", kv_len, B, q.device), _expect_rows("q_start", q_start, B, q.device)
+    strides, device = _expect_input("q", q), q.device
+    _expect("means", means, (B, Hkv, _block_count(seq_k, block), D), torch.float32, device)
+    n, s = _expect_rows("kv_len", kv_len, B, device), _expect_rows("q_start", q_start, B, device)
     if out is not None:
-        _expect("out", out, (B, Hkv, Sq, topk), torch.int32, q.device)
-    with _Launch(q.device, stream) as st:
+        _expect("out", out, (B, Hkv, Sq, topk), torch.int32, device)
+    with _Launch(device, stream) as st:
         if out is None:
             out = q.new_empty((B, Hkv, Sq, topk), dtype=torch.int32)
-        _check(load().dash_block_select(q.data_ptr(), _strides(q), means.data_ptr(), out.data_ptr(),
+        _check(load().dash_block_select(q.data_ptr(), strides, means.data_ptr(), out.data_ptr(),
                                         n, s, B, H, Hkv, Sq, seq_k, D, block, topk,
                                         int(bool(causal)), sink, local, st), "dash_block_select")
     return out

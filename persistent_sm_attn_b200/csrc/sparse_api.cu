@@ -115,6 +115,12 @@ int check_block(int block, int topk) {
   return block > kMostKeys || topk > kMostPicks ? DASH_ERR_UNSUPPORTED : DASH_OK;
 }
 
+// A block longer than the sequence is one of its whole units: what a kernel walks by blocks
+// then ends with the keys
+int trim_block(int block, int Sk) {
+  return (int)std::min((long long)block, ((long long)Sk + dash::kUnit - 1) / dash::kUnit * dash::kUnit);
+}
+
 int check_heads(int B, int H, int Hkv, int Sq, int Sk) {
   if (B < 0 || H < 0 || Sq < 0 || Sk < 1) return DASH_ERR_INVALID_ARG;
   if (Sk > kMostKeys) return DASH_ERR_UNSUPPORTED;
@@ -136,14 +142,14 @@ int plan_shape(int B, int H, int Hkv, int Sq, int Sk, int block, int topk, int c
   if (causal != 0 && causal != 1) return DASH_ERR_INVALID_ARG;
   *s = PlanShape{};
   s->B = B, s->H = H, s->Hkv = Hkv, s->Sq = Sq, s->Sk = Sk;
-  s->block = block, s->topk = topk, s->causal = causal;
+  s->block = trim_block(block, Sk), s->topk = topk, s->causal = causal;
   if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
   s->G = H / Hkv;
   s->T = dash::kTileRows / s->G;
   s->W = (s->T + 31) / 32;
   s->NT = (Sq + s->T - 1) / s->T;
   s->nu = (int)(((long long)Sk + dash::kUnit - 1) / dash::kUnit);
-  const long long picks = (long long)std::min(s->T, Sq) * topk * (block / dash::kUnit);
+  const long long picks = (long long)std::min(s->T, Sq) * topk * (s->block / dash::kUnit);
   s->U = (int)std::min((long long)s->nu, picks);
   s->NW = (s->nu + 31) / 32;
   // the plan kernel holds one tile's masks in shared memory
@@ -565,8 +571,8 @@ int dash_block_means(const void* k, const long long* k_strides, float* means, co
     p.means = means;
     p.kv_len = kv_len;
     p.start = start;
-    p.Hkv = Hkv, p.Sk = Sk, p.D = D, p.block = block;
-    p.nb = (Sk + block - 1) / block;
+    p.Hkv = Hkv, p.Sk = Sk, p.D = D, p.block = trim_block(block, Sk);
+    p.nb = (Sk + p.block - 1) / p.block;
     dash::dash_block_means_kernel<<<dim3(start ? std::min(p.nb, 2) : p.nb, B * Hkv), 128, 0,
                                     static_cast<cudaStream_t>(stream)>>>(p);
     DASH_CUDA(cudaGetLastError());
@@ -597,8 +603,9 @@ int dash_block_select(const void* q, const long long* q_strides, const float* me
     p.idx = idx;
     p.kv_len = kv_len;
     p.q_start = q_start;
-    p.Hkv = Hkv, p.G = H / Hkv, p.Sq = Sq, p.Sk = Sk, p.block = block, p.topk = topk;
-    p.nb = (Sk + block - 1) / block;
+    p.Hkv = Hkv, p.G = H / Hkv, p.Sq = Sq, p.Sk = Sk, p.topk = topk;
+    p.block = trim_block(block, Sk);
+    p.nb = (Sk + p.block - 1) / p.block;
     p.causal = causal, p.sink = sink, p.local = local;
     if (p.nb > 4096) return DASH_ERR_UNSUPPORTED;  // the queries' scores lie in shared memory
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -712,8 +719,9 @@ int dash_attn_sparse_tokens(const void* q, const void* k, const void* v, const l
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
     p.H = H, p.Hkv = Hkv, p.G = H / Hkv, p.RG = (p.G + 15) / 16;
-    p.Sq = Sq, p.Sk = Sk, p.block = block, p.topk = topk, p.causal = causal;
-    p.nb = (int)(((long long)Sk + block - 1) / block);
+    p.Sq = Sq, p.Sk = Sk, p.topk = topk, p.causal = causal;
+    p.block = trim_block(block, Sk);
+    p.nb = (Sk + p.block - 1) / p.block;
     if (topk > dash::kTokenTopk || p.nb > dash::kTokenBlocks) return DASH_ERR_UNSUPPORTED;
     p.scale_log2 = scale_or_default(scale, D) * 1.4426950408889634f;
     const long long units = (long long)B * Hkv * Sq * p.RG;

@@ -924,15 +924,15 @@ __global__ void __launch_bounds__(640, 1)
           }
         } else {
           constexpr uint32_t ID_T = idesc_bf16_f32(128, kUnit, 1, 1);  // dV^T, dK^T
-            const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
+          const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
           // the accumulators of item k - 2 must have been read
           if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
 #pragma unroll 1
           for (int e = first; e < end && ok; ++e, ++j) {
             const uint32_t aV = sdesc_lo(sDO(s), 16384);
             const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
-          const uint32_t bP = sdesc_lo(sP(j), 16384), bS = sdesc_lo(sP(j) + C::kP, 16384);
-          const uint32_t bL = sdesc_lo(sP(j) + 2 * C::kP, 16384);
+            const uint32_t bP = sdesc_lo(sP(j), 16384), bS = sdesc_lo(sP(j) + C::kP, 16384);
+            const uint32_t bL = sdesc_lo(sP(j) + 2 * C::kP, 16384);
             ok = wait(C::kTurns ? DS_READY(j) : P_READY(j), ph2(j));
             if (!ok) break;
             tc_fence_after();

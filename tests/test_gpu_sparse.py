@@ -486,3 +486,21 @@ def test_the_first_use_may_be_captured():
     import sys
     out = subprocess.run([sys.executable, "-c", FIRST_USE], capture_output=True, text=True, timeout=120)
     assert out.returncode == 0 and "same" in out.stdout, out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("Sq", [1, 140])
+def test_a_block_longer_than_the_sequence(Sq):
+    # the same as a block of the sequence's length, in time as well
+    a = case(2, 4, 2, Sq, 200, 64, 256, 2, True, ragged=True, seed=31)
+    b = dict(a, block=1 << 30)
+    results = []
+    for c in (a, b):
+        means = dash.dash_block_means(c["k"], c["block"], kv_len=c["kv_len"])
+        idx = dash.dash_block_select(c["q"], means, 200, c["block"], 2, kv_len=c["kv_len"],
+                                     q_start=c["q_start"])
+        plan = make_plan(c)
+        o, lse = run_fwd(c, plan=plan)
+        results.append((means, idx, *run_fwd(c), o, lse,
+                        *dash.dash_attn_sparse_bwd(c["q"], c["k"], c["v"], o, c["do"], lse, plan)))
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
