@@ -61,6 +61,13 @@ __global__ void __launch_bounds__(256) dash_sparse_delta_kernel(const SparseDelt
   }
 }
 
+// The k-th of this CTA's items of a list whose longest come first: the CTAs take them in turns
+// that go to and fro, so that all get nearly the same sum.  Ascending in k.
+__device__ __forceinline__ int snake_item(int k) {
+  const int x = (int)blockIdx.x, g = (int)gridDim.x;
+  return k * g + ((k & 1) ? g - 1 - x : x);
+}
+
 // ------------------------------------------------------------------ dQ
 struct SparseDqParams {
   PlanView plan;
@@ -95,7 +102,7 @@ struct SparseDqCfg {
 };
 
 // A persistent CTA per SM takes query tiles, those with the longest lists (the last, under a
-// causal mask) first.  Per listed unit j: S = Q K^T, dP = dO V^T (128 x 64, TMEM), dS in bf16
+// causal mask) first, in turns that go to and fro.  Per listed unit j: S = Q K^T, dP = dO V^T (128 x 64, TMEM), dS in bf16
 // over S, dQ += dS K.  Even and odd units have an issuer of S and dP and a softmax warpgroup
 // each, so that one unit's exponentials run beside the other's dS; three buffers of S and dP
 // turn, and a unit's products wait only for the dQ product three units back.  (Two buffers,
@@ -105,9 +112,10 @@ struct SparseDqCfg {
 // token t, head g, so a warp holds few tokens and skips the exponentials of units that none
 // of them picked.
 //
-// Measured: 214 us and 329 us in these two cases, 1400 and 1100 cycles a unit where the products
+// Measured: 198 us and 318 us in these two cases, 1300 and 1000 cycles a unit where the products
 // alone take 1160 and 730 (a 128 x 64 x 16 product 48, which is what reading its operands from
-// shared memory takes, a commit 35); the busiest CTA has 11 % more units than the mean.
+// shared memory takes, a commit 35).  With turns that all go one way the busiest CTA has 11 %
+// more units than the mean and not 2 %: 209 and 328 us.
 //
 // kLow: dS enters its product as the sum of two bf16 values instead of one, whose rounding of
 // up to 2^-8 is otherwise the larger part of the result's error; see sparse_low_part.
@@ -202,9 +210,10 @@ __global__ void __launch_bounds__(384, 1)
   // Tiles without a unit take no part in the numbering k of tiles and j of units.
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-    auto next_tile = [&](int& i, Tile& w) {
-      for (i += gridDim.x; i < p.tiles; i += gridDim.x) {
-        w = tile_at(i);
+    int m = 0;  // tiles looked at
+    auto next_tile = [&](Tile& w) {
+      while (snake_item(m) < p.tiles) {
+        w = tile_at(snake_item(m++));
         if (w.n > 0) return true;
       }
       return false;
@@ -230,13 +239,13 @@ __global__ void __launch_bounds__(384, 1)
       for (int cb = 0; cb < D / 64; ++cb)
         tma_load_4d(dst + cb * 8192, map, cb * 64, u * kUnit, w.hk, w.b, bar);
     };
-    int i = (int)blockIdx.x - (int)gridDim.x, k = 0, j = 0;
+    int k = 0, j = 0;
     Tile w, nw;
-    bool on = next_tile(i, w);
+    bool on = next_tile(w);
     if (on && C::kQ == 2) load_q(w, 0);
     while (on) {
       const int* units = p.plan.unit + w.gt * p.U;
-      const bool more = next_tile(i, nw);
+      const bool more = next_tile(nw);
       int u = units[0];
       for (int e = 0; e < w.n; ++e, ++j) {
         const int next = e + 1 < w.n ? units[e + 1] : 0;
@@ -271,8 +280,8 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;  // no wait has run out: else no more products
     int k = 0, j0 = 0;
 #pragma unroll 1
-    for (int i = blockIdx.x; i < p.tiles && ok; i += gridDim.x) {
-      const int y = i / BHk;
+    for (int m = 0; snake_item(m) < p.tiles && ok; ++m) {
+      const int i = snake_item(m), y = i / BHk;
       const int n = p.plan.count[(long long)(i - y * BHk) * p.NT + (p.NT - 1 - y)];
       if (n == 0) continue;
       if (warp < 3) {
@@ -346,8 +355,8 @@ __global__ void __launch_bounds__(384, 1)
     const float sl2 = p.scale_log2;
     const int bit = t & 31, wsel = min(t >> 5, p.W - 1);
     int j0 = 0, k = 0;
-    for (int i = blockIdx.x; i < p.tiles; i += gridDim.x) {
-      const Tile w = tile_at(i);
+    for (int m = 0; snake_item(m) < p.tiles; ++m) {
+      const Tile w = tile_at(snake_item(m));
       const int token = w.t0 + t;
       const bool valid = t < p.T && token < p.Sq;
       __nv_bfloat16* out =
@@ -550,15 +559,10 @@ __global__ void __launch_bounds__(128)
 }
 
 // Items of the dK/dV pass: every picked unit, its tokens in tiles of T, cut into stretches of
-// at most C tiles with C = max(4, total / kStretches).  The longest come first and the CTAs
-// take them in turns that go to and fro (snake_item), so that all get nearly the same number
-// of tiles.  Fewer and longer stretches would balance less well, more write more partials.
+// at most C tiles with C = max(4, total / kStretches), the longest first (see snake_item).
+// Fewer and longer stretches would balance less well, more write more partials.
 constexpr int kStretches = 148 * 4;
 constexpr int kMinStretch = 4;
-__device__ __forceinline__ int snake_item(int k) {
-  const int x = (int)blockIdx.x, g = (int)gridDim.x;
-  return k * g + ((k & 1) ? g - 1 - x : x);
-}
 
 struct SparseItem {
   int unit, first, end, slot;   // unit, tiles, partial slot or -1
