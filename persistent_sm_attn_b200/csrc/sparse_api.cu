@@ -495,10 +495,11 @@ int ckpt_params(const void* const* src, void* const* dst, signed char* const* ex
   }
   return DASH_OK;
 }
-// Four pieces of 8 elements a thread; at most 32 CTAs of 256 threads for each of 148 SMs, then
-// a stride (8 for each: 175 and 155 us in place of 167 and 135)
-unsigned ckpt_grid(const dash::CkptParams& p) {
-  return (unsigned)std::min((p.groups[p.n] * 4 + 1023) / 1024, 148LL * 32);
+// A CTA takes 1024 pieces of 8 elements at a time: packing with at most 32 CTAs for each of 148
+// SMs and then a stride (268 million elements: 125 us, 130 with a CTA for every 1024 pieces),
+// reading back, which keeps less for each piece, with a CTA for all (119 us, 125 with a stride).
+unsigned ckpt_grid(const dash::CkptParams& p, long long most) {
+  return (unsigned)std::min((p.groups[p.n] * 4 + 1023) / 1024, most);
 }
 
 template <int D, int QT, int NL>
@@ -772,7 +773,7 @@ int dash_ckpt8_pack(const void* const* x, void* const* m, signed char* const* e,
     dash::CkptParams p{};
     int rc = ckpt_params(x, m, e, elems, n, &p);
     if (rc || p.groups[n] == 0) return rc;
-    dash::dash_ckpt8_pack_kernel<<<ckpt_grid(p), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    dash::dash_ckpt8_pack_kernel<<<ckpt_grid(p, 148 * 32), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
   }, DASH_ERR_OOM, DASH_ERR_INVALID_ARG);
@@ -784,7 +785,7 @@ int dash_ckpt8_unpack(const void* const* m, signed char* const* e, void* const* 
     dash::CkptParams p{};
     int rc = ckpt_params(m, x, e, elems, n, &p);
     if (rc || p.groups[n] == 0) return rc;
-    dash::dash_ckpt8_unpack_kernel<<<ckpt_grid(p), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    dash::dash_ckpt8_unpack_kernel<<<ckpt_grid(p, 0x7fffffff), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
     DASH_CUDA(cudaGetLastError());
     return DASH_OK;
   }, DASH_ERR_OOM, DASH_ERR_INVALID_ARG);
