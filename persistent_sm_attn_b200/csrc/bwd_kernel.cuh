@@ -289,12 +289,22 @@ __global__ void __launch_bounds__(512, 1)
         p.trace[((size_t)tmem_slot[1] * p.trace_rows + row) * kTraceEvents + ev] = globaltimer();
     }
   };
-  auto wait = [&](uint32_t bar, uint32_t phase) { mbar_wait(bar, phase, lim, p.err, p.abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t phase) {
+    return mbar_wait(bar, phase, lim, p.err, p.abort_flag);
+  };
+  // TMA producers at work: warp 12, and at D = 128 warp 15.  One whose wait has run out (`ok`)
+  // loads nothing more, so the phases of the loads' barriers are exact to the end, as the
+  // drains need them
+  uint32_t* loading = tmem_slot + 2;
+  auto wait_load = [&](uint32_t bar, uint32_t phase) {
+    mbar_wait_load(bar, phase, lim, p.err, p.abort_flag, loading);
+  };
   auto drain = [&](uint32_t bar, uint32_t phase) {
-    mbar_wait_drain(bar, phase, lim, p.err, p.abort_flag);
+    mbar_wait_drain(bar, phase, drain_ns(lim), p.err, p.abort_flag);
   };
 
   if (threadIdx.x == 0) {
+    *loading = C::kSDouble ? 1u : 2u;
     mbar_init(BAR(B_KV_FULL), 1);
     mbar_init(BAR(B_KV_EMPTY), C::kSDouble ? 2u : 1u);
     mbar_init(BAR(B_S_FULL), 1);
@@ -419,12 +429,14 @@ __global__ void __launch_bounds__(512, 1)
       // S^T and dP^T, which finish before dK frees the stage), and at D = 64 dO.  At
       // D = 128 dO has a producer of its own (warp 15), so a Q load never queues behind
       // the wait for the single dO stage.
-      int it = 0, kn = 0;  // kn: K/V loads so far
+      int it = 0, kn = 0, nd = 0;  // Q, K/V and dO loads so far
+      bool ok = true;
       const uint64_t pol_first = policy_evict_first();  // K/V: one chain's use only
-      for (int ci = cbeg; ci < cend; ++ci) {
+      for (int ci = cbeg; ci < cend && ok; ++ci) {
         const int4 ch = p.chains[ci];
         if (!(ch.w & kChainContPrev)) {
-          if (kn > 0) wait(BAR(B_KV_EMPTY), (kn - 1) & 1);
+          if (kn > 0) ok = wait(BAR(B_KV_EMPTY), (kn - 1) & 1);
+          if (!ok) break;
           mbar_expect_tx(BAR(B_KV_FULL), 2 * C::kTile);
           const int row_kv = (ch.x >> gl2) * S + ch.y * 128;
 #pragma unroll
@@ -434,23 +446,27 @@ __global__ void __launch_bounds__(512, 1)
           }
           ++kn;
         }
-        for (int t = 0; t < n_pairs(ch.w); ++t, ++it) {
+        for (int t = 0; t < n_pairs(ch.w); ++t) {
           const int q = (int)(p.pairs[ch.z + t] & 0xffffu);
           const int s = it % ST;
           const int row_q = ch.x * S + q * 128;
-          if (it >= ST) wait(Q_EMPTY(s), ((it / ST) - 1) & 1);
+          if (it >= ST) ok = wait(Q_EMPTY(s), ((it / ST) - 1) & 1);
+          if (!ok) break;
           mbar_expect_tx(Q_FULL(s), C::kTile + 2048);
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb)
             tma_load_2d(sQ + s * C::kTile + cb * 16384, &tmQ, cb * 64, row_q, Q_FULL(s));
           tma_load_2d(sb + C::OFF_COL + s * C::kColTile, &tmC, 0, row_q, Q_FULL(s));
+          ++it;
           if constexpr (C::kSDouble) {
-            const int sd = it % SD;
-            if (it >= SD) wait(DO_EMPTY(sd), ((it / SD) - 1) & 1);
+            const int sd = nd % SD;
+            if (nd >= SD) ok = wait(DO_EMPTY(sd), ((nd / SD) - 1) & 1);
+            if (!ok) break;
             mbar_expect_tx(DO_FULL(sd), C::kTile);
 #pragma unroll
             for (int cb = 0; cb < D / 64; ++cb)
               tma_load_2d(sDO + sd * C::kTile + cb * 16384, &tmDO, cb * 64, row_q, DO_FULL(sd));
+            ++nd;
           }
         }
       }
@@ -460,22 +476,25 @@ __global__ void __launch_bounds__(512, 1)
         drain(Q_FULL(s), (last_use / ST) & 1);
       }
       if constexpr (C::kSDouble) {
-        for (int s = 0; s < SD && s < it; ++s) {
-          const int last_use = ((it - 1 - s) / SD) * SD + s;
+        for (int s = 0; s < SD && s < nd; ++s) {
+          const int last_use = ((nd - 1 - s) / SD) * SD + s;
           drain(DO_FULL(s), (last_use / SD) & 1);
         }
       }
       if (kn > 0) drain(BAR(B_KV_FULL), (kn - 1) & 1);
+      loads_done(smem_u32(loading));
     } else if (warp == 15 && lane == 0 && !C::kSDouble) {
       // ---------------------------------------------------------- TMA producer: dO
       int it = 0;
-      for (int ci = cbeg; ci < cend; ++ci) {
+      bool ok = true;
+      for (int ci = cbeg; ci < cend && ok; ++ci) {
         const int4 ch = p.chains[ci];
         for (int t = 0; t < n_pairs(ch.w); ++t, ++it) {
           const int q = (int)(p.pairs[ch.z + t] & 0xffffu);
           const int sd = it % SD;
           const int row_q = ch.x * S + q * 128;
-          if (it >= SD) wait(DO_EMPTY(sd), ((it / SD) - 1) & 1);
+          if (it >= SD) ok = wait(DO_EMPTY(sd), ((it / SD) - 1) & 1);
+          if (!ok) break;
           mbar_expect_tx(DO_FULL(sd), C::kTile);
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb)
@@ -486,6 +505,7 @@ __global__ void __launch_bounds__(512, 1)
         const int last_use = ((it - 1 - s) / SD) * SD + s;
         drain(DO_FULL(s), (last_use / SD) & 1);
       }
+      loads_done(smem_u32(loading));
     } else if (warp == 13 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       // One thread issues every MMA at D = 128; at D = 64 this one issues the score
@@ -519,7 +539,7 @@ __global__ void __launch_bounds__(512, 1)
           const uint32_t kQ = sdesc_lo(sQ + s * C::kTile, 16);
           const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
           const uint32_t tSi = tS + s_col(i);
-          wait(Q_FULL(s), (i / ST) & 1);
+          wait_load(Q_FULL(s), (i / ST) & 1);
           trace(i, 12);
           if (i >= 2) wait(DQ_EMPTY(i - 2), s_phase(i - 2));
           tc_fence_after();
@@ -538,7 +558,7 @@ __global__ void __launch_bounds__(512, 1)
           const int s = i % ST, sd = i % SD;
           const uint32_t kDO = sdesc_lo(sDO + sd * C::kTile, 16);
           const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
-          wait(DO_FULL(sd), (i / SD) & 1);
+          wait_load(DO_FULL(sd), (i / SD) & 1);
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -573,7 +593,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int ci = cbeg; ci < cend; ++ci) {
           const int cnt = n_pairs(p.chains[ci].w);
           const bool cprev = cont_prev(ci);
-          if (!cprev) wait(BAR(B_KV_FULL), (kn++) & 1);
+          if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
           tc_fence_after();
           if (cnt > 0) {
             issue_s(it);
@@ -603,7 +623,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int ci = cbeg; ci < cend; ++ci) {
           const int cnt = n_pairs(p.chains[ci].w);
           const bool cprev = cont_prev(ci);
-          if (!cprev) wait(BAR(B_KV_FULL), (kn++) & 1);
+          if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
           tc_fence_after();
           // t = -1 only issues the chain's first S^T/dP^T; each later step finishes
           // tile `it` and then issues S^T/dP^T of the next tile behind it
@@ -657,7 +677,7 @@ __global__ void __launch_bounds__(512, 1)
               const uint32_t kQ = sdesc_lo(sQ + s * C::kTile, 16);
               const uint32_t kDO = sdesc_lo(sDO + sd * C::kTile, 16);
               const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
-              wait(Q_FULL(s), (it / ST) & 1);
+              wait_load(Q_FULL(s), (it / ST) & 1);
               trace(it, 12);
               if (it > 0) wait(BAR(B_DVDK_DONE), (it - 1) & 1);
               tc_fence_after();
@@ -672,7 +692,7 @@ __global__ void __launch_bounds__(512, 1)
               tc_commit(BAR(B_S_FULL));
               // dP^T = V dO^T; at D = 128 these columns hold dQp of the previous tile
               // until the reducers have drained it
-              wait(DO_FULL(sd), (it / SD) & 1);
+              wait_load(DO_FULL(sd), (it / SD) & 1);
               if (C::kDqInDp && it > 0) wait(BAR(B_DQ_EMPTY0), (it - 1) & 1);
               tc_fence_after();
   #pragma unroll
@@ -707,13 +727,15 @@ __global__ void __launch_bounds__(512, 1)
       for (int ci = cbeg; ci < cend; ++ci) {
         const int cnt = n_pairs(p.chains[ci].w);
         const bool cprev = cont_prev(ci);
-        if (!cprev) wait(BAR(B_KV_FULL), (kn++) & 1);
+        if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
         for (int t = 0; t < cnt; ++t, ++it) {
           const int s = it % ST;
           const uint32_t dsb = sDSt + 32768u * (uint32_t)(it & 1);
           const uint32_t mQ = sdesc_lo(sQ + s * C::kTile, 16384);
           const uint32_t mDSi = sdesc_lo(dsb, 16384);  // dS MN-major (dQp)
           const uint32_t kDSi = sdesc_lo(dsb, 16);     // dS^T K-major (dK)
+          // Q is there whenever dS is, but a softmax that gave up a wait reports dS all the same
+          wait_load(Q_FULL(s), (it / ST) & 1);
           wait(DS_READY(it), s_phase(it));
           // a run's first chain: the previous run's dK must have been read out
           if (t == 0 && !cprev && kn >= 2) wait(BAR(B_DKDV_EMPTY), (kn - 2) & 1);
