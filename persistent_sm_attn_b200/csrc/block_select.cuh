@@ -368,7 +368,7 @@ __device__ __forceinline__ void pick_exact(Picks<NL>& k, int need, const SelectP
   }
 }
 
-// Writes the picks ascending, then -1.
+// Writes the picks ascending, then -1; topk places, however many blocks are marked.
 template <int NL>
 __device__ __forceinline__ void put_out(const Picks<NL>& k, int topk, int* out, int lane) {
   constexpr int W = Picks<NL>::W;
@@ -379,17 +379,25 @@ __device__ __forceinline__ void put_out(const Picks<NL>& k, int topk, int* out, 
     if (x >= k.nl) break;
     const bool on = (k.take[W == 1 ? 0 : x >> 5] >> (x & 31)) & 1u;
     const unsigned m = __ballot_sync(0xffffffffu, on);
-    if (on) out[done + __popc(m & below)] = 32 * x + lane;
+    const int at = done + __popc(m & below);
+    if (on && at < topk) out[at] = 32 * x + lane;
     done += __popc(m);
   }
   for (int x = done + lane; x < topk; x += 32) out[x] = -1;
+}
+
+// A vector's squared norm as the bounds take it: below 2^-100 the squares of its elements may
+// have left fp32's range (those under 2^-63 are 0 or inexact), and no bound comes from it.  From
+// there on what is lost, at most 128 squares of 2^-126, is 2^-19 of it.
+__device__ __forceinline__ float norm_or_inf(float n2) {
+  return n2 < 0x1p-100f ? INFINITY : sqrtf(n2);
 }
 
 // Few queries (serving): a CTA per query reads the K/V head's means once, a warp per row with
 // 16 (D = 64: 8) bytes a lane, eight rows in flight.  A score is a sum of D products in fp32
 // with D/32 + 5 roundings on the way of each, so it is off by less than 2^-20 |q||m|, and by
 // what the heads' sum was rounded by (see dash_block_select_kernel); |m| is at most sqrt(D)
-// times the largest element.  Bound by reading the means: 64 tokens of 8 K/V heads, up to 256
+// times the largest element.  Queries too small for their norm go to fp64 altogether.  Bound by reading the means: 64 tokens of 8 K/V heads, up to 256
 // blocks each, in 12.4 us (all scores in fp64: 21).
 template <int D, int NL>
 __global__ void __launch_bounds__(256) dash_block_select_token_kernel(const SelectParams p) {
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(256) dash_block_select_token_kernel(const Sele
       a2 += __shfl_xor_sync(0xffffffffu, a2, o);
     }
     const float mnorm = sqrtf((float)D) * __int_as_float(top_bits);
-    const float qn = sqrtf(n2), most = (qn + 0x1p-10f * sqrtf(a2)) * mnorm;
+    const float qn = norm_or_inf(n2), most = (qn + 0x1p-10f * sqrtf(a2)) * mnorm;
     const float eps2 = 2.f * ((0x1p-20f * qn + 0x1p-24f * p.G * sqrtf(a2)) * mnorm + 1e-35f);
     float guess = 0.f;
     const int need = pick_approx<NL>(k, sc, most, eps2, guess, qn / (most + 1e-30f) *
@@ -526,7 +534,8 @@ struct SelectCfg {
 // their cancelling may make large against q.  Together, with u = 3 * 2^-16 + (3 D + 3) 2^-23
 // and a thousandth for the norms' own rounding, the error is below
 //     eps = 1.001 u (|q| + G 2^-24 / u |sum_g |q_g||) max_j |m_j|.
-// An eps that is not finite (an infinity or NaN among the operands) leaves everything to fp64.
+// An eps that is not finite (an infinity or NaN among the operands, a norm too small for fp32's
+// squares) leaves everything to fp64.
 //
 // NL: 32-block words that a lane's share of a row has room for.
 template <int D, int QT, int NL>
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
       n2 += __shfl_xor_sync(0xffffffffu, n2, o);
       a2 += __shfl_xor_sync(0xffffffffu, a2, o);
     }
-    if (c == 0) qnorm[row] = sqrtf(n2) + 0x1p-24f / C::kError * p.G * sqrtf(a2);
+    if (c == 0) qnorm[row] = norm_or_inf(n2) + 0x1p-24f / C::kError * p.G * sqrtf(a2);
   }
 
   // ---- scores
@@ -659,7 +668,7 @@ __global__ void __launch_bounds__(512, 2) dash_block_select_kernel(const SelectP
 
   // ---- picks, a warp per query.  Queries whose picks the bound leaves open are put off, so
   // that the warps share them (one in fifteen on normal data, two blocks each)
-  const float mnorm = sqrtf(__int_as_float(mnorm_bits));
+  const float mnorm = norm_or_inf(__int_as_float(mnorm_bits));
   uint32_t* saved = reinterpret_cast<uint32_t*>(mstage);  // [QT][2 W][32], over the means
   auto out = [&](int rr) { return p.idx + ((long long)bh * p.Sq + i0 + rr) * p.topk; };
   float guess = 0.f;  // the last cut, of the largest score that could be

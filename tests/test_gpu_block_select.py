@@ -153,3 +153,43 @@ def test_heads_that_cancel(Sq, far):
     means = dash.dash_block_means(k, 64)
     got = dash.dash_block_select(q, means, 3000, 64, 9, False, 1, 1)
     assert torch.equal(got.cpu(), R.select(q, means, 3000, 64, 9, False, 1, 1))
+
+
+def select_into_guarded(q, means, Sk, topk):
+    """The picks, written into the middle of a larger buffer of which nothing else may change."""
+    B, _, Sq, _ = q.shape
+    Hkv = means.shape[1]
+    n, pad = B * Hkv * Sq * topk, 4096
+    buf = torch.full((n + 2 * pad,), -77, device="cuda", dtype=torch.int32)
+    out = buf[pad:pad + n].view(B, Hkv, Sq, topk)
+    dash.dash_block_select(q, means, Sk, 64, topk, False, 1, 1, out=out)
+    assert (buf[:pad] == -77).all() and (buf[pad + n:] == -77).all()
+    return out.cpu()
+
+
+# powers of ten that bf16 holds: an fp32 square is 0 from 1e-23 on, a bf16 subnormal from 1e-38
+@pytest.mark.parametrize("Sq", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("qs,ks", [(1e-12, 1.0), (1e-17, 1e-6), (1e-20, 1.0), (1e-23, 1.0), (1e-25, 1.0),
+                                   (1e-30, 1.0), (1e-38, 1.0), (1.0, 1e-17), (1.0, 1e-23), (1.0, 1e-25),
+                                   (1.0, 1e-38), (1e-25, 1e-25), (1e-19, 1e-19), (1e-30, 1e25)])
+def test_tiny_operands(Sq, D, qs, ks):
+    q, k, _, _ = inputs(1, 2, 1, Sq, 40 * 64, D, False, 8)
+    q, k = (q.double() * qs).to(torch.bfloat16), (k.double() * ks).to(torch.bfloat16)
+    means = dash.dash_block_means(k, 64)
+    want = R.select(q, means, 40 * 64, 64, 6, False, 1, 1)
+    assert torch.equal(select_into_guarded(q, means, 40 * 64, 6), want)
+
+
+def test_tiny_queries_and_blocks_beside_ordinary_ones():
+    q, k, _, _ = inputs(2, 3, 1, 100, 3000, 64, False, 9)
+    q[0, :, ::3] *= 1e-25
+    q[1, :, 1::3] *= 1e-38
+    k[:, :, 640:1280] *= 1e-25
+    k[1, :, 2000:] = 0
+    means = dash.dash_block_means(k, 64)
+    assert torch.equal(select_into_guarded(q, means, 3000, 9), R.select(q, means, 3000, 64, 9, False, 1, 1))
+    for i in (0, 1, 3):
+        one = q[:, :, i:i + 1].contiguous()
+        assert torch.equal(select_into_guarded(one, means, 3000, 9),
+                           R.select(one, means, 3000, 64, 9, False, 1, 1))
