@@ -92,7 +92,7 @@ struct SparseDqCfg {
   static constexpr int OFF_K = kQ * 2 * kTile;
   static constexpr int OFF_V = OFF_K + kK * kKV;
   static constexpr int OFF_BAR = OFF_V + kV * kKV;
-  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 3 * 3 + 1;
+  static constexpr int kBars = 2 * kK + 2 * kV + 2 * 4 + 2 * 6 + 3 + 1;
   static constexpr int OFF_SLOT = OFF_BAR + kBars * 8;
   static constexpr int kSmemBytes = OFF_SLOT + 16;
   static_assert(kSmemBytes <= 232448, "shared memory per block exceeded");
@@ -150,12 +150,17 @@ __global__ void __launch_bounds__(384, 1)
   auto Q_EMPTY = [&](int k) { return bar1 + 16u + 8u * (uint32_t)(k & 1); };
   auto DONE = [&](int k) { return bar1 + 32u + 8u * (uint32_t)(k & 1); };
   auto ACC_FREE = [&](int k) { return bar1 + 48u + 8u * (uint32_t)(k & 1); };
-  // per buffer of S and dP
+  // S and dP have three buffers and six barriers each, so that a barrier belongs to one
+  // softmax warpgroup (units j mod 2), which sees all its phases.  With three, the phase of
+  // unit j + 3 is the other warpgroup's, and j + 6, which the first waits for next, has the
+  // parity of j: if S of j + 3 came late, the wait would pass on the phase of j
   const uint32_t bar2 = bar1 + 64u;
-  auto S_FULL = [&](int j) { return bar2 + 8u * (uint32_t)(j % 3); };
-  auto DP_FULL = [&](int j) { return bar2 + 24u + 8u * (uint32_t)(j % 3); };
-  auto DS_READY = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j % 3); };
-  const uint32_t FINAL = bar2 + 72;
+  auto S_FULL = [&](int j) { return bar2 + 8u * (uint32_t)(j % 6); };
+  auto DP_FULL = [&](int j) { return bar2 + 48u + 8u * (uint32_t)(j % 6); };
+  auto ph6 = [](int j) { return (uint32_t)((j / 6) & 1); };
+  // per buffer: the issuer of dQ, its only reader, sees all phases
+  auto DS_READY = [&](int j) { return bar2 + 96u + 8u * (uint32_t)(j % 3); };
+  const uint32_t FINAL = bar2 + 120;
   auto ph3 = [](int j) { return (uint32_t)((j / 3) & 1); };
   auto ph2 = [](int k) { return (uint32_t)((k >> 1) & 1); };
   auto phK = [](int j) { return (uint32_t)((j / C::kK) & 1); };
@@ -190,11 +195,11 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(DONE(k), 1);
       mbar_init(ACC_FREE(k), 8);
     }
-    for (int j = 0; j < 3; ++j) {
+    for (int j = 0; j < 6; ++j) {
       mbar_init(S_FULL(j), 1);
       mbar_init(DP_FULL(j), 1);
-      mbar_init(DS_READY(j), 4);
     }
+    for (int j = 0; j < 3; ++j) mbar_init(DS_READY(j), 4);
     mbar_init(FINAL, 3);
     fence_mbar_init();
   }
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t keep = v > 0 ? 0xffffffffu : 0u;
         const uint32_t tS = tmem + lane_off + C::TM_S + 128u * (uint32_t)(j % 3), tDP = tS + 64;
         float pr[kUnit];
-        wait(S_FULL(j), ph3(j));
+        wait(S_FULL(j), ph6(j));
         tc_fence_after();
         if (any) {
           uint32_t sv[2][32];
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           fence_proxy_async_smem();
         }
-        wait(DP_FULL(j), ph3(j));
+        wait(DP_FULL(j), ph6(j));
         tc_fence_after();
         if (any) {
 #pragma unroll
