@@ -942,7 +942,12 @@ __global__ void __launch_bounds__(640, 1)
             const uint32_t aK = D == 128 ? sdesc_lo(sQ(s), 16384) : aV;
             const uint32_t bP = sdesc_lo(sP(j), 16384), bS = sdesc_lo(sP(j) + C::kP, 16384);
             const uint32_t bL = sdesc_lo(sP(j) + 2 * C::kP, 16384);
-            ok = wait(C::kTurns ? DS_READY(j) : P_READY(j), ph2(j));
+            // D = 128: P is there before dP, and with it before dO need be.  The dP product has
+            // waited for dO and, once done, read it: only then may dV read the stage and its
+            // commit free it.  (dP of j + 2 needs that commit, so the phase cannot run ahead.)
+            static_assert(C::kTurns || ST == 2, "a stage of dO per parity of the tile");
+            ok = C::kTurns ? wait(DS_READY(j), ph2(j))
+                           : wait(DP_FULL(j), ph2(j)) && wait(P_READY(j), ph2(j));
             if (!ok) break;
             tc_fence_after();
             if (leader) {

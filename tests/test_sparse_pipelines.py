@@ -146,3 +146,94 @@ def test_dq_takes_no_scores_before_they_are_there(stages):
         assert dq_pass(seed, int(n), kK=stages[0], kV=stages[1]) == [], seed
     # one barrier a buffer is not enough: two warpgroups' phases take turns on it
     assert any(dq_pass(seed, 3, kK=stages[0], kV=stages[1]) for seed in range(300))
+
+
+def dkdv_pass(seed, dv_waits_for_dp, tiles=40, stages=2):
+    """dK and dV of one item at D = 128.  Returns the tiles whose dO was read by dV or dP when the
+    stage held another, or replaced while dP still read it."""
+    rng = random.Random(seed)
+    bad = []
+    FULL = [[Barrier() for _ in range(stages)] for _ in range(2)]   # Q, dO
+    EMPTY = [[Barrier() for _ in range(stages)] for _ in range(2)]
+    S_FULL, DP_FULL, SDP_READ, P_READY, P_FREE, DS_READY, DS_FREE = (
+        [Barrier(), Barrier()] for _ in range(7))
+    held, reading = [None] * stages, [None] * stages   # tile whose dO a stage holds; that dP reads
+    ph = lambda j, n: (j // n) & 1
+    slow = lambda: rng.expovariate(1.0) * rng.choice([1, 1, 1, 30])
+
+    def loader(x):
+        for j in range(tiles):
+            s = j % stages
+            if j >= stages:
+                yield EMPTY[x][s], ph(j - stages, stages)
+            if x:
+                if reading[s] is not None:
+                    bad.append(reading[s])
+                held[s] = None
+            yield slow()
+            if x:
+                held[s] = j
+            FULL[x][s].arrive()
+
+    def scores():
+        for j in range(tiles):
+            s = j % stages
+            yield FULL[0][s], ph(j, stages)
+            if j >= 2:
+                yield SDP_READ[j % 2], ph(j - 2, 2)
+            yield 0.3
+            S_FULL[j % 2].arrive()
+            yield rng.choice([0, 0, 3])  # another warp's thread is late now and then
+            yield FULL[1][s], ph(j, stages)
+            if held[s] != j:
+                bad.append(j)
+            reading[s] = j
+            yield 0.3
+            if held[s] != j:
+                bad.append(j)
+            reading[s] = None
+            DP_FULL[j % 2].arrive()
+
+    def softmax():
+        for j in range(tiles):
+            yield S_FULL[j % 2], ph(j, 2)
+            yield 0.4
+            if j:
+                yield P_FREE[(j - 1) % 2], ph(j - 1, 2)
+            P_READY[j % 2].arrive()
+            yield DP_FULL[j % 2], ph(j, 2)
+            if j:
+                yield DS_FREE[(j - 1) % 2], ph(j - 1, 2)
+            yield 0.4
+            SDP_READ[j % 2].arrive()
+            DS_READY[j % 2].arrive()
+
+    def gradients():
+        for j in range(tiles):
+            s = j % stages
+            if dv_waits_for_dp:
+                yield DP_FULL[j % 2], ph(j, 2)
+            yield P_READY[j % 2], ph(j, 2)
+            if held[s] != j:
+                bad.append(j)
+            yield 0.3
+            P_FREE[j % 2].arrive()
+            EMPTY[1][s].arrive()
+            yield DS_READY[j % 2], ph(j, 2)
+            yield 0.3
+            EMPTY[0][s].arrive()
+            DS_FREE[j % 2].arrive()
+
+    m = Machine([loader(0), loader(1), scores(), softmax(), gradients()])
+    try:
+        m.run()
+    except AssertionError:
+        bad.append(None)
+    return bad
+
+
+def test_dv_reads_and_frees_a_stage_of_dO_after_dP():
+    waits = "wait(DP_FULL(j), ph2(j)) && wait(P_READY(j), ph2(j))" in SOURCE
+    for seed in range(300):
+        assert dkdv_pass(seed, waits) == [], seed
+    assert any(dkdv_pass(seed, False) for seed in range(300))
