@@ -224,7 +224,9 @@ int dash_bwd_head_interleave(int num_ctas, int D, int schedule, int n_heads, int
  * waits run out; the kernel still ends, with DASH_ERR_TIMEOUT reported by
  * dash_attn_sync_status (dash_attn_noalloc_sync_status for the second) and
  * invalid outputs.  The fault is made on the host; no memory outside the
- * call's buffers is touched.  mode 0 cancels.  Other modes: INVALID_ARG.
+ * call's buffers is touched.  mode 2: the next block-sparse forward with a plan, or
+ * backward, loads only the first few units of each CTA; waits on the others run out, with
+ * the same status.  mode 0 cancels both.  Other modes: INVALID_ARG.
  */
 int dash_inject_fault(int mode);
 

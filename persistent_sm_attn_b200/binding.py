@@ -317,7 +317,8 @@ def dash_set_spin_limit_us(us: int) -> None:
 
 
 def dash_inject_fault(mode: int) -> None:
-    """Arm (1) or cancel (0) the host-side fault for the next backward."""
+    """Arm the host-side fault for the next backward (1) or block-sparse call with a plan (2), or
+    cancel both (0)."""
     _check(load().dash_inject_fault(int(mode)), "dash_inject_fault")
 
 

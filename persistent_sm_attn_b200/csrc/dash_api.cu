@@ -40,6 +40,7 @@ long long default_spin_us() {
 }
 std::atomic<long long> g_spin_us{0};
 std::atomic<int> g_fault{0};  // host-side fault injection for the next backward (tests only)
+std::atomic<int> g_sparse_fault{0};  // the same for the next block-sparse call with a plan
 long long spin_us() {
   long long v = g_spin_us.load();
   return v > 0 ? v : default_spin_us();
@@ -939,6 +940,7 @@ namespace dash {
 
 long long spin_limit_us() { return spin_us(); }
 int take_armed_fault() { return g_fault.exchange(0); }
+int take_sparse_fault() { return g_sparse_fault.load() ? g_sparse_fault.exchange(0) : 0; }
 int head_interleave_mode() { return g_il_mode.load(); }
 
 }  // namespace dash
@@ -961,8 +963,9 @@ const char* dash_status_string(int s) {
 }
 
 int dash_inject_fault(int mode) {
-  if (mode != 0 && mode != 1) return DASH_ERR_INVALID_ARG;
-  g_fault.store(mode);
+  if (mode < 0 || mode > 2) return DASH_ERR_INVALID_ARG;
+  if (mode != 2) g_fault.store(mode);
+  if (mode != 1) g_sparse_fault.store(mode);
   return DASH_OK;
 }
 

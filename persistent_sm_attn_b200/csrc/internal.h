@@ -15,6 +15,9 @@ int take_armed_fault();
 // The mode set with dash_set_head_interleave (0: the library's choice).
 int head_interleave_mode();
 
+// Takes the fault armed with dash_inject_fault(2) (0: none).
+int take_sparse_fault();
+
 // Status recorded by the block-sparse kernels' bounded waits on (device, stream), cleared by
 // this call; the stream has been waited for.
 int sparse_take_status(int dev, void* stream);

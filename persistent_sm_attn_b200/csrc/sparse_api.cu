@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <map>
@@ -237,6 +238,10 @@ int fwd_splits(const PlanShape& s) {
   return (int)std::max(1LL, std::min({want, (long long)(s.U + 1) / 2, 64LL}));
 }
 
+// Loads of a CTA: all, or with a fault that dash_inject_fault(2) has armed the first few, so that
+// waits run out with work in flight.
+int take_loads() { return dash::take_sparse_fault() ? 3 : INT_MAX; }
+
 float scale_or_default(float scale, int D) { return scale > 0.f ? scale : 1.0f / sqrtf((float)D); }
 
 template <int D>
@@ -268,6 +273,7 @@ int launch_sparse_fwd(const void* q, const void* k, const void* v, const Strides
   p.err = words;
   p.H = s.H, p.Hkv = s.Hkv, p.Sq = s.Sq, p.Sk = s.Sk, p.G = s.G, p.T = s.T, p.W = s.W;
   p.NT = s.NT, p.U = s.U, p.causal = s.causal;
+  p.loads = take_loads();
   p.scale_log2 = scale_or_default(scale, D) * 1.4426950408889634f;
   p.spin_ns = (unsigned long long)dash::spin_limit_us() * 1000ull;
   const long long grid = (long long)s.B * s.Hkv * s.NT * p.splits;
@@ -406,6 +412,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   a.Hkv = s.Hkv, a.Sq = s.Sq, a.Sk = s.Sk, a.G = s.G, a.T = s.T, a.W = s.W;
   a.NT = s.NT, a.U = s.U, a.causal = s.causal;
   a.tiles = s.B * s.Hkv * s.NT;
+  a.loads = take_loads();
   a.scale = sc;
   a.scale_log2 = sc * 1.4426950408889634f;
   a.spin_ns = spin;
@@ -456,6 +463,7 @@ int launch_sparse_bwd(const void* q, const void* k, const void* v, const void* d
   c.err = words;
   c.Hkv = s.Hkv, c.Sq = s.Sq, c.Sk = s.Sk, c.G = s.G, c.T = s.T;
   c.nu = s.nu, c.causal = s.causal;
+  c.loads = a.loads;
   c.scale = sc;
   c.scale_log2 = a.scale_log2;
   c.spin_ns = spin;

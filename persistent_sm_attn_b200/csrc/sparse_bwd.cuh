@@ -76,6 +76,7 @@ struct SparseDqParams {
   __nv_bfloat16* dq;   // [B,H,Sq,D]
   unsigned* err;
   int Hkv, Sq, Sk, G, T, W, NT, U, tiles, causal;
+  int loads;  // units that the producer loads (all, but for a planted fault)
   float scale, scale_log2;
   unsigned long long spin_ns;
 };
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(384, 1)
       int u = units[0];
       for (int e = 0; e < w.n; ++e, ++j) {
         const int next = e + 1 < w.n ? units[e + 1] : 0;
+        ok = ok && j < p.loads;
         if (j >= C::kK) ok = ok && wait(K_EMPTY(j), phK(j - C::kK));
         if (ok) load_unit(sK(j), &tmK, u, w, K_FULL(j)), nk = j + 1;
         if (j >= C::kV) ok = ok && wait(V_EMPTY(j), phV(j - C::kV));
@@ -334,7 +336,9 @@ __global__ void __launch_bounds__(384, 1)
           const int j = j0 + e;
           const uint32_t mK = sdesc_lo(sK(j), 8192);
           const uint32_t tDS = tmem + C::TM_S + 128u * (uint32_t)(j % 3);
-          ok = wait(DS_READY(j), ph3(j));
+          // K is there whenever dS is, but a softmax that gave up a wait reports dS all the same,
+          // and a stage freed before its load has landed would have its barrier armed twice
+          ok = wait(K_FULL(j), phK(j)) && wait(DS_READY(j), ph3(j));
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -689,6 +693,7 @@ struct SparseDkvParams {
   float* part;             // [slots][2][64][D] (dK, dV)
   unsigned* err;
   int Hkv, Sq, Sk, G, T, nu, causal;
+  int loads;  // items whose K and V are loaded (all, but for a planted fault)
   float scale, scale_log2;
   unsigned long long spin_ns;
 };
@@ -877,7 +882,7 @@ __global__ void __launch_bounds__(640, 1)
         const SparseItem w = p.item[snake_item(k)];
         const int u = w.unit - w.bh * p.nu, hk = w.bh - w.b * p.Hkv;
         // K and V of item k - 2 are read to the end; nothing is loaded once a wait has run out
-        if (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2))) break;
+        if (k >= p.loads || (k >= 2 && !wait(ITEM_DONE(k), ph2(k - 2)))) break;
         mbar_expect_tx(KV_FULL(k), 2 * C::kKV);
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb) {
@@ -936,6 +941,9 @@ __global__ void __launch_bounds__(640, 1)
           const uint32_t tA = tmem + C::TM_ACC + 128u * (uint32_t)(k & 1);
           // the accumulators of item k - 2 must have been read
           if (k >= 2) ok = wait(ACC_FREE(k), ph2(k - 2));
+          // it frees K and V: not before they have landed, even where softmax warps that gave up
+          // a wait report P and dS
+          ok = ok && wait(KV_FULL(k), ph2(k));
 #pragma unroll 1
           for (int e = first; e < end && ok; ++e, ++j) {
             const uint32_t aV = sdesc_lo(sDO(s), 16384);

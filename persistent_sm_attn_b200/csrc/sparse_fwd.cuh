@@ -47,6 +47,7 @@ struct SparseFwdParams {
   float* part_l;     // [splits][B*H*Sq] log2-domain log-sum-exp of the part
   unsigned* err;     // [0] error word, [1] abort flag
   int H, Hkv, Sq, Sk, G, T, W, NT, U, causal, splits;
+  int loads;  // units that the producer loads (all, but for a planted fault)
   float scale_log2;
   unsigned long long spin_ns;
 };
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(256, 2)
     int u = n > 0 ? units[0] : 0;
     for (int j = 0; j < n; ++j) {
       const int next = j + 1 < n ? units[j + 1] : 0;
-      if (j >= C::kK && !wait(K_EMPTY(j), phK(j - C::kK))) break;
+      if (j >= p.loads || (j >= C::kK && !wait(K_EMPTY(j), phK(j - C::kK)))) break;
       mbar_expect_tx(K_FULL(j), C::kKV);
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb)

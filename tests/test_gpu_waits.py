@@ -58,3 +58,44 @@ def test_a_forward_with_the_shortest_limit(D, causal):
         o, lse = dash.dash_attn_fwd(case["q"], case["k"], case["v"], causal)
         assert dash.dash_attn_sync_status() == 0
         assert torch.equal(o, case["o"]) and torch.equal(lse, case["lse"])
+
+
+def sparse_case(D, Sq=3000, H=6, Hkv=3, topk=14, seed=44):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    mk = lambda h: torch.randn(2, h, Sq, D, generator=gen, device="cuda").to(torch.bfloat16)
+    q, k, v, do = mk(H), mk(Hkv), mk(Hkv), mk(H)
+    idx = torch.randint(0, -(-Sq // 64), (2, Hkv, Sq, topk), generator=gen, device="cuda", dtype=torch.int32)
+    return q, k, v, do, idx
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("limit", [1, 2000])
+def test_block_sparse_calls_that_run_out(D, limit):
+    q, k, v, do, idx = sparse_case(D)
+    plan = dash.dash_sparse_plan(idx, 6, 3000, 64)
+    forward = lambda: dash.dash_attn_sparse_fwd(q, k, v, idx, 64, plan=plan)
+    o, lse = forward()
+    backward = lambda: dash.dash_attn_sparse_bwd(q, k, v, o, do, lse, plan)
+    want = backward()
+    assert dash.dash_attn_sync_status() == 0
+    side = torch.cuda.Stream()
+    for call, right in ((forward, (o, lse)), (backward, want)) * 2:
+        dash.dash_set_spin_limit_us(limit)
+        dash.dash_inject_fault(2)
+        call()
+        # the stream that ran out reports it once; another one has nothing to report
+        assert dash.dash_attn_sync_status(side) == 0
+        assert dash.dash_attn_sync_status() == TIMEOUT
+        assert dash.dash_attn_sync_status() == 0
+        dash.dash_set_spin_limit_us(0)
+        for a, b in zip(call(), right):
+            assert torch.equal(a, b)
+        assert dash.dash_attn_sync_status() == 0
+
+
+def test_a_cancelled_fault_is_not_taken():
+    q, k, v, _, idx = sparse_case(64, Sq=500)
+    dash.dash_inject_fault(2)
+    dash.dash_inject_fault(0)
+    dash.dash_attn_sparse_fwd(q, k, v, idx, 64, plan=dash.dash_sparse_plan(idx, 6, 500, 64))
+    assert dash.dash_attn_sync_status() == 0
