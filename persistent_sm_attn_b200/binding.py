@@ -677,11 +677,12 @@ def dash_block_select(q, means, seq_k, block, topk, causal=True, sink=1, local=1
 
 class SparsePlan:
     """A selection prepared by dash_sparse_plan for the forward and the backward."""
-    __slots__ = ("buf", "shape", "causal", "stream")
+    __slots__ = ("buf", "shape", "causal", "stream", "has_kv_len", "has_q_start")
 
-    def __init__(self, buf, shape, causal, stream):
+    def __init__(self, buf, shape, causal, stream, has_kv_len=True, has_q_start=True):
         self.buf, self.shape, self.causal = buf, shape, causal  # shape: B,H,Hkv,Sq,Sk,block,topk
         self.stream = stream  # handle of the stream the plan was made on
+        self.has_kv_len, self.has_q_start = has_kv_len, has_q_start  # given when it was made
 
     def on(self, stream):
         """The plan's address for work on `stream` (a handle); the memory outlives that work."""
@@ -717,7 +718,7 @@ def dash_sparse_plan(idx, heads, seq_k, block, causal=True, kv_len=None, q_start
         buf = idx.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_sparse_plan(idx.data_ptr(), n, s, buf.data_ptr(), *shape, int(bool(causal)),
                                     st), "dash_sparse_plan")
-    return SparsePlan(buf, shape, bool(causal), st)
+    return SparsePlan(buf, shape, bool(causal), st, kv_len is not None, q_start is not None)
 
 
 def _expect_qkv(q, k, v):
@@ -747,6 +748,23 @@ def _expect_plan(plan, shape, device):
         raise ValueError(f"the plan must be on {device}")
 
 
+def _expect_same_selection(plan, idx, block, causal, kv_len, q_start):
+    """Reject a forward whose own arguments are not those of its plan, as far as they can be told
+    without reading the device."""
+    if block != plan.shape[5]:
+        raise ValueError(f"the plan is for blocks of {plan.shape[5]}, not {block}")
+    if causal is not None and bool(causal) != plan.causal:
+        raise ValueError(f"the plan was made with causal = {plan.causal}")
+    if idx is not None:
+        B, _, Hkv, Sq, _, _, topk = plan.shape
+        if idx.shape != (B, Hkv, Sq, topk):
+            raise ValueError(f"idx has shape {tuple(idx.shape)}, the plan is for {(B, Hkv, Sq, topk)}")
+    if kv_len is not None and not plan.has_kv_len:
+        raise ValueError("the plan was made without kv_len")
+    if q_start is not None and not plan.has_q_start:
+        raise ValueError("the plan was made without q_start")
+
+
 def _few_queries(B, H, Hkv, Sq):
     """Whether each query reads its keys for itself, without a plan: single tokens, and short
     runs while a token of a K/V head (16 query heads at a time) leaves most SMs free.  With 8
@@ -756,19 +774,24 @@ def _few_queries(B, H, Hkv, Sq):
     return Sq == 1 or B * Hkv * Sq * -(-(H // max(Hkv, 1)) // 16) <= 256
 
 
-def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=None, scale=None,
+def dash_attn_sparse_fwd(q, k, v, idx, block, causal=None, kv_len=None, q_start=None, scale=None,
                          plan=None, out=None, lse=None, stream=None):
     """O, LSE of attention over the selected blocks: q [B,H,Sq,D], k and v [B,Hkv,Sk,D] (any
     strides with a contiguous last dimension), idx int32 [B,Hkv,Sq,topk].  A query that sees
-    nothing gets O = 0 and LSE = -inf.  Give the `plan` of idx where the backward follows;
-    idx, block, causal, kv_len and q_start are then those it was made with."""
+    nothing gets O = 0 and LSE = -inf.  causal: True unless given, or the plan's.  Give the
+    `plan` of idx where the backward follows: the selection is then the plan's; block, and what
+    else is given of idx, causal, kv_len and q_start, have to be those it was made with (the
+    tensors' contents are not compared)."""
     import torch
     B, H, Hkv, Sq, Sk, D, strides = _expect_qkv(q, k, v)
     if out is not None:
         _expect("out", out, (B, H, Sq, D), torch.bfloat16, q.device)
     if lse is not None:
         _expect("lse", lse, (B, H, Sq), torch.float32, q.device)
-    if plan is None:
+    if plan is not None:
+        _expect_same_selection(plan, idx, block, causal, kv_len, q_start)
+    else:
+        causal = causal is None or bool(causal)
         _expect("idx", idx, (B, Hkv, Sq, idx.shape[-1]), torch.int32, q.device)
         topk, blocks = idx.shape[-1], _block_count(Sk, block)
         if _few_queries(B, H, Hkv, Sq) and topk <= 1024 and blocks <= 65536:
@@ -785,7 +808,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=True, kv_len=None, q_start=
                 _check(load().dash_attn_sparse_tokens(
                     q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, idx.data_ptr(), n, s,
                     out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
-                    int(bool(causal)), float(scale or 0.0), st), "dash_attn_sparse_fwd")
+                    int(causal), float(scale or 0.0), st), "dash_attn_sparse_fwd")
             return out, lse
         plan = dash_sparse_plan(idx, H, Sk, block, causal, kv_len, q_start, stream)
     _expect_plan(plan, (B, H, Hkv, Sq, Sk), q.device)

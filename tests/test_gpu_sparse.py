@@ -504,3 +504,21 @@ def test_a_block_longer_than_the_sequence(Sq):
                         *dash.dash_attn_sparse_bwd(c["q"], c["k"], c["v"], o, c["do"], lse, plan)))
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+def test_the_forward_and_its_plan_agree():
+    c = case(2, 4, 2, 190, 640, 64, 64, 4, False, seed=41)
+    plan = make_plan(c)
+    o, lse = run_fwd(c, plan=plan)
+    for call in (lambda: dash.dash_attn_sparse_fwd(c["q"], c["k"], c["v"], c["idx"], 64, plan=plan),
+                 lambda: dash.dash_attn_sparse_fwd(c["q"], c["k"], c["v"], None, 64, plan=plan)):
+        x, y = call()  # the mask is the plan's
+        assert torch.equal(x, o) and torch.equal(y, lse)
+    check_fwd(c, o, lse)
+    full = dash.dash_attn_sparse_fwd(c["q"], c["k"], c["v"], c["idx"], 64)  # causal without a plan
+    check_fwd(dict(c, causal=True), *full)
+    n = torch.full((2,), 640, device="cuda", dtype=torch.int32)
+    for bad in (dict(c, causal=True), dict(c, block=128), dict(c, idx=c["idx"][..., :3].contiguous()),
+                dict(c, kv_len=n), dict(c, q_start=n)):
+        with pytest.raises(ValueError, match="the plan"):
+            run_fwd(bad, plan=plan)

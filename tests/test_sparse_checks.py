@@ -184,3 +184,19 @@ def test_names_are_public():
                  "dash_attn_sparse_bwd", "dash_attn_sparse_bwd_ckpt8", "dash_ckpt8_pack",
                  "dash_ckpt8_unpack", "dash_attn_bwd_ckpt8"):
         assert getattr(pkg, name) is getattr(dash, name)
+
+
+def test_a_plan_of_another_selection_is_refused():
+    idx = host(1, 2, 8, 3, dtype=torch.int32)
+    n = host(1, dtype=torch.int32)
+    plan = dash.SparsePlan(None, (1, 4, 2, 8, 256, 64, 3), True, 0, True, False)
+    same = dash._expect_same_selection
+    same(plan, idx, 64, True, n, None)
+    same(plan, None, 64, None, None, None)
+    for bad, what in (((plan, idx, 128, True, n, None), "blocks of 64"),
+                      ((plan, idx, 64, False, n, None), "causal"),
+                      ((plan, idx[..., :2], 64, True, n, None), "idx"),
+                      ((plan, idx, 64, True, n, n), "q_start"),
+                      ((dash.SparsePlan(None, plan.shape, True, 0, False, True), idx, 64, True, n, n), "kv_len")):
+        with pytest.raises(ValueError, match=what):
+            same(*bad)
