@@ -141,7 +141,9 @@ int dash_bwd_gqa_split_for(int num_ctas, int B, int Hkv, int group, int S, int c
  * Synchronises `stream`, then returns and clears the device error word of
  * that stream's workspace: DASH_ERR_TIMEOUT if a ticket or pipeline wait of a
  * previous backward on this stream ran out (its outputs are then invalid),
- * DASH_ERR_CUDA if the stream reported an error, else DASH_OK.
+ * DASH_ERR_CUDA if the stream reported an error, else DASH_OK.  The block-sparse
+ * calls have a word of their own, which is returned and cleared once the first is
+ * clear: where both recorded something, two calls report it.
  */
 int dash_attn_sync_status(void* stream);
 

@@ -1161,23 +1161,24 @@ int dash_attn_sync_status(void* stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return DASH_ERR_CUDA;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DASH_ERR_CUDA;
-  const int sparse = dash::sparse_take_status(dev, stream);
+  // the dense calls' word first; what the block-sparse calls recorded is taken once that is
+  // clear, so that neither hides the other
   unsigned* err = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);
     auto itw = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-    if (itw == g_ws.end()) return sparse;
-    err = itw->second.err;
+    if (itw != g_ws.end()) err = itw->second.err;
   }
-  unsigned h = 0;
-  if (!err) return sparse;
-  if (cudaMemcpy(&h, err, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return DASH_ERR_CUDA;
-  if (h) {
-    if (cudaMemset(err, 0, sizeof(unsigned)) != cudaSuccess) return DASH_ERR_CUDA;
-    return (h & dash::dev::ERR_TIMEOUT) ? DASH_ERR_TIMEOUT : DASH_ERR_UNSUPPORTED;
+  if (err) {
+    unsigned h = 0;
+    if (cudaMemcpy(&h, err, sizeof(unsigned), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return DASH_ERR_CUDA;
+    if (h) {
+      if (cudaMemset(err, 0, sizeof(unsigned)) != cudaSuccess) return DASH_ERR_CUDA;
+      return (h & dash::dev::ERR_TIMEOUT) ? DASH_ERR_TIMEOUT : DASH_ERR_UNSUPPORTED;
+    }
   }
-  return sparse;
+  return dash::sparse_take_status(dev, stream);
 }
 
 int dash_bwd_num_ctas(int device, int D, int* num_ctas) {

@@ -99,3 +99,19 @@ def test_a_cancelled_fault_is_not_taken():
     dash.dash_inject_fault(0)
     dash.dash_attn_sparse_fwd(q, k, v, idx, 64, plan=dash.dash_sparse_plan(idx, 6, 500, 64))
     assert dash.dash_attn_sync_status() == 0
+
+
+def test_dense_and_block_sparse_timeouts_are_both_reported():
+    q, k, v, _, idx = sparse_case(64)
+    plan = dash.dash_sparse_plan(idx, 6, 3000, 64)
+    case = G.make_case(1, 2, 512, 64, False, seed=45)
+    want = G.bwd(case, "shift")
+    dash.dash_set_spin_limit_us(2000)
+    dash.dash_inject_fault(1)
+    dash.dash_inject_fault(2)
+    dash.dash_attn_bwd(*[case[n] for n in ("q", "k", "v", "o", "do", "lse")], False, "shift")
+    dash.dash_attn_sparse_fwd(q, k, v, idx, 64, plan=plan)
+    assert [dash.dash_attn_sync_status() for _ in range(3)] == [TIMEOUT, TIMEOUT, 0]
+    dash.dash_set_spin_limit_us(0)
+    for a, b in zip(G.bwd(case, "shift"), want):
+        assert torch.equal(a, b)
