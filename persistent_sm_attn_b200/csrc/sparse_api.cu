@@ -101,12 +101,14 @@ int take_strides(const long long* in, int B, int H, int S, int D, Strides* out) 
   const Strides dense{(long long)H * S * D, (long long)S * D, D};
   *out = dense;
   if (!in) return DASH_OK;
-  if (B > 1) out->b = in[0];
-  if (H > 1) out->h = in[1];
-  if (S > 1) out->s = in[2];
-  for (long long x : {out->b, out->h, out->s})
-    if (x < 8 || x % 8 != 0 || x >= (1LL << 38)) return DASH_ERR_INVALID_ARG;
-  return DASH_OK;
+  // (a dense stride may be 0, of an operand without elements)
+  auto take = [&](int extent, long long x, long long* to) {
+    if (extent <= 1) return true;
+    *to = x;
+    return x >= 8 && x % 8 == 0 && x < (1LL << 38);
+  };
+  return take(B, in[0], &out->b) && take(H, in[1], &out->h) && take(S, in[2], &out->s)
+             ? DASH_OK : DASH_ERR_INVALID_ARG;
 }
 
 // What keeps ceil(Sk / block), the places of a tile's picks and the like within 32 bits

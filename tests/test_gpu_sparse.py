@@ -522,3 +522,14 @@ def test_the_forward_and_its_plan_agree():
                 dict(c, kv_len=n), dict(c, q_start=n)):
         with pytest.raises(ValueError, match="the plan"):
             run_fwd(bad, plan=plan)
+
+
+def test_no_queries_before_a_strided_cache():
+    c = case(1, 4, 2, 0, 300, 64, 64, 2, True, seed=42)
+    wide = torch.zeros(1, 300, 2, 72, device="cuda", dtype=torch.bfloat16)
+    c["k"] = c["v"] = wide[..., :64].transpose(1, 2)
+    o, lse = run_fwd(c)
+    assert o.shape == (1, 4, 0, 64) and lse.shape == (1, 4, 0)
+    plan = make_plan(c)
+    dq, dk, dv = grads_of(c, *run_fwd(c, plan=plan), plan)
+    assert dq.shape == o.shape and (dk == 0).all() and (dv == 0).all()

@@ -200,3 +200,12 @@ def test_a_plan_of_another_selection_is_refused():
                       ((dash.SparsePlan(None, plan.shape, True, 0, False, True), idx, 64, True, n, n), "kv_len")):
         with pytest.raises(ValueError, match=what):
             same(*bad)
+
+
+@pytest.mark.parametrize("call", [fwd, tokens])
+def test_no_queries_before_strided_keys(lib, al, call):
+    # one sequence without queries: q's contiguous strides are 0, which is no one's fault
+    flat = (ctypes.c_longlong * 9)(*([64, 64, 64] + [65536, 72, 144] * 2))
+    assert call(lib, al, strides=flat, Sq=0) == OK
+    flat[7] = 12                                           # v's heads: still looked at
+    assert call(lib, al, strides=flat, Sq=0) == INVALID
