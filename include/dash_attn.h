@@ -484,7 +484,8 @@ int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* d
  * The pages have no counterpart to these calls; they serve the long sequences the
  * backward is made for.  Conventions that differ from the calls above:
  *   - q, o, dout, dq: [B, H, Sq, D]; k, v, dk, dv: [B, Hkv, Sk, D], bf16, D in {64, 128},
- *     H any multiple of Hkv up to 128 query heads per K/V head.  Sq >= 0 and Sk >= 1 are
+ *     H any multiple of Hkv up to 128 query heads per K/V head (with B = 0 or H = 0 nothing is
+ *     written; a selection needs a query head).  Sq >= 0 and Sk >= 1 are
  *     free (no multiple of 128), Sk at most 2^30.  Query head h reads K/V head h / (H / Hkv).
  *   - Inputs may be strided: `strides` holds (batch, head, row) strides in elements for
  *     each strided input in the order of the arguments, positive multiples of 8 (the last

@@ -849,6 +849,8 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
         dq = _like(q) if dq is None else dq
         dk = _like(k) if dk is None else dk
         dv = _like(k) if dv is None else dv
+        if H == 0:  # no head reads a key; the C call has nothing to do
+            return dq, dk.zero_(), dv.zero_()
         work = q.new_empty((max(size, 16),), dtype=torch.uint8)
         _check(lib.dash_attn_sparse_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), do.data_ptr(),
                                         _strides(q, k, v, do), plan.on(st), o.data_ptr(),

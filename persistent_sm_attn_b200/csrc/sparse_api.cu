@@ -603,7 +603,8 @@ int dash_block_select(const void* q, const long long* q_strides, const float* me
     if (D != 64 && D != 128) return DASH_ERR_UNSUPPORTED;
     Strides st;
     if ((rc = take_strides(q_strides, B, H, Sq, D, &st))) return rc;
-    if (B == 0 || H == 0 || Sq == 0) return DASH_OK;
+    if (B == 0 || Sq == 0 || (H == 0 && Hkv == 0)) return DASH_OK;
+    if (H == 0) return DASH_ERR_INVALID_ARG;  // places to fill and nothing to score by
     if (!aligned16(q) || !aligned16(means) || !aligned4(idx) || !aligned4_or_null(kv_len) ||
         !aligned4_or_null(q_start))
       return DASH_ERR_INVALID_ARG;

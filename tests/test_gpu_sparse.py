@@ -533,3 +533,17 @@ def test_no_queries_before_a_strided_cache():
     plan = make_plan(c)
     dq, dk, dv = grads_of(c, *run_fwd(c, plan=plan), plan)
     assert dq.shape == o.shape and (dk == 0).all() and (dv == 0).all()
+
+
+def test_no_query_heads():
+    c = case(2, 2, 2, 5, 100, 64, 64, 2, True, seed=43)
+    c["q"], c["do"] = (c[n][:, :0].contiguous() for n in ("q", "do"))
+    plan = make_plan(c)
+    o, lse = run_fwd(c, plan=plan)
+    assert o.shape == (2, 0, 5, 64) and lse.shape == (2, 0, 5)
+    assert run_fwd(c)[0].shape == o.shape
+    held = torch.full_like(c["k"], float("nan")), torch.full_like(c["v"], float("nan"))
+    dq, dk, dv = grads_of(c, o, lse, plan, dk=held[0], dv=held[1])
+    assert dq.shape == o.shape and dk is held[0] and (dk == 0).all() and (dv == 0).all()
+    with pytest.raises(dash.DashError):
+        dash.dash_block_select(c["q"], dash.dash_block_means(c["k"], 64), 100, 64, 2)

@@ -209,3 +209,10 @@ def test_no_queries_before_strided_keys(lib, al, call):
     assert call(lib, al, strides=flat, Sq=0) == OK
     flat[7] = 12                                           # v's heads: still looked at
     assert call(lib, al, strides=flat, Sq=0) == INVALID
+
+
+def test_a_selection_needs_a_query_head(lib, al):
+    call = lambda B=1, H=0, Hkv=2, Sq=8: lib.dash_block_select(
+        al, None, al, al, None, None, B, H, Hkv, Sq, 256, 64, 64, 4, 1, 1, 1, None)
+    assert call() == INVALID                       # places in idx that nothing would fill
+    assert call(B=0) == OK and call(Sq=0) == OK and call(Hkv=0) == OK
