@@ -765,6 +765,16 @@ def _expect_same_selection(plan, idx, block, causal, kv_len, q_start):
         raise ValueError("the plan was made without q_start")
 
 
+def _scale(scale):
+    """The C calls' scale: None is their 0, 1 / sqrt(D).  A number that is 0 there would be taken
+    for it."""
+    if scale is None:
+        return 0.0
+    if ctypes.c_float(scale).value == 0.0:
+        raise ValueError(f"scale must be positive, not {scale} (None is 1 / sqrt(D))")
+    return float(scale)
+
+
 def _few_queries(B, H, Hkv, Sq):
     """Whether each query reads its keys for itself, without a plan: single tokens, and short
     runs while a token of a K/V head (16 query heads at a time) leaves most SMs free.  With 8
@@ -808,7 +818,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=None, kv_len=None, q_start=
                 _check(load().dash_attn_sparse_tokens(
                     q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, idx.data_ptr(), n, s,
                     out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Sk, D, block, topk,
-                    int(causal), float(scale or 0.0), st), "dash_attn_sparse_fwd")
+                    int(causal), _scale(scale), st), "dash_attn_sparse_fwd")
             return out, lse
         plan = dash_sparse_plan(idx, H, Sk, block, causal, kv_len, q_start, stream)
     _expect_plan(plan, (B, H, Hkv, Sq, Sk), q.device)
@@ -825,7 +835,7 @@ def dash_attn_sparse_fwd(q, k, v, idx, block, causal=None, kv_len=None, q_start=
                                         strides, plan.on(st), out.data_ptr(),
                                         lse.data_ptr(), work.data_ptr() if size else None,
                                         *plan.shape[:5], D, *plan.shape[5:], int(plan.causal),
-                                        float(scale or 0.0), st), "dash_attn_sparse_fwd")
+                                        _scale(scale), st), "dash_attn_sparse_fwd")
     return out, lse
 
 
@@ -856,7 +866,7 @@ def dash_attn_sparse_bwd(q, k, v, o, do, lse, plan, scale=None, dq=None, dk=None
                                         _strides(q, k, v, do), plan.on(st), o.data_ptr(),
                                         lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                         dv.data_ptr(), work.data_ptr(), *plan.shape[:5], D,
-                                        *plan.shape[5:], int(plan.causal), float(scale or 0.0), st),
+                                        *plan.shape[5:], int(plan.causal), _scale(scale), st),
                "dash_attn_sparse_bwd")
     return dq, dk, dv
 

@@ -547,3 +547,18 @@ def test_no_query_heads():
     assert dq.shape == o.shape and dk is held[0] and (dk == 0).all() and (dv == 0).all()
     with pytest.raises(dash.DashError):
         dash.dash_block_select(c["q"], dash.dash_block_means(c["k"], 64), 100, 64, 2)
+
+
+def test_a_scale_of_zero_is_refused():
+    c = case(1, 4, 2, 200, 256, 64, 64, 2, True, seed=44)
+    plan = make_plan(c)
+    o, lse = run_fwd(c, plan=plan)
+    few = dict(c, q=c["q"][:, :, :2].contiguous(), idx=c["idx"][:, :, :2].contiguous())
+    for call in (lambda s: run_fwd(c, scale=s), lambda s: run_fwd(few, scale=s),
+                 lambda s: run_fwd(c, plan=plan, scale=s), lambda s: grads_of(c, o, lse, plan, scale=s)):
+        for scale in (0.0, 1e-50):
+            with pytest.raises(ValueError, match="scale"):
+                call(scale)
+        for scale in (-1.0, float("nan"), float("inf"), 1e39):
+            with pytest.raises(dash.DashError):
+                call(scale)

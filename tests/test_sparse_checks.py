@@ -216,3 +216,11 @@ def test_a_selection_needs_a_query_head(lib, al):
         al, None, al, al, None, None, B, H, Hkv, Sq, 256, 64, 64, 4, 1, 1, 1, None)
     assert call() == INVALID                       # places in idx that nothing would fill
     assert call(B=0) == OK and call(Sq=0) == OK and call(Hkv=0) == OK
+
+
+def test_a_scale_of_zero_is_not_the_default():
+    assert dash._scale(None) == 0.0 and dash._scale(0.25) == 0.25 and dash._scale(2) == 2.0
+    for scale in (0, 0.0, -0.0, 1e-50):  # the last is 0 in fp32
+        with pytest.raises(ValueError, match="scale"):
+            dash._scale(scale)
+    # negative, infinite and NaN scales are refused by the C calls
