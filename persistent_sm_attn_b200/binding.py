@@ -543,8 +543,10 @@ class _Launch:
         else:
             if device.index != torch.cuda.current_device():
                 self._ctx = torch.cuda.device(device)
-            # torch.cuda.current_stream(device).cuda_stream without the two objects (2 us)
-            self._handle = torch._C._cuda_getCurrentRawStream(device.index)
+            # the handle without the two objects of the public call (2 us); the name is torch's
+            # own, so a torch may come without it
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            self._handle = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
 
     def __enter__(self):
         if self._ctx is not None:

@@ -562,3 +562,17 @@ def test_a_scale_of_zero_is_refused():
         for scale in (-1.0, float("nan"), float("inf"), 1e39):
             with pytest.raises(dash.DashError):
                 call(scale)
+
+
+def test_the_current_stream_by_the_public_call(monkeypatch):
+    c = case(2, 4, 2, 70, 200, 64, 64, 2, True, seed=45)
+    o, lse = run_fwd(c)
+    torch.cuda.synchronize()
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        with dash._Launch(c["q"].device, None) as handle:
+            assert handle == side.cuda_stream
+        o2, lse2 = run_fwd(c)
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
