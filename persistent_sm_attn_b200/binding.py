@@ -942,7 +942,7 @@ def dash_attn_bwd_ckpt8(q8, k8, v8, o8, do, lse, causal: bool, schedule="shift",
     ctx = torch.cuda.device(do.device) if stream is None else torch.cuda.stream(stream)
     with ctx if do.is_cuda else contextlib.nullcontext():
         q, k, v, o = dash_ckpt8_unpack(q8, k8, v8, o8, stream=stream)
-        bwd = dash_attn_bwd if q.shape[1] == k.shape[1] else dash_attn_bwd_gqa
+        bwd = dash_attn_bwd if q.shape[1:2] == k.shape[1:2] else dash_attn_bwd_gqa
         return bwd(q, k, v, o, do, lse, causal, schedule, dq, dk, dv, stream)
 
 

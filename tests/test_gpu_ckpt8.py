@@ -97,3 +97,10 @@ def test_backward_from_checkpoints(H, Hkv, S, D, causal, schedule):
     assert dash.dash_attn_sync_status() == 0
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+def test_the_backward_takes_checkpoints_of_four_dimensions():
+    x = torch.zeros(64, device="cuda", dtype=torch.bfloat16)
+    packed = dash.dash_ckpt8_pack(x, x, x, x)
+    with pytest.raises(ValueError, match="q must be"):
+        dash.dash_attn_bwd_ckpt8(*packed, x, torch.zeros(1, device="cuda"), True)
