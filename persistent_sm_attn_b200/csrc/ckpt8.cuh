@@ -5,8 +5,9 @@
 //
 // so the group's largest element lies in [64, 128) steps and a value m 2^e (7 significant
 // bits) is exact in bf16: reading back rounds nothing.  The group's error is at most half
-// a step, max|x| 2^-7 (one step, where an element above 127 steps is clamped to 127).  A
-// group that holds an infinity or a NaN gets e = -128 and reads back as NaN.
+// a step, max|x| 2^-7 where e is not held at -126: also of the element that is clamped, since
+// a bf16 in [64, 128) steps is a whole number of halves, 127.5 at most.  A group that holds an
+// infinity or a NaN gets e = -128 and reads back as NaN.
 #pragma once
 #include "ptx.cuh"
 

@@ -104,3 +104,14 @@ def test_the_backward_takes_checkpoints_of_four_dimensions():
     packed = dash.dash_ckpt8_pack(x, x, x, x)
     with pytest.raises(ValueError, match="q must be"):
         dash.dash_attn_bwd_ckpt8(*packed, x, torch.zeros(1, device="cuda"), True)
+
+
+def test_the_error_is_half_a_step():
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(5000, 256, generator=gen, device="cuda").to(torch.bfloat16)
+    back = check(x)
+    # elements up to 127.5 steps; a bf16 in [64, 128) steps is a whole number of halves, so the clamp
+    # to 127 costs half a step as well.  A step is at most max|x| 2^-6
+    g = x.double().unflatten(-1, (-1, 32))
+    off = (back.double() - x.double()).unflatten(-1, (-1, 32)).abs()
+    assert (off <= g.abs().amax(-1, keepdim=True) * 2.0 ** -7).all()
