@@ -525,7 +525,7 @@ int launch_select_tile(const dash::SelectParams& p, int B, cudaStream_t stream) 
 
 // A CTA per query below 16 queries a head: an MMA tile would be mostly empty.  Otherwise as
 // many queries a CTA as their scores leave room for in shared memory (two CTAs an SM up to
-// 512 blocks, one beyond).
+// 448 blocks at D = 128 and 640 at D = 64, one beyond).
 template <int D>
 int launch_select(const dash::SelectParams& p, int B, cudaStream_t stream) {
   if (p.Sq < 16) {

@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(S_FULL(k), 1);
       mbar_init(DP_FULL(k), 1);
       mbar_init(SDP_READ(k), C::kTurns ? 4 : 8);
-      mbar_init(P_READY(k), 8);
+      mbar_init(P_READY(k), 8);  // D = 128 alone: with kTurns P comes and goes with dS
       mbar_init(P_FREE(k), 1);
       mbar_init(DS_READY(k), C::kTurns ? 4 : 8);
       mbar_init(DS_FREE(k), 1);
@@ -962,8 +962,10 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 tc_mma_ss_w(tA, aV + kk * 128, bP + kk * 128, hi, ID_T, (uint32_t)(e - first + kk));
-              tc_commit(P_FREE(j));
-              if (D == 128) tc_commit(EMPTY(1, s));
+              if (!C::kTurns) {
+                tc_commit(P_FREE(j));
+                tc_commit(EMPTY(1, s));
+              }
             }
             ok = C::kTurns || wait(DS_READY(j), ph2(j));
             if (!ok) break;
@@ -977,7 +979,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                   tc_mma_ss_w(tA + 64, aK + kk * 128, bL + kk * 128, hi, ID_T, 1u);
-              if (D == 64) tc_commit(EMPTY(1, s));
+              if (C::kTurns) tc_commit(EMPTY(1, s));
               tc_commit(EMPTY(0, s));
               tc_commit(DS_FREE(j));
               if (e + 1 == end) tc_commit(ITEM_DONE(k));
