@@ -292,19 +292,26 @@ __global__ void __launch_bounds__(512, 1)
   auto wait = [&](uint32_t bar, uint32_t phase) {
     return mbar_wait(bar, phase, lim, p.err, p.abort_flag);
   };
-  // TMA producers at work: warp 12, and at D = 128 warp 15.  One whose wait has run out (`ok`)
-  // loads nothing more, so the phases of the loads' barriers are exact to the end, as the
-  // drains need them
-  uint32_t* loading = tmem_slot + 2;
+  // Once a wait has run out, arrivals no longer mean what they stand for: a softmax warp that
+  // gave up a wait reports P and dS all the same.  But a producer whose own wait has run out
+  // loads nothing more, and an issuer, whose commits free the stages, ends when a load does
+  // not come.  So no stage is freed before its load has landed, no load's barrier is armed
+  // twice in one phase, which would be undefined, and the phases that the drains look at are
+  // exact.
+  // an issuer's wait for a load.  D = 64: all but the first poll out of line, for the smaller
+  // loop (causal 4 x 32 heads of 16k: 18.7 ms, 19.1 inline).  D = 128, where the load of the
+  // single dO stage is often waited for: inline (full 2 x 16 heads of 4k: 0.949 ms, 0.967)
   auto wait_load = [&](uint32_t bar, uint32_t phase) {
-    mbar_wait_load(bar, phase, lim, p.err, p.abort_flag, loading);
+    if constexpr (C::kSDouble)
+      return mbar_try_wait(bar, phase) || mbar_wait_long(bar, phase, lim, p.err, p.abort_flag);
+    else
+      return wait(bar, phase);
   };
   auto drain = [&](uint32_t bar, uint32_t phase) {
     mbar_wait_drain(bar, phase, drain_ns(lim), p.err, p.abort_flag);
   };
 
   if (threadIdx.x == 0) {
-    *loading = C::kSDouble ? 1u : 2u;
     mbar_init(BAR(B_KV_FULL), 1);
     mbar_init(BAR(B_KV_EMPTY), C::kSDouble ? 2u : 1u);
     mbar_init(BAR(B_S_FULL), 1);
@@ -482,7 +489,6 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
       if (kn > 0) drain(BAR(B_KV_FULL), (kn - 1) & 1);
-      loads_done(smem_u32(loading));
     } else if (warp == 15 && lane == 0 && !C::kSDouble) {
       // ---------------------------------------------------------- TMA producer: dO
       int it = 0;
@@ -505,7 +511,6 @@ __global__ void __launch_bounds__(512, 1)
         const int last_use = ((it - 1 - s) / SD) * SD + s;
         drain(DO_FULL(s), (last_use / SD) & 1);
       }
-      loads_done(smem_u32(loading));
     } else if (warp == 13 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       // One thread issues every MMA at D = 128; at D = 64 this one issues the score
@@ -534,12 +539,12 @@ __global__ void __launch_bounds__(512, 1)
         int it = 0, kn = 0;  // kn: runs started (K/V loads consumed)
         // S'^T = K Q^T - LSE/scale of tile i into its buffer, once the softmax has
         // staged out the dQp that tile i - 2 left there
-        auto issue_s = [&](int i) {
+        auto issue_s = [&](int i) -> bool {
           const int s = i % ST;
           const uint32_t kQ = sdesc_lo(sQ + s * C::kTile, 16);
           const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
           const uint32_t tSi = tS + s_col(i);
-          wait_load(Q_FULL(s), (i / ST) & 1);
+          if (!wait_load(Q_FULL(s), (i / ST) & 1)) return false;
           trace(i, 12);
           if (i >= 2) wait(DQ_EMPTY(i - 2), s_phase(i - 2));
           tc_fence_after();
@@ -551,14 +556,15 @@ __global__ void __launch_bounds__(512, 1)
           }
           tc_mma_ss_w(tSi, kOnesS, kCol, hi_none, ID_SS, 1u);  // - LSE / scale
           tc_commit(S_FULL(i));
+          return true;
         };
         // dP'^T = V dO^T - Delta of tile i (the issuer has already seen the softmax
         // finish with tile i - 1's dP'^T)
-        auto issue_dp = [&](int i) {
+        auto issue_dp = [&](int i) -> bool {
           const int s = i % ST, sd = i % SD;
           const uint32_t kDO = sdesc_lo(sDO + sd * C::kTile, 16);
           const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
-          wait_load(DO_FULL(sd), (i / SD) & 1);
+          if (!wait_load(DO_FULL(sd), (i / SD) & 1)) return false;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -569,6 +575,7 @@ __global__ void __launch_bounds__(512, 1)
           tc_commit(DP_FULL(i));
           tc_commit(Q_EMPTY(s));  // S'^T(i) and dP'^T(i) have read Q and the column tile
           trace(i, 15);
+          return true;
         };
         // dV += P^T dO of tile i (A = P^T from the upper half of its S^T buffer), once
         // P^T is packed; a run's first chain waits for the previous run's read-out
@@ -590,15 +597,16 @@ __global__ void __launch_bounds__(512, 1)
         // dV(it + 1) once P^T(it + 1) is packed, S'^T(it + 2) once the softmax has
         // staged dQp(it) out of S^T buffer it mod 2.  The gradient products (dQp, dK)
         // come from warp 15, so none of these waits holds them up.
+        [&] {
         for (int ci = cbeg; ci < cend; ++ci) {
           const int cnt = n_pairs(p.chains[ci].w);
           const bool cprev = cont_prev(ci);
-          if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
+          if (!cprev && !wait_load(BAR(B_KV_FULL), (kn++) & 1)) return;
           tc_fence_after();
           if (cnt > 0) {
-            issue_s(it);
-            if (cnt > 1) issue_s(it + 1);
-            issue_dp(it);
+            if (!issue_s(it)) return;
+            if (cnt > 1 && !issue_s(it + 1)) return;
+            if (!issue_dp(it)) return;
             issue_dv(it, !cprev, cprev ? 1u : 0u);
           }
           for (int t = 0; t < cnt; ++t, ++it) {
@@ -606,10 +614,10 @@ __global__ void __launch_bounds__(512, 1)
             trace(it, 1);
             tc_fence_after();
             if (t + 1 < cnt) {
-              issue_dp(it + 1);
+              if (!issue_dp(it + 1)) return;
               issue_dv(it + 1, false, 1u);
             }
-            if (t + 2 < cnt) issue_s(it + 2);
+            if (t + 2 < cnt && !issue_s(it + 2)) return;
             trace(it, 2);
           }
           // the run's last chain: its dV are all issued, and S^T / dP^T are done with K/V
@@ -618,12 +626,14 @@ __global__ void __launch_bounds__(512, 1)
             tc_commit(BAR(B_KV_EMPTY));
           }
         }
+        }();
       } else {
         int it = 0, kn = 0;  // kn: runs started (K/V loads consumed)
+        [&] {
         for (int ci = cbeg; ci < cend; ++ci) {
           const int cnt = n_pairs(p.chains[ci].w);
           const bool cprev = cont_prev(ci);
-          if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
+          if (!cprev && !wait_load(BAR(B_KV_FULL), (kn++) & 1)) return;
           tc_fence_after();
           // t = -1 only issues the chain's first S^T/dP^T; each later step finishes
           // tile `it` and then issues S^T/dP^T of the next tile behind it
@@ -677,7 +687,7 @@ __global__ void __launch_bounds__(512, 1)
               const uint32_t kQ = sdesc_lo(sQ + s * C::kTile, 16);
               const uint32_t kDO = sdesc_lo(sDO + sd * C::kTile, 16);
               const uint32_t kCol = sdesc_lo_none(sb + C::OFF_COL + s * C::kColTile, 2048);
-              wait_load(Q_FULL(s), (it / ST) & 1);
+              if (!wait_load(Q_FULL(s), (it / ST) & 1)) return;
               trace(it, 12);
               if (it > 0) wait(BAR(B_DVDK_DONE), (it - 1) & 1);
               tc_fence_after();
@@ -692,7 +702,7 @@ __global__ void __launch_bounds__(512, 1)
               tc_commit(BAR(B_S_FULL));
               // dP^T = V dO^T; at D = 128 these columns hold dQp of the previous tile
               // until the reducers have drained it
-              wait_load(DO_FULL(sd), (it / SD) & 1);
+              if (!wait_load(DO_FULL(sd), (it / SD) & 1)) return;
               if (C::kDqInDp && it > 0) wait(BAR(B_DQ_EMPTY0), (it - 1) & 1);
               tc_fence_after();
   #pragma unroll
@@ -709,6 +719,7 @@ __global__ void __launch_bounds__(512, 1)
           // the run's last chain: K/V are done with
           if (!cont_next(ci)) tc_commit(BAR(B_KV_EMPTY));
         }
+        }();
       }
       // drain: all issued MMAs complete before TMEM is released
       tc_commit(BAR(B_FINAL));
@@ -724,18 +735,19 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t hi = sdesc_hi(1024);
       const uint32_t mK = sdesc_lo(sK, 16384);
       int it = 0, kn = 0;  // kn: runs started
+      [&] {
       for (int ci = cbeg; ci < cend; ++ci) {
         const int cnt = n_pairs(p.chains[ci].w);
         const bool cprev = cont_prev(ci);
-        if (!cprev) wait_load(BAR(B_KV_FULL), (kn++) & 1);
+        if (!cprev && !wait_load(BAR(B_KV_FULL), (kn++) & 1)) return;
         for (int t = 0; t < cnt; ++t, ++it) {
           const int s = it % ST;
           const uint32_t dsb = sDSt + 32768u * (uint32_t)(it & 1);
           const uint32_t mQ = sdesc_lo(sQ + s * C::kTile, 16384);
           const uint32_t mDSi = sdesc_lo(dsb, 16384);  // dS MN-major (dQp)
           const uint32_t kDSi = sdesc_lo(dsb, 16);     // dS^T K-major (dK)
-          // Q is there whenever dS is, but a softmax that gave up a wait reports dS all the same
-          wait_load(Q_FULL(s), (it / ST) & 1);
+          // it frees Q as well, which is there whenever dS is, but for waits that ran out
+          if (!wait_load(Q_FULL(s), (it / ST) & 1)) return;
           wait(DS_READY(it), s_phase(it));
           // a run's first chain: the previous run's dK must have been read out
           if (t == 0 && !cprev && kn >= 2) wait(BAR(B_DKDV_EMPTY), (kn - 2) & 1);
@@ -758,6 +770,7 @@ __global__ void __launch_bounds__(512, 1)
           tc_commit(BAR(B_KV_EMPTY));  // dQp has read K
         }
       }
+      }();
       tc_commit(BAR(B_FINAL));
       drain(BAR(B_FINAL), 0);
     } else if (warp == 14 && lane == 0 && !kAtomic && C::kPublisher) {

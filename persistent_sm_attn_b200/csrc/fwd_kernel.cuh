@@ -89,10 +89,6 @@ __global__ void __launch_bounds__(256, 1)
   auto wait = [&](uint32_t bar, uint32_t phase) {
     return mbar_wait(bar, phase, lim, p.err, p.abort_flag);
   };
-  uint32_t* loading = tmem_slot + 1;  // 1 until the producer has stopped and its loads have landed
-  auto wait_load = [&](uint32_t bar, uint32_t phase) {
-    mbar_wait_load(bar, phase, lim, p.err, p.abort_flag, loading);
-  };
 
   const int S = p.S, N = p.N;
   // block t * BH + bh: Q tile N - 1 - t of head bh, so the heaviest (causal) tiles of
@@ -103,7 +99,6 @@ __global__ void __launch_bounds__(256, 1)
   const int row_q = bh * S + qt * 128;
 
   if (threadIdx.x == 0) {
-    *loading = 1u;
     mbar_init(BAR(F_Q_FULL), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(BAR(F_S_FULL0 + b), 1);
@@ -152,7 +147,6 @@ __global__ void __launch_bounds__(256, 1)
     for (int x = j > KST ? j - KST : 0; x < j; ++x)
       mbar_wait_drain(KV_FULL(x % KST), (uint32_t)((x / KST) & 1), drain_ns(lim), p.err,
                       p.abort_flag);
-    loads_done(smem_u32(loading));
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
     constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, 0, 0);  // S = Q K^T, both K-major
@@ -174,12 +168,14 @@ __global__ void __launch_bounds__(256, 1)
       tc_commit(PV_DONE(i));
       tc_commit(KV_EMPTY(s));  // K_i (read by S_i, issued earlier) and V_i are free
     };
-    wait_load(BAR(F_Q_FULL), 0);
+    // ends when a load does not come: it frees no stage before its load has landed
+    [&] {
+    if (!wait(BAR(F_Q_FULL), 0)) return;
     for (int j = 0; j < nkv; ++j) {
       const int s = j % KST;
       const uint32_t kK = sdesc_lo(sK + s * C::kTile, 16);
       const uint32_t tSj = tmem + C::TM_S + 128u * (uint32_t)(j & 1);
-      wait_load(KV_FULL(s), (uint32_t)((j / KST) & 1));
+      if (!wait(KV_FULL(s), (uint32_t)((j / KST) & 1))) return;
       // S_j's buffer held P_{j-2}, which P V_{j-2} must have read
       if (j >= 2) wait(PV_DONE(j - 2), ph2(j - 2));
       tc_fence_after();
@@ -192,6 +188,7 @@ __global__ void __launch_bounds__(256, 1)
       if (j >= 1) issue_pv(j - 1);
     }
     if (nkv > 0) issue_pv(nkv - 1);
+    }();
     tc_commit(BAR(F_O_FINAL));
     mbar_wait_drain(BAR(F_O_FINAL), 0, drain_ns(lim), p.err, p.abort_flag);
   } else if (warp >= 4) {

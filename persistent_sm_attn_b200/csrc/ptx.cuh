@@ -104,54 +104,19 @@ __device__ __forceinline__ uint64_t drain_ns(uint64_t limit_ns) {
   return limit_ns > 1000000000ull ? limit_ns : 1000000000ull;
 }
 
-// An issuer's wait for a load, in a CTA with *loading producers at work.  Once a wait has run
-// out its thread goes on without what it waited for, and arrivals no longer mean what they
-// stand for; a stage that is freed before its last load has landed would have its barrier
-// armed twice in one phase, which is undefined.  So the threads that free stages give up a
-// wait for a load only when the producers have stopped (their own waits end with the abort
-// flag, and they load nothing more) and all that was loaded has landed.
-static __device__ __noinline__ void mbar_wait_load_long(uint32_t bar, uint32_t parity,
-                                                        uint64_t limit_ns, unsigned* err,
-                                                        unsigned* abort_flag,
-                                                        volatile uint32_t* loading) {
-  const uint64_t t0 = globaltimer();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return;
-    if (aborted(abort_flag)) {
-      if (*loading == 0u) return;
-    } else if (globaltimer() - t0 > limit_ns) {
-      raise_timeout(err, abort_flag, ERR_WHERE_PIPE);
-    }
-    // ten drains of a producer and its last wait are over by then
-    if (globaltimer() - t0 > limit_ns + 16 * drain_ns(limit_ns)) *loading = 0u;
-  }
-}
-__device__ __forceinline__ void mbar_wait_load(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                               unsigned* err, unsigned* abort_flag,
-                                               volatile uint32_t* loading) {
-  if (!mbar_try_wait(bar, parity))
-    mbar_wait_load_long(bar, parity, limit_ns, err, abort_flag, loading);
-}
-// A producer says that it loads nothing more and that its loads have landed.
-__device__ __forceinline__ void loads_done(uint32_t loading) {
-  asm volatile("red.release.cta.shared::cta.add.u32 [%0], -1;" ::"r"(loading) : "memory");
-}
-
 // mbar_wait with everything but the first polls out of line.  A thread that issues products
 // runs its loop once a tile, through cold instruction caches: there the time goes by the code
 // it has to fetch.
 static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                                   unsigned* err) {
+                                                   unsigned* err, unsigned* abort_flag) {
   const uint64_t t0 = globaltimer();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (aborted(err + 1)) return false;
+    if (aborted(abort_flag)) return false;
     if (globaltimer() - t0 > limit_ns) {
-      raise_timeout(err, err + 1, ERR_WHERE_PIPE);
+      raise_timeout(err, abort_flag, ERR_WHERE_PIPE);
       return false;
     }
   }
@@ -161,7 +126,7 @@ __device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, ui
 #pragma unroll 1
   for (int i = 0; i < 16; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_long(bar, parity, limit_ns, err);
+  return mbar_wait_long(bar, parity, limit_ns, err, err + 1);
 }
 
 // ---------------------------------------------------------------- clusters
