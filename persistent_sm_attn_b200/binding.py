@@ -779,10 +779,13 @@ def _scale(scale):
 
 def _few_queries(B, H, Hkv, Sq):
     """Whether each query reads its keys for itself, without a plan: single tokens, and short
-    runs while a token of a K/V head (16 query heads at a time) leaves most SMs free.  With 8
-    K/V heads, 16 picks of 64 keys, D = 128, 16 queries of one sequence take 16 us (21 with a
-    plan), 32 take 24 (24); one token of 64 sequences takes 54 us (53, and two more launches),
-    two take 97 (74)."""
+    runs while a token of a K/V head (16 query heads at a time) leaves most SMs free.  Measured
+    on 16 picks of 64 keys, 32 query and 8 K/V heads, D = 128, whole calls: 16 queries of one
+    sequence take 19 us (34 with a plan), 32 take 25 (35); one token of 64 sequences takes 54 (53,
+    and two more launches), two take 97 (74).  The rule does not look at the picks, and long
+    ones are better off with a plan, which can be given: 16 queries of 4096 keys each take 44
+    (35), of 16384 keys 138 (58); single tokens of 4096 and 16384 keys take the same either
+    way."""
     return Sq == 1 or B * Hkv * Sq * -(-(H // max(Hkv, 1)) // 16) <= 256
 
 

@@ -359,11 +359,14 @@ BwdWork bwd_work(const PlanShape& s, int D) {
 template <int D>
 constexpr int kUnitElems = dash::kUnit * D;
 
-// Whether dS keeps a second bf16 part.  Delta comes from the rounded O, and where a query
-// attends to few keys O is large against the terms of dS: the errors of dQ and dK are then
-// 0.0026 of their norms (D = 64, 300 keys) in place of 0.0020 with the second part, the
-// rounding of the result itself being 0.0017.  At 1024 keys and more they are 0.0024, and the
-// second part costs 13 % of a pass of 16k keys, 1024 of them picked.
+// Whether dS keeps a second bf16 part.  It takes much the same off at any length: unit normals,
+// causal sequences of 64, 768 and 2048 keys, dQ off by 0.0020, 0.0018 and 0.0018 of its norm in
+// place of 0.0026, 0.0025 and 0.0025 (the rounding of the result itself is 0.0017); dK alike at
+// D = 64, while at D = 128 shared memory has no room for its part and dK stays at 0.0025.  And it
+// costs much the same: a backward of 8 heads of 8k takes 172 us for 156 at 256 picked keys and
+// 264 for 237 at 1024 (D = 64), 208 for 191 and 319 for 293 (D = 128).  So the limit is no
+// turning point but a choice: few keys, where Delta of the rounded O is the coarsest and the error
+// the largest, get it, and the others stay at what dV has from one bf16 part of P.
 bool sparse_low_part(const PlanShape& s) {
   return std::min((long long)s.Sk, (long long)s.topk * s.block) <= 768;
 }
