@@ -487,6 +487,9 @@ int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* d
  *     H any multiple of Hkv up to 128 query heads per K/V head (with B = 0 or H = 0 nothing is
  *     written; a selection needs a query head).  Sq >= 0 and Sk >= 1 are
  *     free (no multiple of 128), Sk at most 2^30.  Query head h reads K/V head h / (H / Hkv).
+ *     B H Sq stays below 2^31 and B Hkv at most 65535.  A plan's masks of one tile have to fit in
+ *     200 KiB: with g = 128 / (H / Hkv) tokens a tile (rounded down), ceil(Sk / 64) ceil(g / 32) at
+ *     most 51200.  Larger: UNSUPPORTED.
  *   - Inputs may be strided: `strides` holds (batch, head, row) strides in elements for
  *     each strided input in the order of the arguments, positive multiples of 8 (the last
  *     dimension is contiguous; the stride of an extent of 1 is not looked at); NULL means
@@ -503,7 +506,9 @@ int dash_dag_longest_path(int n_nodes, int n_edges, const int* src, const int* d
  *     status), and a workspace is free again when the call's work on `stream` is done.  All
  *     calls may be captured into a graph.  Results are bitwise reproducible.
  *   - A timeout found on the device is reported by dash_attn_sync_status(stream); calls on
- *     the stream between the timeout and that report may be invalid too.
+ *     the stream between the timeout and that report may be invalid too.  A graph's launches
+ *     record on the stream they were captured on: ask that one.  Beyond 256 streams of a
+ *     device, streams share what is recorded.
  */
 
 /*

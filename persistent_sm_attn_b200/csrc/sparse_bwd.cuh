@@ -103,20 +103,20 @@ struct SparseDqCfg {
 };
 
 // A persistent CTA per SM takes query tiles, those with the longest lists (the last, under a
-// causal mask) first, in turns that go to and fro.  Per listed unit j: S = Q K^T, dP = dO V^T (128 x 64, TMEM), dS in bf16
-// over S, dQ += dS K.  Even and odd units have an issuer of S and dP and a softmax warpgroup
-// each, so that one unit's exponentials run beside the other's dS; three buffers of S and dP
-// turn, and a unit's products wait only for the dQ product three units back.  (Two buffers,
+// causal mask) first, in turns that go to and fro.  Per listed unit j: S = Q K^T, dP = dO V^T
+// (128 x 64, TMEM), dS in bf16 over S, dQ += dS K.  Even and odd units have an issuer of S and dP
+// and a softmax warpgroup each, so that one unit's exponentials run beside the other's dS; three
+// buffers of S and dP turn, and a unit's products wait only for the dQ product three units back.  (Two buffers,
 // free again as they were read: 226 us at 16 heads of 8k, D = 128, 16 picks of 64, 351 us at 8
 // heads of 16k, D = 64, 8 picks of 128.  One stream of 128-key products, both warpgroups on
 // the same pair: 231 and 408, exponentials and the rest took turns.)  Row t G + g of a tile is
 // token t, head g, so a warp holds few tokens and skips the exponentials of units that none
 // of them picked.
 //
-// Measured: 198 us and 318 us in these two cases, 1300 and 1000 cycles a unit where the products
-// alone take 1160 and 730 (a 128 x 64 x 16 product 48, which is what reading its operands from
-// shared memory takes, a commit 35).  With turns that all go one way the busiest CTA has 11 %
-// more units than the mean and not 2 %: 209 and 328 us.
+// Measured: 182 us and 312 us in these two cases, 1300 and 1000 cycles a unit of the busiest CTA
+// where the products alone take 1160 and 730 (a 128 x 64 x 16 product 48, which is what reading
+// its operands from shared memory takes, a commit 35).  That CTA has 8 and 10 % more units than
+// the mean; with turns that all go one way 17 and 15 %, and both passes took 10 us more.
 //
 // kLow: dS enters its product as the sum of two bf16 values instead of one, whose rounding of
 // up to 2^-8 is otherwise the larger part of the result's error; see sparse_low_part.
@@ -735,8 +735,8 @@ struct SparseDkvCfg {
 // is computed.  D = 64: they take tiles in turn.  kLow (D = 64, where shared memory has room):
 // as in the dQ kernel.
 //
-// Measured: 16 heads of 8k, 4 K/V heads, D = 128, 16 picks of 64: 181 us, 3000 cycles a tile;
-// 8 heads of 16k, D = 64, 8 picks of 128: 147 us, 2400.  The products take 2000 and 1280.  At
+// Measured: 16 heads of 8k, 4 K/V heads, D = 128, 16 picks of 64: 177 us, 3100 cycles a tile;
+// 8 heads of 16k, D = 64, 8 picks of 128: 142 us, 2500.  The products take 2000 and 1280.  At
 // D = 128 two stages are all that fits, and a stage's way from load to last product bounds it.
 // Tiles of neighbouring tokens: 544 and 1159 us; dV and dK issued together: 201 and 170.
 template <int D, bool kLow>

@@ -19,7 +19,7 @@
 // that none of them picked.
 //
 // Measured: 16 heads of 8k, 4 K/V heads, D = 128, 16 picks of 64 (a tile lists 34 units where a
-// query picks 15): 141 us; 8 heads of 16k, D = 64, 8 picks of 128 (77 and 16): 233 us.  Bound by
+// query picks 15): 134 us; 8 heads of 16k, D = 64, 8 picks of 128 (77 and 16): 224 us.  Bound by
 // the softmax warps' way from S to P, some 1600 cycles a unit beside another CTA; a unit's
 // products take 710 and 450 cycles.  With one issuer, and a comparison for every key: 191 and
 // 335 us.  Lists cut over twice the CTAs, for 376 tiles on 296 places, did not pay for the join
